@@ -9,6 +9,7 @@ call raises :class:`Q4Error` -- there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -19,6 +20,8 @@ from . import build as _build
 
 LAYOUT_INT4G128 = 0
 LAYOUT_NVFP4 = 1
+CACHE_INT8 = 0
+CACHE_INT4 = 1
 FLAG_PDL = 0x1
 FLAG_FORCE_CUDA_CORE = 0x2
 FLAG_FORCE_TENSOR_CORE = 0x4
@@ -54,6 +57,7 @@ def load() -> ctypes.CDLL:
                               f"`python -m bit_weight_only_q4_gb300.build` (no fallback exists)")
         L = ctypes.CDLL(path)
         p, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        i64, f = ctypes.c_int64, ctypes.c_float
         st = ctypes.c_int
         sig = {
             "q4_abi_version": ([], ctypes.c_int),
@@ -73,6 +77,13 @@ def load() -> ctypes.CDLL:
             "q4_embedding_int8": ([p, p, p, p, i, i, i, p], st),
             "q4_linear_int8": ([p, p, p, p, i, i, i, p], st),
             "q4_quantize_nvfp4": ([p, p, p, p, i, i, p], st),
+            "q4_kv_block_bytes": ([i, i], sz),
+            "q4_kv_write": ([p, i64, p, i64, p, i, p, i, i, i, i, i, p], st),
+            "q4_kv_read": ([p, i, i, i, i, i, p, i, p, i, i, p, p, p], st),
+            "q4_kv_attention_workspace_bytes": ([i, i, i, i, i, i, i], sz),
+            "q4_kv_attention": ([p, i64, p, i, i, i, i, i, p, i, p, i, i, i, f, p, p, sz, p], st),
+            "q4_kv_attention_shared": ([p, i64, p, i, i, i, i, i, p, i, p, i, p, i, i, i, f, p, p,
+                                        sz, p], st),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -89,7 +100,9 @@ def symbols() -> list[str]:
             "q4_linear_int4g128", "q4_linear_nvfp4", "audio_head_logits_restricted",
             "q4_linear_int4g128_noalloc", "q4_device_error_flags", "q4_dequant_int4g128_f32",
             "q4_dequant_nvfp4_f32", "q4_quantize_int4g128", "q4_quantize_nvfp4",
-            "q4_embedding_int8", "q4_linear_int8"]
+            "q4_embedding_int8", "q4_linear_int8", "q4_kv_block_bytes", "q4_kv_write",
+            "q4_kv_read", "q4_kv_attention_workspace_bytes", "q4_kv_attention",
+            "q4_kv_attention_shared"]
 
 
 def _check(status: int) -> None:
@@ -132,7 +145,7 @@ def get_launch_flags() -> int:
 
 def device_error_flags(clear: bool = True) -> int:
     """Device error word (bit 0: a bounded in-kernel wait timed out; bit 2: an
-    embedding id out of range). Synchronises."""
+    embedding id, a cache slot or a page id out of range). Synchronises."""
     v = ctypes.c_uint(0)
     _check(load().q4_device_error_flags(ctypes.byref(v), 1 if clear else 0))
     return int(v.value)
@@ -322,3 +335,179 @@ def q4_linear_int8(x, qweight, scale, y=None, stream=None):
     _check(load().q4_linear_int8(_ptr(x), _ptr(qweight), _ptr(scale), _ptr(y), M, N, K,
                                  _stream(stream)))
     return y
+
+
+# ------------------------------------------------------------ paged K/V cache
+def kv_block_bytes(fmt: int, head_dim: int) -> int:
+    """Bytes that 16 tokens of one head take in a cache of the given format."""
+    return int(load().q4_kv_block_bytes(fmt, head_dim))
+
+
+def alloc_kv_cache(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim: int,
+                   device=None) -> torch.Tensor:
+    """An uninitialised K/V cache: uint8 [pages, kv_heads, page_size / 16, block bytes].
+    Tokens are written with q4_kv_write; what no write has reached is never used."""
+    n = kv_block_bytes(fmt, head_dim)
+    if n == 0 or page_size < 16 or page_size & (page_size - 1):
+        raise ValueError(f"no cache of format {fmt}, head_dim {head_dim}, page_size {page_size}")
+    return torch.empty((pages, kv_heads, page_size // 16, n), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def _kv_cache(cache, fmt, head_dim):
+    """(format, pages, page_size, kv_heads, head_dim) of a cache tensor."""
+    _cuda(cache, "cache", torch.uint8)
+    n = kv_block_bytes(fmt, head_dim)
+    if cache.dim() != 4 or n == 0 or cache.shape[3] != n:
+        raise ValueError(f"cache must be [pages, kv_heads, page_size / 16, {n}] for format {fmt} "
+                         f"and head_dim {head_dim}, got {tuple(cache.shape)}")
+    return fmt, cache.shape[0], 16 * cache.shape[2], cache.shape[1], head_dim
+
+
+def _rows(t, name, dims):
+    """A bf16 CUDA tensor [..., heads, D] whose tokens are evenly spaced and whose heads
+    lie side by side (a slice of a fused q|k|v projection does); its token stride."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    heads, D = t.shape[-2:]
+    row = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if dims == 4 else heads * D)
+    if dims == 4 and t.shape[0] == 1 and t.shape[1] == 1:
+        row = heads * D
+    even = dims == 3 or t.shape[0] == 1 or t.stride(0) == t.shape[1] * row
+    if not even or t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, got "
+                         f"strides {tuple(t.stride())}")
+    return row
+
+
+def _table(table, lengths, batch=None):
+    _cuda(table, "page_table", torch.int32)
+    _cuda(lengths, "lengths", torch.int32)
+    if table.dim() != 2 or lengths.dim() != 1 or lengths.shape[0] != table.shape[0]:
+        raise ValueError("page_table must be [batch, width] and lengths [batch]")
+    if batch is not None and table.shape[0] != batch:
+        raise ValueError(f"page_table has {table.shape[0]} sequences, q has {batch}")
+
+
+def q4_kv_write(k, v, cache, slots, fmt, stream=None):
+    """Quantise K and V rows (bf16 [tokens, kv_heads, D]) into the cache's slots
+    (int32 [tokens]; slot = page * page_size + token in the page, negative: left out)."""
+    ks, vs = _rows(k, "k", 3), _rows(v, "v", 3)
+    if k.shape != v.shape:
+        raise ValueError(f"k and v must have one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
+    _cuda(slots, "slots", torch.int32)
+    if slots.numel() != k.shape[0]:
+        raise ValueError("slots must hold one slot for each token")
+    geo = _kv_cache(cache, fmt, k.shape[2])
+    if geo[3] != k.shape[1]:
+        raise ValueError(f"the cache holds {geo[3]} heads, k has {k.shape[1]}")
+    if k.shape[0] == 0:
+        return cache
+    _check(load().q4_kv_write(_ptr(k), ks, _ptr(v), vs, _ptr(slots), k.shape[0], _ptr(cache), *geo,
+                              _stream(stream)))
+    return cache
+
+
+def q4_kv_read(cache, page_table, lengths, max_len, head_dim, fmt, k=None, v=None, stream=None):
+    """(k, v) bf16 [batch, max_len, kv_heads, head_dim] of the first lengths[b] cached tokens
+    of each sequence, zeros behind them."""
+    geo = _kv_cache(cache, fmt, head_dim)
+    _table(page_table, lengths)
+    shape = (page_table.shape[0], max_len, geo[3], head_dim)
+    with _on(stream):
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    for t, name in ((k, "k"), (v, "v")):
+        if tuple(_cuda(t, name, torch.bfloat16).shape) != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    if k.numel() == 0:
+        return k, v
+    _check(load().q4_kv_read(_ptr(cache), *geo, _ptr(page_table), page_table.shape[1], _ptr(lengths),
+                             shape[0], max_len, _ptr(k), _ptr(v), _stream(stream)))
+    return k, v
+
+
+def kv_attention_workspace_bytes(fmt, kv_heads, head_dim, batch, tokens, q_heads, prefix_len=0) -> int:
+    return int(load().q4_kv_attention_workspace_bytes(fmt, kv_heads, head_dim, batch, tokens,
+                                                      q_heads, prefix_len))
+
+
+def _on(stream):
+    """Allocations made inside belong to the stream that the call runs on, so that neither
+    their fill nor their reuse by the allocator overlaps the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _kv_workspace(geo, q, prefix_len, stream):
+    """As _default_workspace: one per device, stream and call shape, zero-filled once."""
+    fmt, _, _, heads, D = geo
+    B, T, Hq, _ = q.shape
+    key = (q.device.index, _stream(stream), "kv", fmt, heads, D, B, T, Hq, prefix_len)
+    ws = _ws_cache.get(key)
+    if ws is None:
+        n = kv_attention_workspace_bytes(fmt, heads, D, B, T, Hq, prefix_len)
+        if n == 0:
+            return None
+        if len(_ws_cache) >= 64:
+            _ws_cache.clear()
+        with _on(stream):
+            ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
+        _ws_cache[key] = ws
+    return ws
+
+
+def _kv_attention(q, cache, prefix, page_table, lengths, fmt, scale, out, workspace, stream):
+    row = _rows(q, "q", 4)
+    B, T, Hq, D = q.shape
+    geo = _kv_cache(cache, fmt, D)
+    _table(page_table, lengths, B)
+    if out is None:
+        with _on(stream):
+            out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    elif tuple(_cuda(out, "out", torch.bfloat16).shape) != (B, T, Hq, D):
+        raise ValueError(f"out must be {(B, T, Hq, D)}, got {tuple(out.shape)}")
+    if out.numel() == 0:
+        return out
+    prefix_len = prefix[1] if prefix else 0
+    if workspace is None:
+        workspace = _kv_workspace(geo, q, prefix_len, stream)
+    wp, wn = _ws_args(workspace)
+    s = D ** -0.5 if scale is None else float(scale)
+    tail = (_ptr(page_table), page_table.shape[1], _ptr(lengths), B, T, Hq, s, _ptr(out), wp, wn,
+            _stream(stream))
+    if prefix:
+        _check(load().q4_kv_attention_shared(_ptr(q), row, _ptr(cache), *geo, _ptr(prefix[0]),
+                                             prefix_len, *tail))
+    else:
+        _check(load().q4_kv_attention(_ptr(q), row, _ptr(cache), *geo, *tail))
+    return out
+
+
+def q4_kv_attention(q, cache, page_table, lengths, fmt, scale=None, out=None, workspace=None,
+                    stream=None):
+    """out [batch, tokens, q_heads, D] (bf16) = softmax(scale q K^T) V over the cached tokens of
+    each sequence; the query tokens q (bf16, same shape) are the sequence's last ones.
+    scale: D ** -0.5 if None; lengths int32 [batch], page_table int32 [batch, width]."""
+    return _kv_attention(q, cache, None, page_table, lengths, fmt, scale, out, workspace, stream)
+
+
+def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, scale=None,
+                           out=None, workspace=None, stream=None):
+    """As q4_kv_attention where every sequence begins with the prefix_len tokens of the pages
+    prefix_pages (int32): they are read and multiplied once for the whole batch.  page_table and
+    lengths describe each sequence's own tokens behind them."""
+    _cuda(prefix_pages, "prefix_pages", torch.int32)
+    page = 16 * cache.shape[2]
+    if prefix_len < 1 or prefix_pages.numel() * page < prefix_len:
+        raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page}, the prefix has "
+                         f"{prefix_len} tokens")
+    return _kv_attention(q, cache, (prefix_pages, prefix_len), page_table, lengths, fmt, scale, out,
+                         workspace, stream)

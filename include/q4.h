@@ -178,7 +178,7 @@ q4_status audio_head_logits_restricted(const void *h, const void *head, int R_to
  */
 #define Q4_DEVERR_TIMEOUT 0x1u
 /* Bit 2: q4_embedding_int8 met a token id outside 0 .. V-1 and wrote a row of
- * zeros for it. */
+ * zeros for it, or a key/value cache call met a slot or a page id outside the cache. */
 #define Q4_DEVERR_INDEX 0x4u
 q4_status q4_device_error_flags(unsigned *flags, int clear);
 
@@ -252,6 +252,107 @@ q4_status q4_quantize_int4g128(const void *w_bf16, uint8_t *qweight, void *scale
                                void *min_f16, int N, int K, void *stream);
 q4_status q4_quantize_nvfp4(const void *w_bf16, uint8_t *codes, uint8_t *scale_e4m3,
                             float *global_scale, int N, int K, void *stream);
+
+/*
+ * Paged key/value cache: K and V rows are quantised as they are written, and the
+ * attention reads them where they lie.  The cache is one device byte array
+ *     [pages][kv_heads][page_size / 16][block]
+ * A block holds 16 consecutive tokens of one head: 16 K code rows, 16 V code rows,
+ * 16 K scales, 16 V scales.
+ *   Q4_CACHE_INT8: a row is head_dim int8 codes -127..127 with one fp16 scale;
+ *     value = code * scale.
+ *   Q4_CACHE_INT4: a row is head_dim / 2 bytes, two codes 0..15 each (low nibble =
+ *     even column), with one fp16 scale and one fp16 min; value = code * scale + min
+ *     (the int4 min/max weight layout with a group of head_dim columns).
+ * The code rows lie in 128-byte lines of eight 16-byte pieces; piece c of the line
+ * holding row r is stored at place c ^ key(r), key(r) = r & 7 for rows of 128 bytes,
+ * r & 6 for 64 and (r >> 1) & 2 for 32.
+ *
+ * Common requirements: head_dim 64 or 128; page_size a power of two, 16 .. 1024;
+ * pages, kv_heads >= 1; cache 16-byte aligned.  A slot is page * page_size + token
+ * within the page.  Page tables are int32 device arrays: entry j of a sequence's row
+ * is the page of its tokens j * page_size and on.  Entries that hold no token are
+ * never read.  A token whose page id lies outside 0 .. pages - 1, or whose position
+ * lies past the table's width, is left out (read back as zeros, not attended to) and
+ * Q4_DEVERR_INDEX is set.  Neither the unused part of a page nor a page outside the
+ * tables influences any result.
+ */
+#define Q4_CACHE_INT8 0
+#define Q4_CACHE_INT4 1
+
+/* Bytes of a block of 16 tokens of one head (0 for an invalid format or head size);
+ * the cache takes pages * kv_heads * page_size / 16 blocks. */
+size_t q4_kv_block_bytes(int format, int head_dim);
+
+/*
+ * Quantise `tokens` rows of K and V into the cache.
+ *   k, v    bf16; token n, head h, column d at n * stride + h * head_dim + d
+ *           (strides in elements, multiples of 8; a fused q|k|v row works as it is)
+ *   slots   int32 [tokens]; a negative slot leaves its token out, a slot past the
+ *           cache does too and sets Q4_DEVERR_INDEX.  No slot may occur twice.
+ * Every step is one IEEE fp32 operation, rounded to nearest even:
+ *   int8: s = fp16(min(amax / 127, 65504)); code = clamp(rint(x / s), -127, 127)
+ *   int4: s = fp16(min((max - min) / 15, 65504)); m = fp16(clamp(min, +-65504));
+ *         code = clamp(rint((x - m) / s), 0, 15)
+ * (code 0 where s is 0).  A row that holds an infinity or a NaN gets a NaN scale (and
+ * min) and so reads back as NaN.  k, v 16-byte, slots 4-byte aligned.
+ */
+q4_status q4_kv_write(const void *k_bf16, int64_t k_stride, const void *v_bf16, int64_t v_stride,
+                      const int32_t *slots, int tokens, uint8_t *cache, int format, int pages,
+                      int page_size, int kv_heads, int head_dim, void *stream);
+
+/*
+ * Read the first lengths[b] cached tokens of each sequence back:
+ *   k, v    bf16 [batch, max_len, kv_heads, head_dim], written whole: the value rounded
+ *           once to bf16, zeros past the sequence's length.
+ * lengths int32 [batch] (at most max_len tokens are read), table int32
+ * [batch, table_width].  k, v 16-byte, table and lengths 4-byte aligned.
+ */
+q4_status q4_kv_read(const uint8_t *cache, int format, int pages, int page_size, int kv_heads,
+                     int head_dim, const int32_t *table, int table_width, const int32_t *lengths,
+                     int batch, int max_len, void *k_bf16, void *v_bf16, void *stream);
+
+/*
+ * Attention of `tokens` query tokens per sequence over the cache,
+ *     out = softmax(scale * q K^T) V,
+ * with the query tokens the last ones of their sequence: query token t of sequence b
+ * sees the cached positions below lengths[b] - tokens + t + 1.  A query token that sees
+ * nothing (a length below `tokens`) gives zeros.
+ *   q     bf16; sequence b, token t, head h, column d at (b * tokens + t) * q_stride +
+ *         h * head_dim + d (q_stride in elements, a multiple of 8)
+ *   out   bf16 [batch, tokens, q_heads, head_dim]
+ * q_heads is a multiple of kv_heads: query heads h * q_heads / kv_heads and on share
+ * the keys of head h.  Scores, softmax statistics and sums are fp32; q and the codes
+ * enter the products exactly, the probabilities (times their row's V scale) as fp16.
+ * lengths is read on the device: nothing on the host depends on it.  batch <= 8192.
+ *
+ * workspace: at least q4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,
+ * zero-filled once after allocation (every call leaves its counters at zero); calls
+ * that run concurrently must not share one.
+ */
+size_t q4_kv_attention_workspace_bytes(int format, int kv_heads, int head_dim, int batch, int tokens,
+                                       int q_heads, int prefix_len);
+q4_status q4_kv_attention(const void *q_bf16, int64_t q_stride, const uint8_t *cache, int format,
+                          int pages, int page_size, int kv_heads, int head_dim,
+                          const int32_t *table, int table_width, const int32_t *lengths, int batch,
+                          int tokens, int q_heads, float scale, void *out_bf16, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * The same where every sequence begins with one shared prefix of prefix_len >= 1
+ * tokens, whose pages prefix_pages names (int32, ceil(prefix_len / page_size) entries);
+ * table and lengths describe what each sequence has behind it.  The result is that of
+ * q4_kv_attention over prefix and own tokens one after the other (query token t of
+ * sequence b sees the positions below prefix_len + lengths[b] - tokens + t + 1), but the
+ * prefix is read and multiplied once for the whole batch.  A sequence may have no
+ * token of its own.
+ */
+q4_status q4_kv_attention_shared(const void *q_bf16, int64_t q_stride, const uint8_t *cache,
+                                 int format, int pages, int page_size, int kv_heads, int head_dim,
+                                 const int32_t *prefix_pages, int prefix_len, const int32_t *table,
+                                 int table_width, const int32_t *lengths, int batch, int tokens,
+                                 int q_heads, float scale, void *out_bf16, void *workspace,
+                                 size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
