@@ -104,19 +104,4 @@ struct KvCache {
     }
 };
 
-// Parameters of the attention kernels.
-struct KvAttnParams {
-    KvCache cache;
-    const uint16_t *q;           // bf16, token b * tokens + t, head hq at token * q_stride + hq * D
-    int64_t q_stride;
-    uint16_t *out;               // bf16 [batch][tokens][q_heads][D]
-    const int32_t *table;        // [batch][table_width] pages of each sequence
-    const int32_t *lengths;      // [batch] cached tokens (behind the prefix), the new ones among them
-    const int32_t *prefix_pages; // pages of the shared prefix
-    int64_t prefix_len;
-    int table_width, tokens, q_heads;
-    float scale;
-    unsigned *err;
-};
-
 }  // namespace q4

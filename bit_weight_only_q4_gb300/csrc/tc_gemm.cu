@@ -39,6 +39,7 @@
 
 #include "q4_device.cuh"
 #include "q4_internal.h"
+#include "tc_device.cuh"
 
 namespace q4 {
 
@@ -82,22 +83,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 }
 
 
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Shared-memory matrix descriptor: K-major operand in the canonical 128-byte
-// swizzle layout (rows of 128 bytes, 8-row atoms of 1024 bytes).
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr)
-{
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);          // start address
-    d |= (uint64_t)1 << 16;                            // leading byte offset (unused)
-    d |= (uint64_t)(1024 >> 4) << 32;                  // stride byte offset: 8 rows
-    d |= (uint64_t)1 << 46;                            // descriptor version
-    d |= (uint64_t)2 << 61;                            // 128-byte swizzle
-    return d;
-}
-
 // Instruction descriptor of tcgen05.mma kind::f16: fp16 A and B (K-major),
 // fp32 accumulator, M = 128, N = n.
 __device__ __forceinline__ uint32_t idesc_f16(int n, bool bf16 = false)
@@ -107,63 +92,6 @@ __device__ __forceinline__ uint32_t idesc_f16(int n, bool bf16 = false)
          | (ab << 7) | (ab << 10)       // A, B format
          | ((uint32_t)(n >> 3) << 17)   // N / 8
          | ((uint32_t)(TC_ROWS >> 4) << 24);   // M / 16
-}
-
-// tcgen05.mma kind::f16 (M = 128) with both descriptors passed as 32-bit halves,
-// so that the issuing loop only steps the start-address fields (low halves: +2 per
-// 32 bytes).  One thread issues every MMA of a CTA; rebuilding two 64-bit
-// descriptors per MMA costs that thread more than the MMA costs the tensor core.
-__device__ __forceinline__ void mma_f16_2(uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
-                                          uint32_t b_hi, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .b64 ad, bd;\n\t.reg .pred p;\n\t"
-                 "setp.ne.u32 p, %6, 0;\n\t"
-                 "mov.b64 ad, {%1, %2};\n\t"
-                 "mov.b64 bd, {%3, %4};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t}"
-                 ::"r"(tmem_d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-// The same MMA with the A operand in tensor memory (row i of A in lane i, its K
-// values packed two per 32-bit column, K = 16 in eight columns).
-__device__ __forceinline__ void mma_f16_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
-                                               uint32_t b_hi, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .b64 bd;\n\t.reg .pred p;\n\t"
-                 "setp.ne.u32 p, %5, 0;\n\t"
-                 "mov.b64 bd, {%2, %3};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}"
-                 ::"r"(tmem_d), "r"(tmem_a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-// A warp writes 16 consecutive 32-bit columns of its 32 TMEM lanes.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-                   "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
-                   "r"(v[13]), "r"(v[14]), "r"(v[15])
-                 : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-                   "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
-                   "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)

@@ -208,6 +208,8 @@ SHAPES = [  # batch lengths, tokens, q_heads, kv_heads, page
     ([513, 40], 33, 8, 2, 64),                              # a chunk
     ([260, 200, 130], 130, 3, 1, 32),                       # more rows than a tile
     ([290], 200, 4, 4, 16),
+    ([20000, 3], 1, 34, 2, 64),                             # 17 rows, many tiles
+    ([6, 70], 9, 30, 2, 32),                                # 135 rows: a tile of 128 and one of 7
 ]
 
 
@@ -356,6 +358,16 @@ def test_repeated_captured_and_streamed_calls_agree(q4, shared):
                 np.testing.assert_array_equal(got, first)
     finally:
         q4.set_launch_flags(0)
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
+@pytest.mark.parametrize("scale", [0.0, -0.07, 1e-9])
+def test_scales_of_any_sign(q4, scale, Hq):
+    rng = np.random.default_rng([13, Hq])
+    cache, table, _ = filled(rng, 0, 64, 2, 16, [200, 131])
+    q = rows(rng, 2, Hq, 64).reshape(2, 1, Hq, 64)
+    out = call(q4, q, cache, table, [200, 131], 0, scale)
+    check(out, q, cache, table, [200, 131], 0, float(np.float32(scale)))
 
 
 def test_query_rows_of_a_fused_projection(q4):
