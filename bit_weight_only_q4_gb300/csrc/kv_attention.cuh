@@ -269,27 +269,54 @@ __device__ __forceinline__ float4 kv_scales(uint32_t blk, int r)
     return s;
 }
 
-// A token's row of codes (16 RB bytes of the block, swizzled) as fp16 into a tile of 128
-// tokens: 64-column halves of 128 rows x 128 bytes, 128-byte swizzle.  As an MMA operand
-// that is K-major with tokens as rows and M- or N-major with tokens as K.
+// Where a thread finds its token's row of codes in a staged tile, computed once: the row's
+// 16-byte pieces lie at `base` plus the offsets of `piece` (see KvLayout).
 template <int FMT, int D>
-__device__ __forceinline__ void kv_row_to_tile(uint32_t codes, uint32_t tile, int tok)
+struct KvRowAt {
+    using L = KvLayout<FMT, D>;
+    static constexpr int PIECES = L::RB / 16;
+    uint32_t base, piece[PIECES];
+    __device__ __forceinline__ explicit KvRowAt(int tok)
+    {
+        const int r = tok & (KV_BLOCK - 1);
+        const uint32_t line = (uint32_t)(r * L::RB) & ~127u;
+        base = (uint32_t)(tok / KV_BLOCK) * L::BLOCK + line;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j)
+            piece[j] = (uint32_t)L::place(r, 16 * j) - line;
+    }
+};
+
+// A token's row of fp16 values in a tile of 128 tokens: 64-column halves of 128 rows x 128
+// bytes, 128-byte swizzle.  As an MMA operand that is K-major with tokens as rows and M- or
+// N-major with tokens as K.
+struct KvRowTo {
+    uint32_t base, chunk[8];
+    __device__ __forceinline__ explicit KvRowTo(int tok)
+    {
+        base = (uint32_t)tok * 128u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            chunk[j] = (uint32_t)((j ^ tok) & 7) << 4;
+    }
+};
+
+template <int FMT, int D>
+__device__ __forceinline__ void kv_row_to_tile(uint32_t codes, const KvRowAt<FMT, D> &from, uint32_t tile, const KvRowTo &to)
 {
     using L = KvLayout<FMT, D>;
-    const int r = tok & (KV_BLOCK - 1);
-    const uint32_t row = tile + (uint32_t)tok * 128u;
-    constexpr int PIECES = L::RB / 16;
     constexpr int OUT = L::I8 ? 2 : 4;             // 8-column chunks of a piece
-#pragma unroll 2
-    for (int j = 0; j < PIECES; ++j) {
-        const uint4 c = lds128(codes + L::place(r, 16 * j));
+    const uint32_t src = codes + from.base, dst = tile + to.base;
+#pragma unroll
+    for (int j = 0; j < KvRowAt<FMT, D>::PIECES; ++j) {
+        const uint4 c = lds128(src + from.piece[j]);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int x = 0; x < OUT; ++x) {
             uint32_t v[4];
             kv_decode8<L::I8>(L::I8 ? w[2 * x] : w[x], L::I8 ? w[2 * x + 1] : 0u, v);
-            const uint32_t ch = (uint32_t)(OUT * j + x);
-            sts128(row + (ch >> 3) * (KT_TOKENS * 128u) + (((ch ^ (uint32_t)tok) & 7u) << 4), v[0], v[1], v[2], v[3]);
+            const int ch = OUT * j + x;
+            sts128(dst + to.chunk[ch & 7] + (uint32_t)(ch >> 3) * (KT_TOKENS * 128u), v[0], v[1], v[2], v[3]);
         }
     }
 }
@@ -584,30 +611,50 @@ __device__ __forceinline__ void kv_join(const KvTileParams &p, const KvShare &sh
     if (!*s_last)
         return;
     __threadfence();
+    // Four items (four columns of a row) at a time, two pieces of each: the loads are what
+    // this takes, and they have to be in flight together.  Piece j lies in slot
+    // 2 (first + j), the first one in the slot behind.
+    constexpr int IT = 4;
+    const int total = nrows * (D / 4);
 #pragma unroll 1
-    for (int item = t; item < nrows * (D / 4); item += NT) {
-        const int n = item / (D / 4), c4 = item % (D / 4);
-        KvRowSum r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        // piece j lies in slot 2 (first + j), the first one in the slot behind
-        const float *so = p.piece_o + (2 * first * TILE + n) * D + c4 * 4;
-        const float *sml = p.piece_ml + (2 * first * TILE + n) * 2;
-#pragma unroll 1
-        for (int j0 = 0; j0 < np; j0 += 4) {
-            float2 ml[4];
-            float4 x[4];
+    for (int item = t; item < total; item += NT * IT) {
+        KvRowSum r[IT];
+        const float *so[IT], *sml[IT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {          // past the end: the last piece again, unused
+        for (int y = 0; y < IT; ++y) {
+            const int x = item + y * NT < total ? item + y * NT : item;
+            const int64_t at = 2 * first * TILE + x / (D / 4);
+            so[y] = p.piece_o + at * D + x % (D / 4) * 4;
+            sml[y] = p.piece_ml + at * 2;
+            r[y] = KvRowSum{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        }
+#pragma unroll 1
+        for (int j0 = 0; j0 < np; j0 += 2) {
+            float2 ml[2 * IT];
+            float4 x[2 * IT];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {          // past the end: the last piece again, unused
                 const int jj = j0 + j < np ? j0 + j : np - 1;
-                const int64_t at = 2 * jj + (jj == 0 ? 1 : 0);
-                ml[j] = __ldcg(reinterpret_cast<const float2 *>(sml + at * TILE * 2));
-                x[j] = __ldcg(reinterpret_cast<const float4 *>(so + at * TILE * D));
+                const int64_t at = (int64_t)(2 * jj + (jj == 0 ? 1 : 0)) * TILE;
+#pragma unroll
+                for (int y = 0; y < IT; ++y) {
+                    ml[j * IT + y] = __ldcg(reinterpret_cast<const float2 *>(sml[y] + at * 2));
+                    x[j * IT + y] = __ldcg(reinterpret_cast<const float4 *>(so[y] + at * D));
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
                 if (j0 + j < np)
-                    r.add(ml[j], x[j]);
+#pragma unroll
+                    for (int y = 0; y < IT; ++y)
+                        r[y].add(ml[j * IT + y], x[j * IT + y]);
         }
-        kv_store4<D>(p, grow0 + n, un.h, c4, r);
+#pragma unroll
+        for (int y = 0; y < IT; ++y) {
+            const int x = item + y * NT;
+            if (x < total)
+                kv_store4<D>(p, grow0 + x / (D / 4), un.h, x % (D / 4), r[y]);
+        }
     }
 }
 

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         const int tok = (warp & 3) * 32 + lane;            // TMEM lane
         const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
         const int r = tok & (KV_BLOCK - 1);
-        const uint32_t at = (uint32_t)(tok / KV_BLOCK) * L::BLOCK;
+        const KvRowAt<FMT, D> from(tok);
         int k = 0, k1 = 0, ntok = 0, u = 0, s = 0;
         uint32_t round = 0u;                               // parity of the ring's round
 #pragma unroll 1
@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             if (i >= 2)
                 kv_wait(s_full + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
             tc_fence_after();
-            const uint32_t blk = sm + (uint32_t)s * RAW + at;
+            const uint32_t blk = sm + (uint32_t)s * RAW + (uint32_t)(tok / KV_BLOCK) * L::BLOCK;
+            const uint32_t src = sm + (uint32_t)s * RAW + from.base;
             // blocks of the tile that are there and hold tokens; bit 8: all of them do, wholly
             uint32_t mask = s_valid[s];
             if (mask == 0xffu && (k + 1) * KT_TOKENS <= ntok)
@@ -237,17 +238,17 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             if (warp == KF_K && lane == 0)
                 s_vmask[i & 3] = mask;
             const uint32_t dst = tmem + t_lane + (uint32_t)(i & 1) * (D / 2);
-#pragma unroll 2
+#pragma unroll
             for (int j = 0; j < D / 32; ++j) {             // 32 columns: 16 packed
                 uint32_t v[4][4];
                 if constexpr (L::I8) {
-                    const uint4 a = lds128(blk + L::place(r, 32 * j)), b = lds128(blk + L::place(r, 32 * j + 16));
+                    const uint4 a = lds128(src + from.piece[2 * j]), b = lds128(src + from.piece[2 * j + 1]);
                     kv_decode8<true>(a.x, a.y, v[0]);
                     kv_decode8<true>(a.z, a.w, v[1]);
                     kv_decode8<true>(b.x, b.y, v[2]);
                     kv_decode8<true>(b.z, b.w, v[3]);
                 } else {
-                    const uint4 a = lds128(blk + L::place(r, 16 * j));
+                    const uint4 a = lds128(src + from.piece[j]);
                     kv_decode8<false>(a.x, 0u, v[0]);
                     kv_decode8<false>(a.y, 0u, v[1]);
                     kv_decode8<false>(a.z, 0u, v[2]);
@@ -268,7 +269,8 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     } else if (warp < KF_S) {
         // ------------------------------------------- V: fp16 to shared memory
         const int tok = (warp - KF_V) * 32 + lane;
-        const uint32_t at = (uint32_t)(tok / KV_BLOCK) * L::BLOCK + L::V_CODES;
+        const KvRowAt<FMT, D> from(tok);
+        const KvRowTo to(tok);
         int s = 0;
         uint32_t round = 0u;
 #pragma unroll 1
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             kv_wait(raw_full + 8u * s, round, dead);
             if (i >= 2)
                 kv_wait(pv_done + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
-            kv_row_to_tile<FMT, D>(sm + (uint32_t)s * RAW + at, sm + off.v + (uint32_t)(i & 1) * V_BYTES, tok);
+            kv_row_to_tile<FMT, D>(sm + (uint32_t)s * RAW + L::V_CODES, from, sm + off.v + (uint32_t)(i & 1) * V_BYTES, to);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {

@@ -11,7 +11,7 @@
 // row, and while one half's scores are turned into probabilities the tensor cores work
 // on the other half or the next tile.  The halves are added up at the end of a unit.
 //
-// One CTA per SM, 18 warps: one copies blocks, one issues the MMAs, four decode K, four
+// One CTA per SM, 20 warps: one copies blocks, two issue the MMAs, four decode K, four
 // V, eight do the softmax and the results.  Measured alone, the MMAs of a tile take 1,050
 // cycles (D = 128); the softmax issues about 3,000 instructions, the decoding 1,800.
 #include "kv_attention.cuh"
@@ -20,16 +20,21 @@ namespace q4 {
 
 constexpr int KM_ROWS = 128;
 constexpr int KM_HALF = 64;                        // tokens of a half tile
-constexpr int KM_K = 2, KM_V = 6, KM_S = 10, KM_WARPS = 18;
+// warps, in groups of four: softmax of the two halves, K, V; copies, S, O (and one idle)
+constexpr int KM_K = 8, KM_V = 12, KM_COPY = 16, KM_S = 17, KM_O = 18, KM_WARPS = 20;
+// Registers of a softmax thread and of the others: the launch's 20 x 32 x 96 shared out
+// (8 x 128 + 12 x 72 <= 20 x 96).  A softmax thread holds 64 scores and 32 packed
+// probabilities; at 96 registers its loop ran with too few instructions in flight.
+constexpr int KM_REGS_SOFTMAX = 128, KM_REGS_OTHERS = 72;
 
 // Token scales of a tile (see kv_scales), one array each: four tokens are one broadcast load.
 struct KmScales {
     float ks[KT_TOKENS], km[KT_TOKENS], vs[KT_TOKENS], vm[KT_TOKENS];
 };
 
-// Shared memory: [raw ring][K: 2][V: 2][token scales: 4][lengths]
+// Shared memory: [raw ring][K: 2][V: 2][token scales: 4][results: 2 KB a softmax warp][lengths]
 struct KmSmem {
-    uint32_t k, v, scales, len, total;
+    uint32_t k, v, scales, stage, len, total;
 };
 
 template <int FMT, int D>
@@ -41,6 +46,7 @@ __host__ __device__ inline KmSmem km_smem(int stages, int seqs)
     s.k = at, at += 2u * KT_TOKENS * D * 2;
     s.v = at, at += 2u * KT_TOKENS * D * 2;
     s.scales = at, at += 4u * (uint32_t)sizeof(KmScales);
+    s.stage = at, at += 8u * 2048;
     s.len = at, at += ((uint32_t)seqs * 4u + 15u) & ~15u;
     s.total = at;
     return s;
@@ -93,9 +99,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 17 + KT_UNITS];
     __shared__ KvUnit s_unit[KT_UNITS];
     __shared__ float s_wmax[4][4];                         // largest V scale of 32 tokens
-    __shared__ uint32_t s_top[2][KM_ROWS];
-    __shared__ float s_qs[2][KM_ROWS];
-    __shared__ float4 s_sum[2][KM_ROWS];                   // m, l, offset
+    __shared__ float2 s_ml[KM_ROWS];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
     __shared__ int s_last, s_dead;
     const int NS = p.stages;
@@ -104,6 +108,10 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     const uint32_t sm = smem_u32(smem);
     KmScales *s_scales = reinterpret_cast<KmScales *>(smem + off.scales);
     int *s_len = reinterpret_cast<int *>(smem + off.len);
+    // exchanged between a row's two threads, where the results go later
+    uint32_t (*s_top)[KM_ROWS] = reinterpret_cast<uint32_t (*)[KM_ROWS]>(smem + off.stage);
+    float (*s_qs)[KM_ROWS] = reinterpret_cast<float (*)[KM_ROWS]>(smem + off.stage + 1024);
+    float4 (*s_sum)[KM_ROWS] = reinterpret_cast<float4 (*)[KM_ROWS]>(smem + off.stage);   // m, l, offset
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -132,7 +140,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
         mbar_init_fence();
         s_dead = 0;
     }
-    if (warp == 1) {
+    if (warp == KM_S) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&s_tmem)), "n"(TM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -144,138 +152,13 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     auto gone = [&]() { return *dead.flag != 0; };
     auto unit_wait = [&](int u) { kv_wait(unit_full + 8u * (u & (KT_UNITS - 1)), (u / KT_UNITS) & 1, dead); };
 
-    if (warp == 0) {
-        kv_copy_warp<FMT, D, KM_ROWS>(p, sh, s_len, s_unit, unit_full, sm, s_valid, raw_full, raw_empty, dead);
-    } else if (warp == 1) {
-        // --------------------------------------------------------------- MMAs
-        // S of tile i is asked for before O of tile i - 1, except where i begins a unit: its
-        // queries replace those of the unit before once that one's results have been read.
-        constexpr uint32_t idesc1 = (1u << 4) | ((uint32_t)(KM_HALF >> 3) << 17) | (8u << 24);       // f16, f32 sums, M = 128
-        constexpr uint32_t idesc2 = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);   // B is N-major
-        int u = -1, left = 0;
-        uint32_t more = 0u;                                // O(i - 1) adds to what is there
-        auto mma2 = [&](int i) {
-            kv_wait(v_full + 8u * (i & 1), (i >> 1) & 1, dead);
-            const uint64_t bd = (smem_desc_sw128(sm + off.v + (uint32_t)(i & 1) * TILE_BYTES) & ~((uint64_t)0x3fff << 16)) |
-                                ((uint64_t)(D == 128 ? KT_TOKENS * 128 >> 4 : 0) << 16);
-            const uint32_t blo = (uint32_t)bd, bhi = (uint32_t)(bd >> 32);
-#pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                kv_wait(p_full + 8u * g, i & 1, dead);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < KM_HALF / 16; ++kk)          // 16 tokens: two groups of 8
-                        mma_f16_tmem_a(tmem + TM_O + (uint32_t)g * D, tmem + TM_P + 32u * g + 8u * kk,
-                                       blo + (uint32_t)g * (8192 >> 4) + (uint32_t)kk * (2048 >> 4), bhi, idesc2,
-                                       kk > 0 ? 1u : more);
-                    mma_commit(pv_done + 8u * g);
-                    if (g == 1)
-                        mma_commit(v_done + 8u * (i & 1));
-                }
-                __syncwarp();
-            }
-            more = 1u;
-        };
-#pragma unroll 1
-        for (int i = 0; i <= sh.tiles && !gone(); ++i) {
-            const bool first = left == 0;
-            if (i > 0 && first)
-                mma2(i - 1);
-            if (i == sh.tiles)
-                break;
-            if (first) {
-                ++u;
-                unit_wait(u);
-                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-                left = un.k1 - un.k0;
-                kv_wait(q_full, u & 1, dead);
-            }
-            --left;
-            kv_wait(k_full + 8u * (i & 1), (i >> 1) & 1, dead);
-            const uint64_t bd = smem_desc_sw128(sm + off.k + (uint32_t)(i & 1) * TILE_BYTES);
-            const uint32_t blo = (uint32_t)bd, bhi = (uint32_t)(bd >> 32);
-#pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                if (i > 0)
-                    kv_wait(s_free + 8u * g, (i - 1) & 1, dead);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)    // 64-column halves of K 16 KB apart
-                        mma_f16_tmem_a(tmem + TM_S + 64u * g, tmem + 8u * kk,
-                                       blo + (uint32_t)g * (8192 >> 4) + (uint32_t)(kk >> 2) * (KT_TOKENS * 128 >> 4) +
-                                           2u * (kk & 3),
-                                       bhi, idesc1, kk > 0 ? 1u : 0u);
-                    mma_commit(s_full + 8u * g);
-                    if (g == 1)
-                        mma_commit(k_done + 8u * (i & 1));
-                }
-                __syncwarp();
-            }
-            if (first)
-                more = 0u;
-            else
-                mma2(i - 1);
-        }
-    } else if (warp < KM_S) {
-        // ------------------------------- K and V: fp16 tiles in shared memory
-        const bool is_v = warp >= KM_V;
-        const int tok = (warp & 3) * 32 + lane;
-        const int r = tok & (KV_BLOCK - 1);
-        const uint32_t at = (uint32_t)(tok / KV_BLOCK) * L::BLOCK;
-        const uint32_t full = is_v ? v_full : k_full, done = is_v ? v_done : k_done;
-        const uint32_t dst = sm + (is_v ? off.v : off.k);
-        int k = 0, k1 = 0, ntok = 0, u = 0, s = 0;
-        uint32_t round = 0u;                               // parity of the ring's round
-#pragma unroll 1
-        for (int i = 0; i < sh.tiles && !gone(); ++i, ++k) {
-            if (!is_v && k == k1) {
-                unit_wait(u);
-                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-                k = un.k0, k1 = un.k1, ntok = un.ntok;
-                ++u;
-            }
-            kv_wait(raw_full + 8u * s, round, dead);
-            if (i >= 2)
-                kv_wait(done + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
-            const uint32_t blk = sm + (uint32_t)s * RAW + at;
-            if (!is_v) {
-                // blocks of the tile that are there and hold tokens; bit 8: all of them do, wholly
-                uint32_t mask = s_valid[s];
-                if (mask == 0xffu && (k + 1) * KT_TOKENS <= ntok)
-                    mask |= 0x100u;
-                const bool here = ((mask >> (tok / KV_BLOCK)) & 1u) && k * KT_TOKENS + tok < ntok;
-                const float4 sc = here ? kv_scales<FMT, D>(blk, r) : make_float4(0.f, 0.f, 0.f, 0.f);
-                KmScales &out = s_scales[i & 3];
-                out.ks[tok] = sc.x;
-                out.vs[tok] = sc.z;
-                if constexpr (!L::I8) {
-                    out.km[tok] = sc.y;
-                    out.vm[tok] = sc.w;
-                }
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.z));
-                if (lane == 0)
-                    s_wmax[i & 3][warp & 3] = __uint_as_float(top);
-                if (warp == KM_K && lane == 0)
-                    s_vmask[i & 3] = mask;
-            }
-            kv_row_to_tile<FMT, D>(blk + (is_v ? L::V_CODES : 0), dst + (uint32_t)(i & 1) * TILE_BYTES, tok);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(full + 8u * (i & 1));
-                mbar_arrive(raw_empty + 8u * s);
-            }
-            if (++s == NS)
-                s = 0, round ^= 1u;
-        }
-    } else {
+    if (warp < KM_K) {
         // ----------------------------------------- softmax, sums and results
-        const int g = (warp - KM_S) >> 2;                  // half of the tile
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(KM_REGS_SOFTMAX));
+        const int g = warp >> 2;                           // half of the tile
         const int quad = warp & 3;
         const int row = quad * 32 + lane;                  // TMEM lane
-        const int t = (warp - KM_S) * 32 + lane;
+        const int t = tid;
         const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
         int i = 0;
 #pragma unroll 1
@@ -353,7 +236,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
             const int lim = mine ? kv_row_limit(p, grow0 + row, s_len[un.b]) : 0x7fffffff;
             const int least = __reduce_min_sync(0xffffffffu, lim);
             float m = -INFINITY, level = -36.f;            // reference; E - 6
-            f32x2 l2 = 0ull, off2 = 0ull;
+            f32x2 l2 = 0ull, l2b = 0ull, off2 = 0ull, off2b = 0ull;        // (two chains each)
             const f32x2 qs2 = pack2(qs, qs), f2 = pack2(f, f);
             bool first = true;
 #pragma unroll 1
@@ -373,107 +256,168 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                 uint32_t v[KM_HALF];
 #pragma unroll
                 for (int j = 0; j < KM_HALF; j += 16)
-                    tmem_ld16(tmem + t_lane + TM_S + 64u * g + j, reinterpret_cast<uint32_t(&)[16]>(v[j]));
+                    tmem_ld16_async(tmem + t_lane + TM_S + 64u * g + j, reinterpret_cast<uint32_t(&)[16]>(v[j]));
+                tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(s_free + 8u * g);
                 const uint32_t sc = smem_u32(&s_scales[i & 3]) + (uint32_t)g * (KM_HALF * 4);
-                // scores over f, and their maximum
-                float top = -INFINITY;
                 const int pos0 = (k0 + i) * KT_TOKENS + g * KM_HALF;
                 const uint32_t mask = s_vmask[i & 3];
                 const bool masked = !(mask & 0x100u) || pos0 + KM_HALF > least;
-#pragma unroll
-                for (int j = 0; j < KM_HALF; j += 4) {
-                    f32x2 ka, kb;
-                    lds_f32x4(sc + 4u * j, ka, kb);
-                    f32x2 a = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                    f32x2 b = pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-                    if constexpr (L::I8) {
-                        a = mul2(a, ka);
-                        b = mul2(b, kb);
-                    } else {
-                        f32x2 ma, mb;
-                        lds_f32x4(sc + 512u + 4u * j, ma, mb);
-                        a = fma2(a, ka, mul2(ma, qs2));
-                        b = fma2(b, kb, mul2(mb, qs2));
-                    }
-                    float x[4];
-                    unpack2(a, x[0], x[1]);
-                    unpack2(b, x[2], x[3]);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        top = fmaxf(top, x[y]);
-                        v[j + y] = __float_as_uint(x[y]);
-                    }
-                }
-                if (masked) {
-                    const uint32_t blocks = mask >> (4 * g);
-                    const int lim1 = lim < ntok ? lim : ntok;
-                    top = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < KM_HALF; ++j) {
-                        if (pos0 + j >= lim1 || !((blocks >> (j / KV_BLOCK)) & 1u))
-                            v[j] = 0xff800000u;
-                        top = fmaxf(top, __uint_as_float(v[j]));
-                    }
-                }
-                level = fmaxf(level, kv_scale_level(fmaxf(s_wmax[i & 3][2 * g], s_wmax[i & 3][2 * g + 1])));
-                const float want = fmaf(top, f, level);
-                const bool move = want > m + 8.f || (first && top > -INFINITY);
-                if (__any_sync(0xffffffffu, move)) {
-                    const float old = m;
-                    m = fmaxf(m, want);
-                    const float c = old == -INFINITY ? 0.f : ex2(old - m);
-                    const f32x2 c2 = pack2(c, c);
-                    l2 = mul2(l2, c2);
-                    off2 = mul2(off2, c2);
-                    if (!first) {
-                        kv_wait(pv_done + 8u * g, (i - 1) & 1, dead);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int j = 0; j < D; j += 16) {
-                            uint32_t o[16];
-                            const uint32_t a = tmem + t_lane + TM_O + (uint32_t)g * D + j;
-                            tmem_ld16(a, o);
-#pragma unroll
-                            for (int x = 0; x < 16; ++x)
-                                o[x] = __float_as_uint(__uint_as_float(o[x]) * c);
-                            tmem_st16(a, o);
-                        }
-                        tmem_wait_st();
-                    }
-                }
-                const float neg = m == -INFINITY ? 0.f : -m;
-                const f32x2 n2 = pack2(neg, neg);
                 uint32_t ph[KM_HALF / 2];
+                // With every token seen and every reference set, go by the references as they are;
+                // if some product then reaches 2^15, go again the careful way.
+                bool careful = masked || __any_sync(0xffffffffu, m == -INFINITY);
+                if (!careful) {
+                    const f32x2 n2 = pack2(-m, -m);
+                    f32x2 la = 0ull, lb = 0ull, oa = 0ull, ob = 0ull;
+                    uint32_t high[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int j = 0; j < KM_HALF; j += 4) {
-                    f32x2 a = fma2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2, n2);
-                    f32x2 b = fma2(pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f2, n2);
-                    float x[4];
-                    unpack2(a, x[0], x[1]);
-                    unpack2(b, x[2], x[3]);
-                    a = pack2(ex2(x[0]), ex2(x[1]));
-                    b = pack2(ex2(x[2]), ex2(x[3]));
-                    l2 = add2(l2, a);
-                    l2 = add2(l2, b);
-                    f32x2 va, vb;
-                    lds_f32x4(sc + 1024u + 4u * j, va, vb);
-                    if constexpr (!L::I8) {
-                        f32x2 oa, ob;
-                        lds_f32x4(sc + 1536u + 4u * j, oa, ob);
-                        off2 = fma2(a, oa, off2);
-                        off2 = fma2(b, ob, off2);
+                    for (int j = 0; j < KM_HALF; j += 4) {
+                        f32x2 ka, kb, va, vb;
+                        lds_f32x4(sc + 4u * j, ka, kb);
+                        f32x2 a = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                        f32x2 b = pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                        if constexpr (L::I8) {
+                            a = fma2(a, mul2(ka, f2), n2);
+                            b = fma2(b, mul2(kb, f2), n2);
+                        } else {
+                            f32x2 ma, mb;
+                            lds_f32x4(sc + 512u + 4u * j, ma, mb);
+                            a = fma2(fma2(a, ka, mul2(ma, qs2)), f2, n2);
+                            b = fma2(fma2(b, kb, mul2(mb, qs2)), f2, n2);
+                        }
+                        float x[4];
+                        unpack2(a, x[0], x[1]);
+                        unpack2(b, x[2], x[3]);
+                        a = pack2(ex2(x[0]), ex2(x[1]));
+                        b = pack2(ex2(x[2]), ex2(x[3]));
+                        la = add2(la, a);
+                        lb = add2(lb, b);
+                        lds_f32x4(sc + 1024u + 4u * j, va, vb);
+                        if constexpr (!L::I8) {
+                            f32x2 wa, wb;
+                            lds_f32x4(sc + 1536u + 4u * j, wa, wb);
+                            oa = fma2(a, wa, oa);
+                            ob = fma2(b, wb, ob);
+                        }
+                        a = mul2(a, va);
+                        b = mul2(b, vb);
+                        unpack2(a, x[0], x[1]);
+                        unpack2(b, x[2], x[3]);
+                        const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
+                        ph[j / 2] = *reinterpret_cast<const uint32_t *>(&h0);
+                        ph[j / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+                        high[(j / 2) & 3] = __vmaxu2(high[(j / 2) & 3], ph[j / 2]);
+                        high[(j / 2 + 1) & 3] = __vmaxu2(high[(j / 2 + 1) & 3], ph[j / 2 + 1]);
                     }
-                    a = mul2(a, va);
-                    b = mul2(b, vb);
-                    unpack2(a, x[0], x[1]);
-                    unpack2(b, x[2], x[3]);
-                    const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
-                    ph[j / 2] = *reinterpret_cast<const uint32_t *>(&h0);
-                    ph[j / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+                    const uint32_t hi = __vmaxu2(__vmaxu2(high[0], high[1]), __vmaxu2(high[2], high[3]));
+                    careful = __any_sync(0xffffffffu, (hi & 0xffffu) >= 0x7800u || hi >= 0x78000000u);
+                    if (!careful) {
+                        l2 = add2(l2, la);
+                        l2b = add2(l2b, lb);
+                        off2 = add2(off2, oa);
+                        off2b = add2(off2b, ob);
+                    }
+                }
+                if (careful) {
+                    // scores over f, and their maximum
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};      // (short chains)
+#pragma unroll
+                    for (int j = 0; j < KM_HALF; j += 4) {
+                        f32x2 ka, kb;
+                        lds_f32x4(sc + 4u * j, ka, kb);
+                        f32x2 a = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                        f32x2 b = pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                        if constexpr (L::I8) {
+                            a = mul2(a, ka);
+                            b = mul2(b, kb);
+                        } else {
+                            f32x2 ma, mb;
+                            lds_f32x4(sc + 512u + 4u * j, ma, mb);
+                            a = fma2(a, ka, mul2(ma, qs2));
+                            b = fma2(b, kb, mul2(mb, qs2));
+                        }
+                        float x[4];
+                        unpack2(a, x[0], x[1]);
+                        unpack2(b, x[2], x[3]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            tops[y] = fmaxf(tops[y], x[y]);
+                            v[j + y] = __float_as_uint(x[y]);
+                        }
+                    }
+                    if (masked) {
+                        const uint32_t blocks = mask >> (4 * g);
+                        const int lim1 = lim < ntok ? lim : ntok;
+                        tops[0] = tops[1] = tops[2] = tops[3] = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < KM_HALF; ++j) {
+                            if (pos0 + j >= lim1 || !((blocks >> (j / KV_BLOCK)) & 1u))
+                                v[j] = 0xff800000u;
+                            tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(v[j]));
+                        }
+                    }
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    level = fmaxf(level, kv_scale_level(fmaxf(s_wmax[i & 3][2 * g], s_wmax[i & 3][2 * g + 1])));
+                    const float want = fmaf(top, f, level);
+                    const bool move = want > m + 8.f || (first && top > -INFINITY);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float old = m;
+                        m = fmaxf(m, want);
+                        const float c = old == -INFINITY ? 0.f : ex2(old - m);
+                        const f32x2 c2 = pack2(c, c);
+                        l2 = mul2(l2, c2);
+                        l2b = mul2(l2b, c2);
+                        off2 = mul2(off2, c2);
+                        off2b = mul2(off2b, c2);
+                        if (!first) {
+                            kv_wait(pv_done + 8u * g, (i - 1) & 1, dead);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int j = 0; j < D; j += 16) {
+                                uint32_t o[16];
+                                const uint32_t a = tmem + t_lane + TM_O + (uint32_t)g * D + j;
+                                tmem_ld16(a, o);
+#pragma unroll
+                                for (int x = 0; x < 16; ++x)
+                                    o[x] = __float_as_uint(__uint_as_float(o[x]) * c);
+                                tmem_st16(a, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float neg = m == -INFINITY ? 0.f : -m;
+                    const f32x2 n2 = pack2(neg, neg);
+#pragma unroll
+                    for (int j = 0; j < KM_HALF; j += 4) {
+                        f32x2 a = fma2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2, n2);
+                        f32x2 b = fma2(pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f2, n2);
+                        float x[4];
+                        unpack2(a, x[0], x[1]);
+                        unpack2(b, x[2], x[3]);
+                        a = pack2(ex2(x[0]), ex2(x[1]));
+                        b = pack2(ex2(x[2]), ex2(x[3]));
+                        l2 = add2(l2, a);
+                        l2b = add2(l2b, b);
+                        f32x2 va, vb;
+                        lds_f32x4(sc + 1024u + 4u * j, va, vb);
+                        if constexpr (!L::I8) {
+                            f32x2 oa, ob;
+                            lds_f32x4(sc + 1536u + 4u * j, oa, ob);
+                            off2 = fma2(a, oa, off2);
+                            off2b = fma2(b, ob, off2b);
+                        }
+                        a = mul2(a, va);
+                        b = mul2(b, vb);
+                        unpack2(a, x[0], x[1]);
+                        unpack2(b, x[2], x[3]);
+                        const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
+                        ph[j / 2] = *reinterpret_cast<const uint32_t *>(&h0);
+                        ph[j / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+                    }
                 }
                 if (i > 0)                                 // the half's last P has been read
                     kv_wait(pv_done + 8u * g, (i - 1) & 1, dead);
@@ -490,8 +434,8 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
             // ---- add the two halves up: this thread stores its row's half of the columns
             {
                 float a, b, c, d;
-                unpack2(l2, a, b);
-                unpack2(off2, c, d);
+                unpack2(add2(l2, l2b), a, b);
+                unpack2(add2(off2, off2b), c, d);
                 s_sum[g][row] = make_float4(m, a + b, c + d, 0.f);
             }
             kv_wait(pv_done + 8u * g, (i - 1) & 1, dead);
@@ -504,43 +448,190 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
             r.l = s0.y * c0 + s1.y * c1;
             const float offset = s0.z * c0 + s1.z * c1;
             const bool whole = un.k0 == 0 && un.k1 == un.n;
-            const int64_t slot = kv_piece_slot(un) * KM_ROWS + row;
-            const bool dead_now = bar_or(1, 256, gone());
-            if (warp_rows) {
+            const int64_t slot = kv_piece_slot(un) * KM_ROWS;
+            if (g == 0)
+                s_ml[row] = make_float2(r.m, r.l);
+            const bool leave = bar_or(1, 256, gone());     // (s_sum has been read)
+            if (warp_rows && !leave) {
+                // 16 columns at a time through the warp's 2 KB of shared memory: written by row,
+                // read four lanes to a row, so that a store fills whole sectors.  Float4 c of row
+                // n lies at place c ^ (n / 2 & 3): no bank conflicts either way.
+                const uint32_t st = sm + off.stage + (uint32_t)warp * 2048u;
+                const uint32_t w_at = st + (uint32_t)lane * 64u, w_key = (uint32_t)(lane >> 1) & 3u;
 #pragma unroll 1
                 for (int j = g * (D / 2); j < (g + 1) * (D / 2); j += 16) {
                     uint32_t a[16], b[16];
-                    tmem_ld16(tmem + t_lane + TM_O + j, a);
-                    tmem_ld16(tmem + t_lane + TM_O + D + j, b);
-                    if (!mine || dead_now)
-                        continue;
+                    tmem_ld16_async(tmem + t_lane + TM_O + j, a);
+                    tmem_ld16_async(tmem + t_lane + TM_O + D + j, b);
+                    tmem_wait_ld();
                     float x[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y)           // place -> column: permuted within 8
                         x[kv_column<L::I8>(y)] = fmaf(__uint_as_float(a[y]), c0, fmaf(__uint_as_float(b[y]), c1, offset));
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        r.o = make_float4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
+                    for (int y = 0; y < 4; ++y)
+                        sts128(w_at + ((((uint32_t)y) ^ w_key) << 4), __float_as_uint(x[4 * y]), __float_as_uint(x[4 * y + 1]),
+                               __float_as_uint(x[4 * y + 2]), __float_as_uint(x[4 * y + 3]));
+                    __syncwarp();
+#pragma unroll 1
+                    for (int n = lane >> 2; n < 32; n += 8) {
+                        const int nn = quad * 32 + n, c = lane & 3;
+                        const uint4 v = lds128(st + (uint32_t)n * 64u + (((uint32_t)c ^ ((uint32_t)n >> 1 & 3u)) << 4));
+                        if (nn >= nrows)
+                            continue;
+                        const float4 o = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                                                     __uint_as_float(v.w));
                         if (whole)
-                            kv_store4<D>(p, grow0 + row, un.h, j / 4 + y, r);
+                            kv_store4<D>(p, grow0 + nn, un.h, j / 4 + c, KvRowSum{s_ml[nn].x, s_ml[nn].y, o});
                         else
-                            *reinterpret_cast<float4 *>(p.piece_o + slot * D + j + 4 * y) = r.o;
+                            *reinterpret_cast<float4 *>(p.piece_o + (slot + nn) * D + j + 4 * c) = o;
                     }
+                    __syncwarp();
                 }
             }
-            if (!whole && !dead_now) {
+            if (!whole && !leave) {
                 if (mine && g == 0)
-                    *reinterpret_cast<float2 *>(p.piece_ml + slot * 2) = make_float2(r.m, r.l);
+                    *reinterpret_cast<float2 *>(p.piece_ml + (slot + row) * 2) = make_float2(r.m, r.l);
                 kv_join<D, KM_ROWS, 256>(p, sh, un, nrows, grow0, &s_last, t, 1);
             }
             tc_fence_before();
             bar_sync(1, 256);                              // O and s_sum may be written again
         }
+    } else if (warp < KM_COPY) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KM_REGS_OTHERS));
+        // ------------------------------- K and V: fp16 tiles in shared memory
+        const bool is_v = warp >= KM_V;
+        const int tok = (warp & 3) * 32 + lane;
+        const int r = tok & (KV_BLOCK - 1);
+        const KvRowAt<FMT, D> from(tok);
+        const KvRowTo to(tok);
+        const uint32_t full = is_v ? v_full : k_full, done = is_v ? v_done : k_done;
+        const uint32_t dst = sm + (is_v ? off.v : off.k);
+        int k = 0, k1 = 0, ntok = 0, u = 0, s = 0;
+        uint32_t round = 0u;                               // parity of the ring's round
+#pragma unroll 1
+        for (int i = 0; i < sh.tiles && !gone(); ++i, ++k) {
+            if (!is_v && k == k1) {
+                unit_wait(u);
+                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
+                k = un.k0, k1 = un.k1, ntok = un.ntok;
+                ++u;
+            }
+            kv_wait(raw_full + 8u * s, round, dead);
+            if (i >= 2)
+                kv_wait(done + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
+            const uint32_t raw = sm + (uint32_t)s * RAW, blk = raw + (uint32_t)(tok / KV_BLOCK) * L::BLOCK;
+            if (!is_v) {
+                // blocks of the tile that are there and hold tokens; bit 8: all of them do, wholly
+                uint32_t mask = s_valid[s];
+                if (mask == 0xffu && (k + 1) * KT_TOKENS <= ntok)
+                    mask |= 0x100u;
+                const bool here = ((mask >> (tok / KV_BLOCK)) & 1u) && k * KT_TOKENS + tok < ntok;
+                const float4 sc = here ? kv_scales<FMT, D>(blk, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+                KmScales &out = s_scales[i & 3];
+                out.ks[tok] = sc.x;
+                out.vs[tok] = sc.z;
+                if constexpr (!L::I8) {
+                    out.km[tok] = sc.y;
+                    out.vm[tok] = sc.w;
+                }
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.z));
+                if (lane == 0)
+                    s_wmax[i & 3][warp & 3] = __uint_as_float(top);
+                if (warp == KM_K && lane == 0)
+                    s_vmask[i & 3] = mask;
+            }
+            kv_row_to_tile<FMT, D>(raw + (is_v ? L::V_CODES : 0), from, dst + (uint32_t)(i & 1) * TILE_BYTES, to);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(full + 8u * (i & 1));
+                mbar_arrive(raw_empty + 8u * s);
+            }
+            if (++s == NS)
+                s = 0, round ^= 1u;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KM_REGS_OTHERS));
+        if (warp == KM_COPY) {
+            kv_copy_warp<FMT, D, KM_ROWS>(p, sh, s_len, s_unit, unit_full, sm, s_valid, raw_full, raw_empty, dead);
+        } else if (warp == KM_S) {
+        // ------------------------------------------------------ MMAs: S = q' K^T
+        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(KM_HALF >> 3) << 17) | (8u << 24);       // f16, f32 sums, M = 128
+        int u = -1, left = 0;
+#pragma unroll 1
+        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+            if (left == 0) {
+                ++u;
+                unit_wait(u);
+                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
+                left = un.k1 - un.k0;
+                kv_wait(q_full, u & 1, dead);
+            }
+            --left;
+            kv_wait(k_full + 8u * (i & 1), (i >> 1) & 1, dead);
+            const uint64_t bd = smem_desc_sw128(sm + off.k + (uint32_t)(i & 1) * TILE_BYTES);
+            const uint32_t blo = (uint32_t)bd, bhi = (uint32_t)(bd >> 32);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (i > 0)
+                    kv_wait(s_free + 8u * g, (i - 1) & 1, dead);
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)    // 64-column halves of K 16 KB apart
+                        mma_f16_tmem_a(tmem + TM_S + 64u * g, tmem + 8u * kk,
+                                       blo + (uint32_t)g * (8192 >> 4) + (uint32_t)(kk >> 2) * (KT_TOKENS * 128 >> 4) +
+                                           2u * (kk & 3),
+                                       bhi, idesc, kk > 0 ? 1u : 0u);
+                    mma_commit(s_full + 8u * g);
+                    if (g == 1)
+                        mma_commit(k_done + 8u * (i & 1));
+                }
+                __syncwarp();
+            }
+        }
+        } else if (warp == KM_O) {
+        // ------------------------------------------------------- MMAs: O += P V
+        constexpr uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);   // B is N-major
+        int u = -1, left = 0;
+#pragma unroll 1
+        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+            const bool first = left == 0;
+            if (first) {
+                ++u;
+                unit_wait(u);
+                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
+                left = un.k1 - un.k0;
+            }
+            --left;
+            kv_wait(v_full + 8u * (i & 1), (i >> 1) & 1, dead);
+            const uint64_t bd = (smem_desc_sw128(sm + off.v + (uint32_t)(i & 1) * TILE_BYTES) & ~((uint64_t)0x3fff << 16)) |
+                                ((uint64_t)(D == 128 ? KT_TOKENS * 128 >> 4 : 0) << 16);
+            const uint32_t blo = (uint32_t)bd, bhi = (uint32_t)(bd >> 32);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                kv_wait(p_full + 8u * g, i & 1, dead);
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < KM_HALF / 16; ++kk)          // 16 tokens: two groups of 8
+                        mma_f16_tmem_a(tmem + TM_O + (uint32_t)g * D, tmem + TM_P + 32u * g + 8u * kk,
+                                       blo + (uint32_t)g * (8192 >> 4) + (uint32_t)kk * (2048 >> 4), bhi, idesc,
+                                       kk > 0 || !first ? 1u : 0u);
+                    mma_commit(pv_done + 8u * g);
+                    if (g == 1)
+                        mma_commit(v_done + 8u * (i & 1));
+                }
+                __syncwarp();
+            }
+        }
+        }
     }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == KM_S) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");
     }
@@ -553,8 +644,8 @@ static KvKernel km_describe(const DeviceInfo &dev, int seqs)
     k.fn = reinterpret_cast<const void *>(&kv_many_rows_kernel<FMT, D>);
     k.tile = KM_ROWS;
     k.threads = KM_WARPS * 32;
-    // 1024: alignment; 10240: static arrays and the CTA's reserve
-    const size_t budget = dev.smem_optin - 1024 - 10240;
+    // 1024: alignment; 4096: static arrays and the CTA's reserve
+    const size_t budget = dev.smem_optin - 1024 - 4096;
     for (k.stages = KT_MAX_STAGES; k.stages > 1 && km_smem<FMT, D>(k.stages, seqs).total > budget;)
         --k.stages;
     k.smem = km_smem<FMT, D>(k.stages, seqs).total + 1024;
