@@ -1,6 +1,8 @@
 // Host side of the attention over the paged cache: choice of kernel, workspace, launches.
-// The kernels: kv_attention_few.cu, kv_attention_many.cu; what they compute and how work
+// The kernels: kv_attention_few.cuh, kv_attention_many.cu; what they compute and how work
 // is dealt out: kv_attention.cuh.
+#include <mutex>
+
 #include "kv_attention.cuh"
 
 namespace q4 {
@@ -15,7 +17,11 @@ static KvPlan kv_plan(const DeviceInfo &dev, const KvCacheDesc &c, int seqs, int
 {
     KvPlan t = {};
     t.rows = rows;
-    t.k = rows <= 16 ? kv_few_kernel(dev, c.format, c.head_dim, seqs) : kv_many_kernel(dev, c.format, c.head_dim, seqs);
+    if (rows > 16)
+        t.k = kv_many_kernel(dev, c.format, c.head_dim);
+    else
+        t.k = c.format == Q4_CACHE_INT8 ? kv_few_kernel_int8(dev, c.head_dim, (int)rows)
+                                        : kv_few_kernel_int4(dev, c.head_dim, (int)rows);
     t.row_tiles = (int)((rows + t.k.tile - 1) / t.k.tile);
     t.units = (int64_t)seqs * c.heads * t.row_tiles;
     t.grid = dev.sms;
@@ -68,6 +74,36 @@ size_t kv_attention_workspace_bytes(const DeviceInfo &dev, const KvCacheDesc &c,
     return kv_workspace(c, plans, n, n == 2 ? plans[1].rows : 0).total;
 }
 
+// Lets a kernel have the shared memory that its launches ask for, once per context and
+// larger size (the call costs about as much as a launch).
+static q4_status kv_allow_smem(const KvKernel &k)
+{
+    struct Set {
+        const void *fn;
+        void *ctx;
+        size_t bytes;
+    };
+    static std::mutex mu;
+    static Set sets[16];
+    void *ctx = current_context();
+    std::lock_guard<std::mutex> lock(mu);
+    Set *at = nullptr;
+    for (Set &s : sets)
+        if (s.fn == k.fn || (!s.fn && !at)) {
+            at = &s;
+            if (s.fn)
+                break;
+        }
+    if (at && at->fn == k.fn && ctx && at->ctx == ctx && at->bytes >= k.smem)
+        return Q4_OK;
+    cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaFuncSetAttribute(attention kernel)");
+    if (at)
+        *at = Set{k.fn, ctx, k.smem};
+    return Q4_OK;
+}
+
 static q4_status kv_tile_launch(const KvPlan &plan, KvTileParams &p, cudaStream_t st, bool pdl)
 {
     // a group of units of one (sequence, row tile) is counted in 32 bits
@@ -76,9 +112,9 @@ static q4_status kv_tile_launch(const KvPlan &plan, KvTileParams &p, cudaStream_
     p.rows = (int)plan.rows;
     p.row_tiles = plan.row_tiles;
     p.stages = plan.k.stages;
-    cudaError_t e = cudaFuncSetAttribute(plan.k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.k.smem);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "cudaFuncSetAttribute(attention kernel)");
+    q4_status s = kv_allow_smem(plan.k);
+    if (s != Q4_OK)
+        return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)plan.grid);
     cfg.blockDim = dim3((unsigned)plan.k.threads);
@@ -90,7 +126,7 @@ static q4_status kv_tile_launch(const KvPlan &plan, KvTileParams &p, cudaStream_
     cfg.attrs = pdl ? attr : nullptr;
     cfg.numAttrs = pdl ? 1 : 0;
     void *args[] = {&p};
-    e = cudaLaunchKernelExC(&cfg, plan.k.fn, args);
+    cudaError_t e = cudaLaunchKernelExC(&cfg, plan.k.fn, args);
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of the attention kernel");
 }
 

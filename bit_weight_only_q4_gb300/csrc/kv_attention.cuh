@@ -1,7 +1,7 @@
 // What the two attention kernels over the paged cache share: parameters, the list of
 // work, the copying warp, and the decoding of codes.
 //
-// kv_attention_few.cu   at most 16 query rows per key head: tokens are the MMA's M
+// kv_attention_few.cuh  at most 16 query rows per key head: tokens are the MMA's M
 //                       dimension
 // kv_attention_many.cu  more: query rows are its M dimension
 //
@@ -126,6 +126,41 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t v)
 {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((unsigned short)v) : "memory");
+}
+
+// Pairs of fp32 in one 64-bit register: one instruction for two operations.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ void lds_f32x4(uint32_t a, f32x2 &x, f32x2 &y)
+{
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
 }
 
 // True in one lane of a converged warp.  tcgen05 instructions issued under it take their
@@ -325,7 +360,7 @@ __device__ __forceinline__ void kv_row_to_tile(uint32_t codes, const KvRowAt<FMT
 // Units in list order: sequence, tile of rows, key head.  A unit's tiles cover the
 // tokens that its last row sees.
 struct KvWalk {
-    int b, rt;
+    int b, rt, len;
     int64_t base;                // first tile of (b, rt, head 0) in the list
     int ntok, nch;               // tokens and tiles of each unit of (b, rt)
 };
@@ -347,7 +382,8 @@ __device__ __forceinline__ int kv_tiles_of(int ntok)
 
 // What a CTA has of one unit: tiles k0 .. k1 - 1 of its n.
 struct KvUnit {
-    int b, rt, h, ntok, k0, k1, n, pad;
+    int b, rt, h, ntok, k0, k1, n;
+    int len;                     // cached tokens of the sequence (of the prefix)
     int64_t u0;                  // the unit's first tile in the list
 };
 
@@ -355,87 +391,84 @@ struct KvUnit {
 struct KvShare {
     int64_t share, c0, c1;
     int tiles;
-    KvWalk walk;                 // at c0
 };
 
-// Counts the tiles of all units (every thread of the CTA takes part); s_len gets the
-// sequences' lengths.  Two barriers.
-template <int N, int WARPS>
-__device__ __forceinline__ KvShare kv_share(const KvTileParams &p, int *s_len)
+__device__ __forceinline__ int kv_length(const KvTileParams &p, int b)
 {
-    __shared__ int64_t s_scan[WARPS], s_base;
-    __shared__ int s_b;
-    constexpr int NT = WARPS * 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int H = p.cache.heads;
-    const int per = (p.seqs + NT - 1) / NT;
-    const int first = tid * per;
-    auto tiles = [&](int len) {
-        int n = 0;
+    if (p.prefix_len > 0)
+        return p.prefix_len;
+    const int len = p.lengths[b];
+    return len < 0 ? 0 : (len < p.cap ? len : (int)p.cap);
+}
+
+// Tiles of all units of a sequence.
+template <int N>
+__device__ __forceinline__ int64_t kv_tiles_of_sequence(const KvTileParams &p, int len)
+{
+    int n = 0;
 #pragma unroll 1
-        for (int rt = 0; rt < p.row_tiles; ++rt)
-            n += kv_tiles_of(kv_unit_tokens<N>(p, len, rt));
-        return n;
-    };
-    int64_t mine = 0;
+    for (int rt = 0; rt < p.row_tiles; ++rt)
+        n += kv_tiles_of(kv_unit_tokens<N>(p, len, rt));
+    return (int64_t)n * p.cache.heads;
+}
+
+// Every warp counts the tiles of all units for itself: no warp waits for another before
+// it can start.
+template <int N>
+__device__ __forceinline__ KvShare kv_share(const KvTileParams &p)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t total = 0;
 #pragma unroll 1
-    for (int i = first; i < first + per && i < p.seqs; ++i) {
-        int64_t len = p.prefix_len > 0 ? p.prefix_len : p.lengths[i];
-        if (len > p.cap) {
-            len = p.cap;
-            if (blockIdx.x == 0)
-                atomicOr(p.err, kErrIndex);
-        }
-        const int n = len < 0 ? 0 : (int)len;
-        s_len[i] = n;
-        mine += (int64_t)tiles(n) * H;
-    }
-    int64_t incl = mine;
+    for (int i = lane; i < p.seqs; i += 32)
+        total += kv_tiles_of_sequence<N>(p, kv_length(p, i));
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += u;
-    }
-    if (lane == 31)
-        s_scan[warp] = incl;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int64_t at = incl - mine, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp)
-            at += s_scan[w];
-        total += s_scan[w];
-    }
-    KvShare s = {};
-    s.share = (total + gridDim.x - 1) / gridDim.x;
+    for (int o = 16; o >= 1; o >>= 1)
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    KvShare s;
+    s.share = (total >> 31) == 0 ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
+                                 : (total + gridDim.x - 1) / gridDim.x;
     s.c0 = s.share * blockIdx.x;
     s.c1 = s.c0 + s.share < total ? s.c0 + s.share : total;
     s.tiles = s.c1 > s.c0 ? (int)(s.c1 - s.c0) : 0;
-    if (s.c0 >= at && s.c0 < at + mine) {
-        int i = first;
-#pragma unroll 1
-        for (int64_t n; at + (n = (int64_t)tiles(s_len[i]) * H) <= s.c0; ++i)
-            at += n;
-        s_b = i;
-        s_base = at;
-    }
-    __syncthreads();
-    if (s.tiles > 0) {
-        s.walk.b = s_b;
-        s.walk.base = s_base;
-        s.walk.ntok = kv_unit_tokens<N>(p, s_len[s_b], 0);
-        s.walk.nch = kv_tiles_of(s.walk.ntok);
-    }
     return s;
+}
+
+// The sequence that tile c0 of the list lies in (a warp, 32 sequences at a time).
+template <int N>
+__device__ __forceinline__ KvWalk kv_find(const KvTileParams &p, int64_t c0)
+{
+    const int lane = threadIdx.x & 31;
+    KvWalk w = {};
+    int64_t before = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < p.seqs; i0 += 32) {
+        const int64_t mine = i0 + lane < p.seqs ? kv_tiles_of_sequence<N>(p, kv_length(p, i0 + lane)) : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += u;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > c0);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            w.b = i0 + at;
+            w.base = before + __shfl_sync(0xffffffffu, incl - mine, at);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    w.len = kv_length(p, w.b);
+    w.ntok = kv_unit_tokens<N>(p, w.len, 0);
+    w.nch = kv_tiles_of(w.ntok);
+    return w;
 }
 
 // The unit at tile f of the list.
 template <int N>
-__device__ __forceinline__ KvUnit kv_next_unit(const KvTileParams &p, const int *s_len, KvWalk &w, int64_t f,
-                                               int64_t c1)
+__device__ __forceinline__ KvUnit kv_next_unit(const KvTileParams &p, KvWalk &w, int64_t f, int64_t c1)
 {
     const int H = p.cache.heads;
 #pragma unroll 1
@@ -444,8 +477,9 @@ __device__ __forceinline__ KvUnit kv_next_unit(const KvTileParams &p, const int 
         if (++w.rt == p.row_tiles) {
             w.rt = 0;
             ++w.b;
+            w.len = kv_length(p, w.b);
         }
-        w.ntok = kv_unit_tokens<N>(p, s_len[w.b], w.rt);
+        w.ntok = kv_unit_tokens<N>(p, w.len, w.rt);
         w.nch = kv_tiles_of(w.ntok);
     }
     const uint32_t x = (uint32_t)(f - w.base);     // the host bounds a unit group's tiles
@@ -455,7 +489,7 @@ __device__ __forceinline__ KvUnit kv_next_unit(const KvTileParams &p, const int 
     s.rt = w.rt;
     s.ntok = w.ntok;
     s.n = w.nch;
-    s.pad = 0;
+    s.len = w.len;
     s.u0 = w.base + (int64_t)s.h * w.nch;
     s.k0 = (int)(f - s.u0);
     s.k1 = c1 - s.u0 < w.nch ? (int)(c1 - s.u0) : w.nch;
@@ -469,15 +503,22 @@ __device__ __forceinline__ KvUnit kv_next_unit(const KvTileParams &p, const int 
 // before them are being copied: a look-up takes about as long as the copy of a tile.
 // s_valid[stage] says which blocks of the tile there are.
 template <int FMT, int D, int N>
-__device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShare &sh, const int *s_len,
-                                             KvUnit *s_unit, uint32_t unit_full, uint32_t ring, uint32_t *s_valid,
+__device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShare &sh, KvUnit *s_unit,
+                                             uint32_t unit_full, uint32_t ring, uint32_t *s_valid,
                                              uint32_t raw_full, uint32_t raw_empty, const KvDead &dead)
 {
     using L = KvLayout<FMT, D>;
     constexpr uint32_t RAW = KT_BLOCKS * L::BLOCK;
     const int lane = threadIdx.x & 31;
     const int NS = p.stages;
-    KvWalk walk = sh.walk;
+    if (blockIdx.x == 0 && p.prefix_len == 0)      // a length that the table cannot hold
+#pragma unroll 1
+        for (int b = lane; b < p.seqs; b += 32)
+            if (p.lengths[b] > p.cap)
+                atomicOr(p.err, kErrIndex);
+    if (sh.tiles == 0)
+        return;
+    KvWalk walk = kv_find<N>(p, sh.c0);
     int64_t f = sh.c0;
     int k = 0, k1 = 0, u = 0, ntok = 0, head = 0;
     const int32_t *table = p.table;
@@ -496,7 +537,7 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
         const int m = n;
         // the next ones
         if (k == k1 && f < sh.c1) {
-            const KvUnit un = kv_next_unit<N>(p, s_len, walk, f, sh.c1);
+            const KvUnit un = kv_next_unit<N>(p, walk, f, sh.c1);
             if (lane == 0) {
                 s_unit[u & (KT_UNITS - 1)] = un;
                 mbar_arrive(unit_full + 8u * (u & (KT_UNITS - 1)));
@@ -677,6 +718,15 @@ __device__ __forceinline__ const uint16_t *kv_q_row(const KvTileParams &p, int g
     return p.q + token * p.q_stride + (int64_t)(h * p.group + grow - token * p.group) * D;
 }
 
+// Initialises barriers first .. first + n - 1 of a CTA with a count each, a lane per
+// barrier (at most 32).
+__device__ __forceinline__ void kv_init_bars(uint32_t first, int n, uint32_t count)
+{
+    const int lane = threadIdx.x & 31;
+    if (lane < n)
+        mbar_init(first + 8u * lane, count);
+}
+
 // ------------------------------------------------------------------ host side
 struct KvKernel {
     const void *fn;
@@ -685,7 +735,8 @@ struct KvKernel {
     size_t smem;
 };
 
-KvKernel kv_few_kernel(const DeviceInfo &dev, int format, int head_dim, int seqs);
-KvKernel kv_many_kernel(const DeviceInfo &dev, int format, int head_dim, int seqs);
+KvKernel kv_few_kernel_int8(const DeviceInfo &dev, int head_dim, int rows);
+KvKernel kv_few_kernel_int4(const DeviceInfo &dev, int head_dim, int rows);
+KvKernel kv_many_kernel(const DeviceInfo &dev, int format, int head_dim);
 
 }  // namespace q4

@@ -6,18 +6,24 @@
 // so a few rows cost the tensor cores little, each token is one thread's TMEM lane and
 // its scales are that thread's scalars, and no row needs a reduction over tokens until
 // its reference has to move.  K goes dequantised into tensor memory (A operand), V into
-// shared memory (A operand, token rows as they lie: M-major), P^T into shared memory.
+// shared memory (A operand, token rows as they lie: M-major), P^T into shared memory
+// (B operand, a token's 16 rows together: N-major).  Of the 16 columns only the first NR
+// = 4, 8 or 16, the least that holds the rows, are ever computed.
 //
-// One CTA per SM, 23 warps: one copies blocks, one issues the MMAs, one loads queries;
+// One CTA per SM, 24 warps: one copies blocks, two issue the MMAs, one loads queries;
 // four decode K, four V; two groups of four take the tiles' softmax in turn, each with
 // references, sums and an accumulator of its own; four put the two together at the end of
-// a unit and store, while the others are at the next one.
+// a unit and store, while the others are at the next one.  A tile's MMAs take some 660
+// cycles (D = 128), its decoding and softmax some 2,500 warp instructions.
+#pragma once
+
 #include "kv_attention.cuh"
 
 namespace q4 {
 
 constexpr int KF_N = 16;
-constexpr int KF_K = 2, KF_V = 6, KF_S = 10, KF_E = 18, KF_Q = 22, KF_WARPS = 23;
+constexpr int KF_COPY = 0, KF_MMA_S = 1, KF_K = 2, KF_V = 6, KF_S = 10, KF_E = 18, KF_Q = 22, KF_MMA_O = 23,
+              KF_WARPS = 24;
 constexpr int KF_ROW_SLOTS = 8;                    // units whose rows are described at a time
 
 struct KfRows {
@@ -36,13 +42,13 @@ struct KfSums {
     int pad[3];
 };
 
-// Shared memory: [raw ring][V: 2][q: 2][P: 2][o][token scales: 4][lengths]
+// Shared memory: [raw ring][V: 2][q: 2][P: 2][o][token scales: 4]
 struct KfSmem {
-    uint32_t v, q, p, o, info, len, total;
+    uint32_t v, q, p, o, info, total;
 };
 
 template <int FMT, int D>
-__host__ __device__ inline KfSmem kf_smem(int stages, int seqs)
+__host__ __device__ inline KfSmem kf_smem(int stages)
 {
     KfSmem s = {};
     uint32_t at = (uint32_t)stages * KT_BLOCKS * KvLayout<FMT, D>::BLOCK;
@@ -52,12 +58,42 @@ __host__ __device__ inline KfSmem kf_smem(int stages, int seqs)
     s.p = at, at += 2u * KF_N * KT_TOKENS * 2;
     s.o = at, at += KF_N * D * 4u;
     s.info = at, at += 4u * KT_TOKENS * 16;
-    s.len = at, at += ((uint32_t)seqs * 4u + 15u) & ~15u;
     s.total = at;
     return s;
 }
 
-template <int FMT, int D>
+// NR fp32 columns of the warp's lanes (after a wait).
+template <int NR>
+__device__ __forceinline__ void kf_tmem_ld(uint32_t addr, uint32_t (&v)[NR])
+{
+    if constexpr (NR == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+    else if constexpr (NR == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "r"(addr));
+    else
+        tmem_ld16_async(addr, v);
+    tmem_wait_ld();
+}
+
+template <int NR>
+__device__ __forceinline__ void kf_tmem_st(uint32_t addr, const uint32_t (&v)[NR])
+{
+    if constexpr (NR == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
+                     ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    else if constexpr (NR == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    else
+        tmem_st16(addr, v);
+    tmem_wait_st();
+}
+
+template <int FMT, int D, int NR>
 __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvTileParams p)
 {
     using L = KvLayout<FMT, D>;
@@ -68,7 +104,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     // tensor memory: two K tiles (D / 2 columns), two S tiles (16), O of two units and groups (16)
     constexpr uint32_t TM_S = D, TM_O = D + 2 * KF_N, TM_COLS = 256;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 20 + KT_UNITS];
+    __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 22 + KT_UNITS];
     __shared__ KvUnit s_unit[KT_UNITS];
     __shared__ __align__(16) KfRows s_rows[KF_ROW_SLOTS];
     __shared__ __align__(16) KfSums s_sums[2][2];          // [unit][group]
@@ -79,117 +115,120 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
     __shared__ int s_last, s_dead;
     const int NS = p.stages;
-    const KfSmem off = kf_smem<FMT, D>(NS, p.seqs);
+    const KfSmem off = kf_smem<FMT, D>(NS);
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = smem_u32(smem);
     float4 *s_info = reinterpret_cast<float4 *>(smem + off.info);      // [4][128], see kv_scales
-    int *s_len = reinterpret_cast<int *>(smem + off.len);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t raw_full = smem_u32(s_bar), raw_empty = raw_full + 8u * KT_MAX_STAGES;
-    const uint32_t k_full = raw_empty + 8u * KT_MAX_STAGES, s_full = k_full + 16, p_full = k_full + 32,
-                   v_full = k_full + 48, pv_done = k_full + 64, q_full = k_full + 80, q_empty = k_full + 96,
-                   o_full = k_full + 112, o_empty = k_full + 128, sums_full = k_full + 144,
-                   unit_full = k_full + 160;
-    if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(raw_full + 8u * i, 1);
-            mbar_init(raw_empty + 8u * i, 8);              // K and V warps
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(k_full + 8u * i, 4);
-            mbar_init(s_full + 8u * i, 1);                 // commit: S is there, K has been read
-            mbar_init(p_full + 8u * i, 4);
-            mbar_init(v_full + 8u * i, 4);
-            mbar_init(pv_done + 8u * i, 1);                // commit: P and V have been read, O is there
-            mbar_init(q_full + 8u * i, 1);
-            mbar_init(q_empty + 8u * i, 1);                // commit after a unit's last S
-            mbar_init(o_full + 8u * i, 1);                 // commit after a unit's last O
-            mbar_init(o_empty + 8u * i, 4);
-            mbar_init(sums_full + 8u * i, 8);
-        }
-        for (int i = 0; i < KT_UNITS; ++i)
-            mbar_init(unit_full + 8u * i, 1);
+    const uint32_t k_full = raw_empty + 8u * KT_MAX_STAGES, s_full = k_full + 16, s_free = k_full + 32,
+                   p_full = k_full + 48, v_full = k_full + 64, pv_done = k_full + 80, q_full = k_full + 96,
+                   q_empty = k_full + 112, o_full = k_full + 128, o_empty = k_full + 144, sums_full = k_full + 160,
+                   unit_full = k_full + 176;
+    if (warp == KF_COPY) {
+        kv_init_bars(raw_full, NS, 1);
+        kv_init_bars(raw_empty, NS, 8);                    // K and V warps
+        kv_init_bars(k_full, 2, 4);
+        kv_init_bars(s_full, 2, 1);                        // commit: S is there, K has been read
+        kv_init_bars(s_free, 2, 4);
+        kv_init_bars(p_full, 2, 4);
+        kv_init_bars(v_full, 2, 4);
+        kv_init_bars(pv_done, 2, 1);                       // commit: P and V have been read, O is there
+        kv_init_bars(q_full, 2, 1);
+        kv_init_bars(q_empty, 2, 1);                       // commit after a unit's last S
+        kv_init_bars(o_full, 2, 1);                        // commit after a unit's last O
+        kv_init_bars(o_empty, 2, 4);
+        kv_init_bars(sums_full, 2, 8);
+        kv_init_bars(unit_full, KT_UNITS, 1);
+        if (lane == 0)
+            s_dead = 0;
+        if (lane < KF_N)
+            s_zero[lane] = 0.f;
         mbar_init_fence();
-    }
-    if (tid < KF_N)
-        s_zero[tid] = 0.f;
-    if (tid == 0)
-        s_dead = 0;
-    if (warp == 1) {
+    } else if (warp == KF_MMA_S) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&s_tmem)), "n"(TM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (warp >= KF_S && warp < KF_E) {              // the rows of P that no one writes
+        for (uint32_t x = (uint32_t)(tid - KF_S * 32) * 16u; x < 2u * P_BYTES; x += 8u * 32u * 16u)
+            sts128(sm + off.p + x, 0u, 0u, 0u, 0u);
+        fence_proxy_async();
     }
-    pdl_wait();
-    const KvShare sh = kv_share<KF_N, KF_WARPS>(p, s_len);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     const uint32_t tmem = s_tmem;
+    pdl_wait();
+    const KvShare sh = kv_share<KF_N>(p);
     const KvDead dead = {p.err, &s_dead};
     auto gone = [&]() { return *dead.flag != 0; };
     // unit u of this CTA, once it has been described
     auto unit_wait = [&](int u) { kv_wait(unit_full + 8u * (u & (KT_UNITS - 1)), (u / KT_UNITS) & 1, dead); };
 
-    if (warp == 0) {
-        kv_copy_warp<FMT, D, KF_N>(p, sh, s_len, s_unit, unit_full, sm, s_valid, raw_full, raw_empty, dead);
-    } else if (warp == 1) {
-        // --------------------------------------------------------------- MMAs
-        constexpr uint32_t idesc1 = (1u << 4) | ((uint32_t)(KF_N >> 3) << 17) | (8u << 24);   // f16, f32 sums, M = 128
-        constexpr uint32_t idesc2 = idesc1 | (1u << 15);                                      // A is M-major
-        // V^T: 64-column halves 16 KB apart, groups of 8 tokens 1 KB apart (D = 64 has one half;
-        // lanes 64 .. 127 of O^T then repeat lanes 0 .. 63)
-        constexpr uint32_t v_lbo = D == 128 ? KT_TOKENS * 128 >> 4 : 0u;
-        int u1 = -1, left1 = 0;                            // unit of the next S, tiles left in it
-        int u2 = -1, left2 = 0;                            // unit of the next O
-        uint32_t begun = 0u;                               // groups that have begun u2
-        auto begin = [&](int &u, int &left) {
-            ++u;
-            unit_wait(u);
-            const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-            left = un.k1 - un.k0;
-        };
-        auto mma1 = [&](int i) {                           // S(i) = K q^T
-            if (left1 == 0) {
-                begin(u1, left1);
-                kv_wait(q_full + 8u * (u1 & 1), (u1 >> 1) & 1, dead);
+    if (warp == KF_COPY) {
+        kv_copy_warp<FMT, D, KF_N>(p, sh, s_unit, unit_full, sm, s_valid, raw_full, raw_empty, dead);
+    } else if (warp == KF_MMA_S) {
+        // -------------------------------------------------- MMAs: S^T = K q'^T
+        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(KF_N >> 3) << 17) | (8u << 24);    // f16, f32 sums, M = 128
+        int u = -1, left = 0;
+#pragma unroll 1
+        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+            if (left == 0) {
+                ++u;
+                unit_wait(u);
+                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
+                left = un.k1 - un.k0;
+                kv_wait(q_full + 8u * (u & 1), (u >> 1) & 1, dead);
             }
+            --left;
             kv_wait(k_full + 8u * (i & 1), (i >> 1) & 1, dead);
+            if (i >= 2)
+                kv_wait(s_free + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
             tc_fence_after();
-            --left1;
-            const uint64_t bd = smem_desc_sw128(sm + off.q + (u1 & 1) * Q_BYTES);
+            const uint64_t bd = smem_desc_sw128(sm + off.q + (u & 1) * Q_BYTES);
             const uint32_t blo = (uint32_t)bd, bhi = (uint32_t)(bd >> 32);
             const uint32_t a = tmem + (uint32_t)(i & 1) * (D / 2);
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)        // 64-column sub-tiles of q: 16 x 128 bytes
                     mma_f16_tmem_a(tmem + TM_S + (uint32_t)(i & 1) * KF_N, a + 8u * kk,
-                                   blo + (uint32_t)(kk >> 2) * (KF_N * 128 >> 4) + 2u * (kk & 3), bhi, idesc1,
+                                   blo + (uint32_t)(kk >> 2) * (KF_N * 128 >> 4) + 2u * (kk & 3), bhi, idesc,
                                    kk > 0 ? 1u : 0u);
                 mma_commit(s_full + 8u * (i & 1));
-                if (left1 == 0)
-                    mma_commit(q_empty + 8u * (u1 & 1));
+                if (left == 0)
+                    mma_commit(q_empty + 8u * (u & 1));
             }
             __syncwarp();
-        };
-        if (sh.tiles > 0)
-            mma1(0);
+        }
+    } else if (warp == KF_MMA_O) {
+        // ------------------------------------------------ MMAs: O^T += V^T P^T
+        // A is M-major: 64-column halves 16 KB apart, groups of 8 tokens 1 KB apart (D = 64 has
+        // one half; lanes 64 .. 127 of O^T then repeat lanes 0 .. 63).  B is N-major without
+        // swizzle: 16 bytes a token, its rows 8 .. 15 2 KB behind.
+        constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(KF_N >> 3) << 17) | (8u << 24);
+        constexpr uint32_t v_lbo = D == 128 ? KT_TOKENS * 128 >> 4 : 0u;
+        int u = -1, left = 0;
+        uint32_t begun = 0u;                               // groups that have begun the unit
 #pragma unroll 1
         for (int i = 0; i < sh.tiles && !gone(); ++i) {
             const int g = i & 1;
-            if (i + 1 < sh.tiles)
-                mma1(i + 1);
-            if (left2 == 0) {
-                begin(u2, left2);
+            if (left == 0) {
+                ++u;
+                unit_wait(u);
+                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
+                left = un.k1 - un.k0;
                 begun = 0u;
-                if (u2 >= 2)                               // its accumulators have been read
-                    kv_wait(o_empty + 8u * (u2 & 1), ((u2 >> 1) - 1) & 1, dead);
+                if (u >= 2)                                // its accumulators have been read
+                    kv_wait(o_empty + 8u * (u & 1), ((u >> 1) - 1) & 1, dead);
             }
+            --left;
             kv_wait(v_full + 8u * g, (i >> 1) & 1, dead);
             kv_wait(p_full + 8u * g, (i >> 1) & 1, dead);
             tc_fence_after();
-            --left2;
-            const uint64_t bd = smem_desc_sw128(sm + off.p + (uint32_t)g * P_BYTES);
-            const uint32_t blo = (uint32_t)bd, bhi = (uint32_t)(bd >> 32);
+            const uint32_t b_at = sm + off.p + (uint32_t)g * P_BYTES;
+            const uint32_t blo = ((b_at & 0x3FFFFu) >> 4) | (8u << 16), bhi = (2048u >> 4) | (1u << 14);
             const uint64_t ad = (smem_desc_sw128(sm + off.v + (uint32_t)g * V_BYTES) & ~((uint64_t)0x3fff << 16)) |
                                 ((uint64_t)v_lbo << 16);
             const uint32_t alo = (uint32_t)ad, ahi = (uint32_t)(ad >> 32);
@@ -197,12 +236,11 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < KT_TOKENS / 16; ++kk)        // 16 tokens: two groups of 8
-                    mma_f16_2(tmem + TM_O + (uint32_t)((u2 & 1) * 2 + g) * KF_N, alo + (uint32_t)kk * (2048 >> 4), ahi,
-                              blo + (uint32_t)(kk >> 2) * (KF_N * 128 >> 4) + 2u * (kk & 3), bhi, idesc2,
-                              kk > 0 ? 1u : more);
+                    mma_f16_2(tmem + TM_O + (uint32_t)((u & 1) * 2 + g) * KF_N, alo + (uint32_t)kk * (2048 >> 4), ahi,
+                              blo + (uint32_t)kk * (256 >> 4), bhi, idesc, kk > 0 ? 1u : more);
                 mma_commit(pv_done + 8u * g);
-                if (left2 == 0)
-                    mma_commit(o_full + 8u * (u2 & 1));
+                if (left == 0)
+                    mma_commit(o_full + 8u * (u & 1));
             }
             __syncwarp();
             begun |= 1u << g;
@@ -227,17 +265,17 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             if (i >= 2)
                 kv_wait(s_full + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
             tc_fence_after();
-            const uint32_t blk = sm + (uint32_t)s * RAW + (uint32_t)(tok / KV_BLOCK) * L::BLOCK;
-            const uint32_t src = sm + (uint32_t)s * RAW + from.base;
+            const uint32_t raw = sm + (uint32_t)s * RAW;
             // blocks of the tile that are there and hold tokens; bit 8: all of them do, wholly
             uint32_t mask = s_valid[s];
             if (mask == 0xffu && (k + 1) * KT_TOKENS <= ntok)
                 mask |= 0x100u;
             const bool here = ((mask >> (tok / KV_BLOCK)) & 1u) && k * KT_TOKENS + tok < ntok;
-            s_info[(i & 3) * KT_TOKENS + tok] = here ? kv_scales<FMT, D>(blk, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+            s_info[(i & 3) * KT_TOKENS + tok] =
+                here ? kv_scales<FMT, D>(raw + (uint32_t)(tok / KV_BLOCK) * L::BLOCK, r) : make_float4(0.f, 0.f, 0.f, 0.f);
             if (warp == KF_K && lane == 0)
                 s_vmask[i & 3] = mask;
-            const uint32_t dst = tmem + t_lane + (uint32_t)(i & 1) * (D / 2);
+            const uint32_t src = raw + from.base, dst = tmem + t_lane + (uint32_t)(i & 1) * (D / 2);
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {             // 32 columns: 16 packed
                 uint32_t v[4][4];
@@ -329,7 +367,6 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             int ex = 141 - (int)(top >> 7);                // the largest goes to [2^14, 2^15)
             ex = ex > 126 ? 126 : ex;
             const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-            int least = 0x7fffffff;
 #pragma unroll
             for (int j = 0; j < KF_N / RPP; ++j) {
                 const int n = lane / LPR + j * RPP;
@@ -357,10 +394,10 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                         rows.qsum[n] = sum;
                 }
             }
+            int least = 0x7fffffff;
             if (lane < KF_N) {                             // rows that fill the tile up: no limit, never stored
-                const int lim = lane < nrows ? kv_row_limit(p, grow0 + lane, s_len[un.b]) : 0x7fffffff;
-                rows.lim[lane] = lim;
-                least = lim;
+                least = lane < nrows ? kv_row_limit(p, grow0 + lane, un.len) : 0x7fffffff;
+                rows.lim[lane] = least;
             }
             least = __reduce_min_sync(0xffffffffu, least);
             if (lane == 0) {
@@ -381,9 +418,9 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         const int tok = quad * 32 + lane;                  // TMEM lane
         const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
         const int bar_id = 1 + grp;
-        const uint32_t p_dst = sm + off.p + (uint32_t)grp * P_BYTES + (uint32_t)(tok >> 6) * (KF_N * 128u) +
-                               (uint32_t)(tok & 7) * 2u;
-        const uint32_t ch = (uint32_t)(tok & 63) << 1 & 0x70u;
+        const uint32_t p_dst = sm + off.p + (uint32_t)grp * P_BYTES + (uint32_t)tok * 16u;
+        const uint32_t s_at = tmem + t_lane + TM_S + (uint32_t)grp * KF_N;
+        const uint32_t nm_at = smem_u32(s_nm[grp]), zero_at = smem_u32(s_zero);
         int nmb = 0;                                       // current half of s_nm
         bool leave = false;                                // a wait has given up: agreed on by vote
         int i = 0;                                         // first tile of the unit
@@ -391,137 +428,149 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         for (int u = 0; i < sh.tiles && !leave; ++u) {
             unit_wait(u);
             const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-            const int ntok = un.ntok, k0 = un.k0;
-            const int end = i + un.k1 - k0;
+            const int ntok = un.ntok, k0 = un.k0 - i;
+            const int end = i + un.k1 - un.k0;
             const KfRows &rows = s_rows[u & (KF_ROW_SLOTS - 1)];
-            float l[KF_N], sum_off[L::I8 ? 1 : KF_N];
+            f32x2 l2[NR / 2], off2[L::I8 ? 1 : NR / 2];
 #pragma unroll
-            for (int j = 0; j < KF_N; ++j)
-                l[j] = 0.f;
+            for (int j = 0; j < NR / 2; ++j)
+                l2[j] = 0ull;
 #pragma unroll
-            for (int j = 0; j < (L::I8 ? 1 : KF_N); ++j)
-                sum_off[j] = 0.f;
+            for (int j = 0; j < (L::I8 ? 1 : NR / 2); ++j)
+                off2[j] = 0ull;
             float level = -36.f;                           // E - 6
             bool first = true;
-            const int i0 = i + ((i ^ grp) & 1);
 #pragma unroll 1
-            for (int it = i0; it < end && !leave; it += 2) {
+            for (int it = i + ((i ^ grp) & 1); it < end && !leave; it += 2) {
                 kv_wait(s_full + 8u * grp, (it >> 1) & 1, dead);
                 tc_fence_after();
                 const float4 info = s_info[(it & 3) * KT_TOKENS + tok];
                 const uint32_t mask = s_vmask[it & 3];
-                const int k = k0 + it - i;
-                const bool masked = !(mask & 0x100u) || (k + 1) * KT_TOKENS > rows.least;
-                int pos = k * KT_TOKENS + tok;
-                if (pos >= ntok || !((mask >> (tok / KV_BLOCK)) & 1u))
+                const bool masked = !(mask & 0x100u) || (k0 + it + 1) * KT_TOKENS > rows.least;
+                int pos = (k0 + it) * KT_TOKENS + tok;
+                if (masked && (pos >= ntok || !((mask >> (tok / KV_BLOCK)) & 1u)))
                     pos = 0x7fffffff;
-                const float ks = info.x * rows.f, km = info.y * rows.f;
-                // Scores over the references (what = 0).  If one is too large, or none are
-                // set, the group goes round again: scores over zero (1), from which the new
-                // references are taken, then over those (2).
-                float s[KF_N];
+                const float ks = info.x * rows.f;
+                const f32x2 ks2 = pack2(ks, ks), vs2 = pack2(info.z, info.z);
+                // Products over the references as they are (what = 0).  If one reaches 2^15, or the
+                // unit begins, the group goes round with scores over zero (1), from which the new
+                // references are taken, and then over those (2).
+                f32x2 x2[NR / 2];
+                uint32_t h[NR / 2];
 #pragma unroll 1
-                for (int what = 0; what < 3; ++what) {
-                    const float *nms = what == 1 ? s_zero : s_nm[grp][nmb];
-                    uint32_t acc[KF_N];
-                    tmem_ld16(tmem + t_lane + TM_S + (uint32_t)grp * KF_N, acc);
+                for (int what = first ? 1 : 0; what < 3; ++what) {
+                    uint32_t acc[NR];
+                    kf_tmem_ld<NR>(s_at, acc);
+                    const uint32_t nm = what == 1 ? zero_at : nm_at + (uint32_t)nmb * (KF_N * 4);
 #pragma unroll
-                    for (int j = 0; j < KF_N; j += 4) {
-                        const float4 nm = *reinterpret_cast<const float4 *>(nms + j);
-                        const float base[4] = {nm.x, nm.y, nm.z, nm.w};
-                        if constexpr (L::I8) {
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                s[j + x] = fmaf(__uint_as_float(acc[j + x]), ks, base[x]);
-                        } else {
-                            const float4 qs = *reinterpret_cast<const float4 *>(rows.qsum + j);
-                            const float q4[4] = {qs.x, qs.y, qs.z, qs.w};
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                s[j + x] = fmaf(__uint_as_float(acc[j + x]), ks, fmaf(km, q4[x], base[x]));
+                    for (int j = 0; j < NR / 4; ++j) {
+                        f32x2 na, nb;
+                        lds_f32x4(nm + 16u * j, na, nb);
+                        if constexpr (!L::I8) {
+                            const float km = info.y * rows.f;
+                            f32x2 qa, qb;
+                            lds_f32x4(smem_u32(rows.qsum) + 16u * j, qa, qb);
+                            na = fma2(pack2(km, km), qa, na);
+                            nb = fma2(pack2(km, km), qb, nb);
                         }
+                        x2[2 * j] = fma2(pack2(__uint_as_float(acc[4 * j]), __uint_as_float(acc[4 * j + 1])), ks2, na);
+                        x2[2 * j + 1] = fma2(pack2(__uint_as_float(acc[4 * j + 2]), __uint_as_float(acc[4 * j + 3])), ks2, nb);
                     }
                     if (masked) {
 #pragma unroll
-                        for (int j = 0; j < KF_N; j += 4) {
-                            const int4 lm = *reinterpret_cast<const int4 *>(rows.lim + j);
-                            s[j] = pos >= lm.x ? -INFINITY : s[j];
-                            s[j + 1] = pos >= lm.y ? -INFINITY : s[j + 1];
-                            s[j + 2] = pos >= lm.z ? -INFINITY : s[j + 2];
-                            s[j + 3] = pos >= lm.w ? -INFINITY : s[j + 3];
+                        for (int j = 0; j < NR / 2; ++j) {
+                            float a, b;
+                            unpack2(x2[j], a, b);
+                            a = pos >= rows.lim[2 * j] ? -INFINITY : a;
+                            b = pos >= rows.lim[2 * j + 1] ? -INFINITY : b;
+                            x2[j] = pack2(a, b);
                         }
                     }
-                    if (what == 0) {
-                        float top = s[0];
+                    if (what != 1) {
+                        uint32_t high = 0u;
 #pragma unroll
-                        for (int j = 1; j < KF_N; ++j)
-                            top = fmaxf(top, s[j]);
-                        if (!bar_or(bar_id, 128, first || top + level > 8.f || kv_scale_level(info.z) > level || gone()))
+                        for (int j = 0; j < NR / 2; ++j) {
+                            float a, b;
+                            unpack2(x2[j], a, b);
+                            x2[j] = pack2(ex2(a), ex2(b));
+                            unpack2(mul2(x2[j], vs2), a, b);
+                            const __half2 hh = __floats2half2_rn(a, b);
+                            h[j] = *reinterpret_cast<const uint32_t *>(&hh);
+                            high = __vmaxu2(high, h[j]);
+                        }
+                        if (what == 0 &&
+                            !bar_or(bar_id, 128, (high & 0xffffu) >= 0x7800u || high >= 0x78000000u || gone()))
                             break;
-                    } else if (what == 1) {
-                        // Move the references; rescale what has been summed.
+                        continue;
+                    }
+                    // Move the references; rescale what has been summed.
+                    {
+                        float z[NR];
+#pragma unroll
+                        for (int j = 0; j < NR / 2; ++j)
+                            unpack2(x2[j], z[2 * j], z[2 * j + 1]);
                         int idx;
-                        const float z = warp_max_transpose<KF_N>(s, lane, idx);
-                        s_red[grp][gw][idx] = z;           // lanes of one idx hold one value
-                        float wm = info.z;
+                        const float top = warp_max_transpose<NR>(z, lane, idx);
+                        s_red[grp][gw][idx] = top;         // lanes of one idx hold one value
+                    }
+                    // (magnitudes order as their bits do)
+                    const uint32_t wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(info.z)));
+                    if (lane == 0)
+                        s_wred[grp][gw] = gone() ? -1.f : __uint_as_float(wtop);
+                    bar_sync(bar_id, 128);
+                    float wm = 0.f;
 #pragma unroll
-                        for (int o = 16; o >= 1; o >>= 1)
-                            wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-                        if (lane == 0)
-                            s_wred[grp][gw] = gone() ? -1.f : wm;
-                        bar_sync(bar_id, 128);
+                    for (int w = 0; w < 4; ++w) {
+                        leave = leave || s_wred[grp][w] < 0.f;
+                        wm = fmaxf(wm, s_wred[grp][w]);
+                    }
+                    level = fmaxf(level, kv_scale_level(wm));
+                    if (gtid < NR) {
+                        const float old = first ? -INFINITY : -s_nm[grp][nmb][gtid];
+                        const float m = fmaxf(fmaxf(fmaxf(s_red[grp][0][gtid], s_red[grp][1][gtid]),
+                                                    fmaxf(s_red[grp][2][gtid], s_red[grp][3][gtid])) + level, old);
+                        s_nm[grp][nmb ^ 1][gtid] = -m;
+                        s_c[grp][gtid] = old == -INFINITY ? 0.f : ex2(old - m);
+                    }
+                    bar_sync(bar_id, 128);
+                    nmb ^= 1;
+                    if (!first) {
+                        kv_wait(pv_done + 8u * grp, ((it >> 1) - 1) & 1, dead);
+                        tc_fence_after();
+                        const uint32_t a = tmem + t_lane + TM_O + (uint32_t)((u & 1) * 2 + grp) * KF_N;
+                        kf_tmem_ld<NR>(a, acc);
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            leave = leave || s_wred[grp][w] < 0.f;
-                            wm = fmaxf(wm, s_wred[grp][w]);
+                        for (int j = 0; j < NR / 2; ++j) {
+                            const f32x2 c2 = pack2(s_c[grp][2 * j], s_c[grp][2 * j + 1]);
+                            l2[j] = mul2(l2[j], c2);
+                            if constexpr (!L::I8)
+                                off2[j] = mul2(off2[j], c2);
+                            float x, y;
+                            unpack2(mul2(pack2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1])), c2), x, y);
+                            acc[2 * j] = __float_as_uint(x);
+                            acc[2 * j + 1] = __float_as_uint(y);
                         }
-                        level = fmaxf(level, kv_scale_level(wm));
-                        if (gtid < KF_N) {
-                            const float old = first ? -INFINITY : -s_nm[grp][nmb][gtid];
-                            const float m = fmaxf(fmaxf(fmaxf(s_red[grp][0][gtid], s_red[grp][1][gtid]),
-                                                        fmaxf(s_red[grp][2][gtid], s_red[grp][3][gtid])) + level, old);
-                            s_nm[grp][nmb ^ 1][gtid] = -m;
-                            s_c[grp][gtid] = old == -INFINITY ? 0.f : ex2(old - m);
-                        }
-                        bar_sync(bar_id, 128);
-                        nmb ^= 1;
-                        if (!first) {
-                            kv_wait(pv_done + 8u * grp, ((it >> 1) - 1) & 1, dead);
-                            tc_fence_after();
-                            const uint32_t a = tmem + t_lane + TM_O + (uint32_t)((u & 1) * 2 + grp) * KF_N;
-                            tmem_ld16(a, acc);
-#pragma unroll
-                            for (int j = 0; j < KF_N; ++j) {
-                                const float c = s_c[grp][j];
-                                l[j] *= c;
-                                if constexpr (!L::I8)
-                                    sum_off[j] *= c;
-                                acc[j] = __float_as_uint(__uint_as_float(acc[j]) * c);
-                            }
-                            tmem_st16(a, acc);
-                            tmem_wait_st();
-                        }
+                        kf_tmem_st<NR>(a, acc);
                     }
                 }
                 first = false;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(s_free + 8u * grp);
+#pragma unroll
+                for (int j = 0; j < NR / 2; ++j) {
+                    l2[j] = add2(l2[j], x2[j]);
+                    if constexpr (!L::I8)
+                        off2[j] = fma2(x2[j], pack2(info.w, info.w), off2[j]);
+                }
                 if (it >= 2)                               // the group's last P has been read
                     kv_wait(pv_done + 8u * grp, ((it >> 1) - 1) & 1, dead);
-                // P^T: row n, tokens in 64-token sub-tiles of 16 x 128 bytes
+                if constexpr (NR == 4)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p_dst), "r"(h[0]), "r"(h[1]) : "memory");
 #pragma unroll
-                for (int j = 0; j < KF_N; j += 2) {
-                    const float p0 = ex2(s[j]), p1 = ex2(s[j + 1]);
-                    l[j] += p0;
-                    l[j + 1] += p1;
-                    if constexpr (!L::I8) {
-                        sum_off[j] = fmaf(p0, info.w, sum_off[j]);
-                        sum_off[j + 1] = fmaf(p1, info.w, sum_off[j + 1]);
-                    }
-                    const __half2 h = __floats2half2_rn(p0 * info.z, p1 * info.z);
-                    const uint32_t hb = *reinterpret_cast<const uint32_t *>(&h);
-                    sts16(p_dst + j * 128u + (ch ^ ((uint32_t)(j & 7) << 4)), hb);
-                    sts16(p_dst + (j + 1) * 128u + (ch ^ ((uint32_t)((j + 1) & 7) << 4)), hb >> 16);
-                }
-                tc_fence_before();
+                for (int j = 0; j < NR / 8; ++j)
+                    sts128(p_dst + 2048u * j, h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0)
@@ -533,15 +582,22 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                 kv_wait(o_empty + 8u * (u & 1), ((u >> 1) - 1) & 1, dead);
             KfSums &sums = s_sums[u & 1][grp];
             {
+                float z[NR];
                 int idx;
-                const float x = warp_sum_transpose<KF_N>(l, lane, idx);
+#pragma unroll
+                for (int j = 0; j < NR / 2; ++j)
+                    unpack2(l2[j], z[2 * j], z[2 * j + 1]);
+                const float x = warp_sum_transpose<NR>(z, lane, idx);
                 sums.l[gw][idx] = x;                       // lanes of one idx hold one value
                 if constexpr (!L::I8) {
-                    const float y = warp_sum_transpose<KF_N>(sum_off, lane, idx);
+#pragma unroll
+                    for (int j = 0; j < NR / 2; ++j)
+                        unpack2(off2[j], z[2 * j], z[2 * j + 1]);
+                    const float y = warp_sum_transpose<NR>(z, lane, idx);
                     sums.off[gw][idx] = y;
                 }
             }
-            if (gw == 0 && lane < KF_N)
+            if (gw == 0 && lane < NR)
                 sums.m[lane] = first ? -INFINITY : -s_nm[grp][nmb][lane];
             if (gw == 0 && lane == 0)
                 sums.any = !first;
@@ -549,7 +605,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             if (lane == 0)
                 mbar_arrive(sums_full + 8u * (u & 1));
         }
-    } else {
+    } else if (warp < KF_Q) {
         // --------------------------------------------- the results of a unit
         const int quad = warp & 3;
         const int tok = quad * 32 + lane;                  // TMEM lane: a column of O^T
@@ -563,12 +619,12 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             unit_wait(u);
             kv_wait(sums_full + 8u * (u & 1), (u >> 1) & 1, dead);
             kv_wait(o_full + 8u * (u & 1), (u >> 1) & 1, dead);
-            if (bar_or(3, 128, gone()))              // leave together
+            if (bar_or(3, 128, gone()))                    // leave together
                 break;
             const KvUnit un = s_unit[u & (KT_UNITS - 1)];
             done += un.k1 - un.k0;
             tc_fence_after();
-            if (t < KF_N) {
+            if (t < NR) {
                 const KfSums &a = s_sums[u & 1][0], &b = s_sums[u & 1][1];
                 const float m = fmaxf(a.m[t], b.m[t]);
                 const float ca = a.m[t] == -INFINITY ? 0.f : ex2(a.m[t] - m);
@@ -586,12 +642,12 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             for (int g = 0; g < 2; ++g) {
                 if (!s_sums[u & 1][g].any)
                     continue;
-                uint32_t v[KF_N];
-                tmem_ld16(tmem + t_lane + TM_O + (uint32_t)((u & 1) * 2 + g) * KF_N, v);
+                uint32_t v[NR];
+                kf_tmem_ld<NR>(tmem + t_lane + TM_O + (uint32_t)((u & 1) * 2 + g) * KF_N, v);
                 const bool add = g == 1 && s_sums[u & 1][0].any;
                 if (tok < D) {
 #pragma unroll
-                    for (int j = 0; j < KF_N; ++j) {
+                    for (int j = 0; j < NR; ++j) {
                         float *o = s_o + j * D + d;
                         *o = fmaf(__uint_as_float(v[j]), s_e[g][j], add ? *o : s_e[2][j]);
                     }
@@ -626,32 +682,27 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == KF_MMA_S) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");
     }
 }
 
 template <int FMT, int D>
-static KvKernel kf_describe(const DeviceInfo &dev, int seqs)
+static KvKernel kf_describe(const DeviceInfo &dev, int rows)
 {
     KvKernel k = {};
-    k.fn = reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D>);
+    k.fn = rows <= 4   ? reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 4>)
+           : rows <= 8 ? reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 8>)
+                       : reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 16>);
     k.tile = KF_N;
     k.threads = KF_WARPS * 32;
     // 1024: alignment; 8192: static arrays and the CTA's reserve
     const size_t budget = dev.smem_optin - 1024 - 8192;
-    for (k.stages = KT_MAX_STAGES; k.stages > 1 && kf_smem<FMT, D>(k.stages, seqs).total > budget;)
+    for (k.stages = KT_MAX_STAGES; k.stages > 1 && kf_smem<FMT, D>(k.stages).total > budget;)
         --k.stages;
-    k.smem = kf_smem<FMT, D>(k.stages, seqs).total + 1024;
+    k.smem = kf_smem<FMT, D>(k.stages).total + 1024;
     return k;
-}
-
-KvKernel kv_few_kernel(const DeviceInfo &dev, int format, int head_dim, int seqs)
-{
-    if (format == Q4_CACHE_INT8)
-        return head_dim == 64 ? kf_describe<Q4_CACHE_INT8, 64>(dev, seqs) : kf_describe<Q4_CACHE_INT8, 128>(dev, seqs);
-    return head_dim == 64 ? kf_describe<Q4_CACHE_INT4, 64>(dev, seqs) : kf_describe<Q4_CACHE_INT4, 128>(dev, seqs);
 }
 
 }  // namespace q4

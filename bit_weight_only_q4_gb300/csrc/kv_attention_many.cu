@@ -32,13 +32,13 @@ struct KmScales {
     float ks[KT_TOKENS], km[KT_TOKENS], vs[KT_TOKENS], vm[KT_TOKENS];
 };
 
-// Shared memory: [raw ring][K: 2][V: 2][token scales: 4][results: 2 KB a softmax warp][lengths]
+// Shared memory: [raw ring][K: 2][V: 2][token scales: 4][results: 2 KB a softmax warp]
 struct KmSmem {
-    uint32_t k, v, scales, stage, len, total;
+    uint32_t k, v, scales, stage, total;
 };
 
 template <int FMT, int D>
-__host__ __device__ inline KmSmem km_smem(int stages, int seqs)
+__host__ __device__ inline KmSmem km_smem(int stages)
 {
     KmSmem s = {};
     uint32_t at = (uint32_t)stages * KT_BLOCKS * KvLayout<FMT, D>::BLOCK;
@@ -47,44 +47,8 @@ __host__ __device__ inline KmSmem km_smem(int stages, int seqs)
     s.v = at, at += 2u * KT_TOKENS * D * 2;
     s.scales = at, at += 4u * (uint32_t)sizeof(KmScales);
     s.stage = at, at += 8u * 2048;
-    s.len = at, at += ((uint32_t)seqs * 4u + 15u) & ~15u;
     s.total = at;
     return s;
-}
-
-// Pairs of fp32 in one 64-bit register: one instruction for two operations.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(float a, float b)
-{
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
-{
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ void lds_f32x4(uint32_t a, f32x2 &x, f32x2 &y)
-{
-    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
 }
 
 template <int FMT, int D>
@@ -103,11 +67,10 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
     __shared__ int s_last, s_dead;
     const int NS = p.stages;
-    const KmSmem off = km_smem<FMT, D>(NS, p.seqs);
+    const KmSmem off = km_smem<FMT, D>(NS);
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = smem_u32(smem);
     KmScales *s_scales = reinterpret_cast<KmScales *>(smem + off.scales);
-    int *s_len = reinterpret_cast<int *>(smem + off.len);
     // exchanged between a row's two threads, where the results go later
     uint32_t (*s_top)[KM_ROWS] = reinterpret_cast<uint32_t (*)[KM_ROWS]>(smem + off.stage);
     float (*s_qs)[KM_ROWS] = reinterpret_cast<float (*)[KM_ROWS]>(smem + off.stage + 1024);
@@ -119,35 +82,33 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     const uint32_t k_full = raw_empty + 8u * KT_MAX_STAGES, k_done = k_full + 16, v_full = k_full + 32,
                    v_done = k_full + 48, s_full = k_full + 64, s_free = k_full + 80, p_full = k_full + 96,
                    pv_done = k_full + 112, q_full = k_full + 128, unit_full = k_full + 136;
-    if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(raw_full + 8u * i, 1);
-            mbar_init(raw_empty + 8u * i, 8);              // K and V warps
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(k_full + 8u * i, 4);                 // K, V: by buffer
-            mbar_init(k_done + 8u * i, 1);
-            mbar_init(v_full + 8u * i, 4);
-            mbar_init(v_done + 8u * i, 1);
-            mbar_init(s_full + 8u * i, 1);                 // S, P, O: by half
-            mbar_init(s_free + 8u * i, 4);
-            mbar_init(p_full + 8u * i, 4);
-            mbar_init(pv_done + 8u * i, 1);
-        }
-        mbar_init(q_full, 8);
-        for (int i = 0; i < KT_UNITS; ++i)
-            mbar_init(unit_full + 8u * i, 1);
+    if (warp == KM_COPY) {
+        kv_init_bars(raw_full, NS, 1);
+        kv_init_bars(raw_empty, NS, 8);                    // K and V warps
+        kv_init_bars(k_full, 2, 4);                        // K, V: by buffer
+        kv_init_bars(k_done, 2, 1);
+        kv_init_bars(v_full, 2, 4);
+        kv_init_bars(v_done, 2, 1);
+        kv_init_bars(s_full, 2, 1);                        // S, P, O: by half
+        kv_init_bars(s_free, 2, 4);
+        kv_init_bars(p_full, 2, 4);
+        kv_init_bars(pv_done, 2, 1);
+        kv_init_bars(q_full, 1, 8);
+        kv_init_bars(unit_full, KT_UNITS, 1);
+        if (lane == 0)
+            s_dead = 0;
         mbar_init_fence();
-        s_dead = 0;
-    }
-    if (warp == KM_S) {
+    } else if (warp == KM_S) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&s_tmem)), "n"(TM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait();
-    const KvShare sh = kv_share<KM_ROWS, KM_WARPS>(p, s_len);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     const uint32_t tmem = s_tmem;
+    pdl_wait();
+    const KvShare sh = kv_share<KM_ROWS>(p);
     const KvDead dead = {p.err, &s_dead};
     auto gone = [&]() { return *dead.flag != 0; };
     auto unit_wait = [&](int u) { kv_wait(unit_full + 8u * (u & (KT_UNITS - 1)), (u / KT_UNITS) & 1, dead); };
@@ -233,7 +194,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                     qs = s_qs[0][row] + s_qs[1][row];
                 }
             }
-            const int lim = mine ? kv_row_limit(p, grow0 + row, s_len[un.b]) : 0x7fffffff;
+            const int lim = mine ? kv_row_limit(p, grow0 + row, un.len) : 0x7fffffff;
             const int least = __reduce_min_sync(0xffffffffu, lim);
             float m = -INFINITY, level = -36.f;            // reference; E - 6
             f32x2 l2 = 0ull, l2b = 0ull, off2 = 0ull, off2b = 0ull;        // (two chains each)
@@ -535,7 +496,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                     out.km[tok] = sc.y;
                     out.vm[tok] = sc.w;
                 }
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.z));
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(sc.z)));
                 if (lane == 0)
                     s_wmax[i & 3][warp & 3] = __uint_as_float(top);
                 if (warp == KM_K && lane == 0)
@@ -554,7 +515,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KM_REGS_OTHERS));
         if (warp == KM_COPY) {
-            kv_copy_warp<FMT, D, KM_ROWS>(p, sh, s_len, s_unit, unit_full, sm, s_valid, raw_full, raw_empty, dead);
+            kv_copy_warp<FMT, D, KM_ROWS>(p, sh, s_unit, unit_full, sm, s_valid, raw_full, raw_empty, dead);
         } else if (warp == KM_S) {
         // ------------------------------------------------------ MMAs: S = q' K^T
         constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(KM_HALF >> 3) << 17) | (8u << 24);       // f16, f32 sums, M = 128
@@ -638,7 +599,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
 }
 
 template <int FMT, int D>
-static KvKernel km_describe(const DeviceInfo &dev, int seqs)
+static KvKernel km_describe(const DeviceInfo &dev)
 {
     KvKernel k = {};
     k.fn = reinterpret_cast<const void *>(&kv_many_rows_kernel<FMT, D>);
@@ -646,17 +607,17 @@ static KvKernel km_describe(const DeviceInfo &dev, int seqs)
     k.threads = KM_WARPS * 32;
     // 1024: alignment; 4096: static arrays and the CTA's reserve
     const size_t budget = dev.smem_optin - 1024 - 4096;
-    for (k.stages = KT_MAX_STAGES; k.stages > 1 && km_smem<FMT, D>(k.stages, seqs).total > budget;)
+    for (k.stages = KT_MAX_STAGES; k.stages > 1 && km_smem<FMT, D>(k.stages).total > budget;)
         --k.stages;
-    k.smem = km_smem<FMT, D>(k.stages, seqs).total + 1024;
+    k.smem = km_smem<FMT, D>(k.stages).total + 1024;
     return k;
 }
 
-KvKernel kv_many_kernel(const DeviceInfo &dev, int format, int head_dim, int seqs)
+KvKernel kv_many_kernel(const DeviceInfo &dev, int format, int head_dim)
 {
     if (format == Q4_CACHE_INT8)
-        return head_dim == 64 ? km_describe<Q4_CACHE_INT8, 64>(dev, seqs) : km_describe<Q4_CACHE_INT8, 128>(dev, seqs);
-    return head_dim == 64 ? km_describe<Q4_CACHE_INT4, 64>(dev, seqs) : km_describe<Q4_CACHE_INT4, 128>(dev, seqs);
+        return head_dim == 64 ? km_describe<Q4_CACHE_INT8, 64>(dev) : km_describe<Q4_CACHE_INT8, 128>(dev);
+    return head_dim == 64 ? km_describe<Q4_CACHE_INT4, 64>(dev) : km_describe<Q4_CACHE_INT4, 128>(dev);
 }
 
 }  // namespace q4

@@ -338,9 +338,17 @@ def q4_linear_int8(x, qweight, scale, y=None, stream=None):
 
 
 # ------------------------------------------------------------ paged K/V cache
+# Bytes that 16 tokens of one head take, by (format, head_dim): 32 code rows, 32 scales.
+_KV_BLOCK = {(CACHE_INT8, 64): 32 * (64 + 2), (CACHE_INT8, 128): 32 * (128 + 2),
+             (CACHE_INT4, 64): 32 * (32 + 4), (CACHE_INT4, 128): 32 * (64 + 4)}
+# The handle of a device's current stream without building a Stream object around it:
+# these calls take a few microseconds on the GPU, and building one takes three.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def kv_block_bytes(fmt: int, head_dim: int) -> int:
-    """Bytes that 16 tokens of one head take in a cache of the given format."""
-    return int(load().q4_kv_block_bytes(fmt, head_dim))
+    """Bytes that 16 tokens of one head take in a cache of the given format (0: no such cache)."""
+    return _KV_BLOCK.get((fmt, head_dim), 0)
 
 
 def alloc_kv_cache(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim: int,
@@ -354,59 +362,86 @@ def alloc_kv_cache(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim
                        device=device or "cuda")
 
 
+def _kv_stream(stream, t):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
+def _on(stream):
+    """Allocations made inside belong to the stream that the call runs on, so that neither
+    their fill nor their reuse by the allocator overlaps the call."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _kv_empty(shape, like, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    with _on(stream):
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+
+
 def _kv_cache(cache, fmt, head_dim):
     """(format, pages, page_size, kv_heads, head_dim) of a cache tensor."""
-    _cuda(cache, "cache", torch.uint8)
-    n = kv_block_bytes(fmt, head_dim)
-    if cache.dim() != 4 or n == 0 or cache.shape[3] != n:
+    n = _KV_BLOCK.get((fmt, head_dim), 0)
+    if not (cache.is_cuda and cache.is_contiguous() and cache.dtype is torch.uint8):
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor")
+    shape = cache.shape
+    if n == 0 or len(shape) != 4 or shape[3] != n:
         raise ValueError(f"cache must be [pages, kv_heads, page_size / 16, {n}] for format {fmt} "
-                         f"and head_dim {head_dim}, got {tuple(cache.shape)}")
-    return fmt, cache.shape[0], 16 * cache.shape[2], cache.shape[1], head_dim
+                         f"and head_dim {head_dim}, got {tuple(shape)}")
+    return fmt, shape[0], 16 * shape[2], shape[1], head_dim
 
 
-def _rows(t, name, dims):
-    """A bf16 CUDA tensor [..., heads, D] whose tokens are evenly spaced and whose heads
-    lie side by side (a slice of a fused q|k|v projection does); its token stride."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+def _kv_ints(t, name, dims):
+    """An int32 CUDA tensor of the given number of dimensions: its shape."""
+    if not (t.is_cuda and t.is_contiguous() and t.dtype is torch.int32 and t.dim() == dims):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {dims} dimension(s)")
+    return t.shape
+
+
+def _kv_rows(t, name, shape):
+    """A bf16 CUDA tensor [..., heads, D] whose tokens are evenly spaced and whose heads lie
+    side by side (a slice of a fused q|k|v projection does): the token stride."""
+    if not (t.is_cuda and t.dtype is torch.bfloat16):
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    heads, D = t.shape[-2:]
-    row = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if dims == 4 else heads * D)
-    if dims == 4 and t.shape[0] == 1 and t.shape[1] == 1:
+    strides = t.stride()
+    heads, D = shape[-2:]
+    row, even = strides[-3], True
+    if len(shape) == 4:
+        if shape[1] == 1:
+            row = strides[0]
+        even = shape[0] == 1 or strides[0] == shape[1] * row
+        if shape[0] == 1 and shape[1] == 1:
+            row = heads * D
+    elif shape[0] == 1:
         row = heads * D
-    even = dims == 3 or t.shape[0] == 1 or t.stride(0) == t.shape[1] * row
-    if not even or t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != D):
+    if not even or strides[-1] != 1 or (heads > 1 and strides[-2] != D):
         raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, got "
-                         f"strides {tuple(t.stride())}")
+                         f"strides {strides}")
     return row
-
-
-def _table(table, lengths, batch=None):
-    _cuda(table, "page_table", torch.int32)
-    _cuda(lengths, "lengths", torch.int32)
-    if table.dim() != 2 or lengths.dim() != 1 or lengths.shape[0] != table.shape[0]:
-        raise ValueError("page_table must be [batch, width] and lengths [batch]")
-    if batch is not None and table.shape[0] != batch:
-        raise ValueError(f"page_table has {table.shape[0]} sequences, q has {batch}")
 
 
 def q4_kv_write(k, v, cache, slots, fmt, stream=None):
     """Quantise K and V rows (bf16 [tokens, kv_heads, D]) into the cache's slots
     (int32 [tokens]; slot = page * page_size + token in the page, negative: left out)."""
-    ks, vs = _rows(k, "k", 3), _rows(v, "v", 3)
-    if k.shape != v.shape:
-        raise ValueError(f"k and v must have one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
-    _cuda(slots, "slots", torch.int32)
-    if slots.numel() != k.shape[0]:
+    shape = k.shape
+    if len(shape) != 3 or shape != v.shape:
+        raise ValueError(f"k and v must be [tokens, kv_heads, D], got {tuple(shape)} and {tuple(v.shape)}")
+    ks, vs = _kv_rows(k, "k", shape), _kv_rows(v, "v", shape)
+    if _kv_ints(slots, "slots", 1)[0] != shape[0]:
         raise ValueError("slots must hold one slot for each token")
-    geo = _kv_cache(cache, fmt, k.shape[2])
-    if geo[3] != k.shape[1]:
-        raise ValueError(f"the cache holds {geo[3]} heads, k has {k.shape[1]}")
-    if k.shape[0] == 0:
+    geo = _kv_cache(cache, fmt, shape[2])
+    if geo[3] != shape[1]:
+        raise ValueError(f"the cache holds {geo[3]} heads, k has {shape[1]}")
+    if shape[0] == 0:
         return cache
-    _check(load().q4_kv_write(_ptr(k), ks, _ptr(v), vs, _ptr(slots), k.shape[0], _ptr(cache), *geo,
-                              _stream(stream)))
+    status = (_lib or load()).q4_kv_write(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), shape[0],
+                                          cache.data_ptr(), *geo, _kv_stream(stream, k))
+    if status:
+        _check(status)
     return cache
 
 
@@ -414,20 +449,25 @@ def q4_kv_read(cache, page_table, lengths, max_len, head_dim, fmt, k=None, v=Non
     """(k, v) bf16 [batch, max_len, kv_heads, head_dim] of the first lengths[b] cached tokens
     of each sequence, zeros behind them."""
     geo = _kv_cache(cache, fmt, head_dim)
-    _table(page_table, lengths)
-    shape = (page_table.shape[0], max_len, geo[3], head_dim)
-    with _on(stream):
-        if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    for t, name in ((k, "k"), (v, "v")):
-        if tuple(_cuda(t, name, torch.bfloat16).shape) != shape:
-            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    if k.numel() == 0:
+    batch, width = _kv_ints(page_table, "page_table", 2)
+    if _kv_ints(lengths, "lengths", 1)[0] != batch:
+        raise ValueError("page_table must be [batch, width] and lengths [batch]")
+    shape = (batch, max_len, geo[3], head_dim)
+    if k is None:
+        k = _kv_empty(shape, cache, stream)
+    elif tuple(_cuda(k, "k", torch.bfloat16).shape) != shape:
+        raise ValueError(f"k must be {shape}, got {tuple(k.shape)}")
+    if v is None:
+        v = _kv_empty(shape, cache, stream)
+    elif tuple(_cuda(v, "v", torch.bfloat16).shape) != shape:
+        raise ValueError(f"v must be {shape}, got {tuple(v.shape)}")
+    if batch * max_len == 0:
         return k, v
-    _check(load().q4_kv_read(_ptr(cache), *geo, _ptr(page_table), page_table.shape[1], _ptr(lengths),
-                             shape[0], max_len, _ptr(k), _ptr(v), _stream(stream)))
+    status = (_lib or load()).q4_kv_read(cache.data_ptr(), *geo, page_table.data_ptr(), width,
+                                         lengths.data_ptr(), batch, max_len, k.data_ptr(), v.data_ptr(),
+                                         _kv_stream(stream, cache))
+    if status:
+        _check(status)
     return k, v
 
 
@@ -436,58 +476,57 @@ def kv_attention_workspace_bytes(fmt, kv_heads, head_dim, batch, tokens, q_heads
                                                       q_heads, prefix_len))
 
 
-def _on(stream):
-    """Allocations made inside belong to the stream that the call runs on, so that neither
-    their fill nor their reuse by the allocator overlaps the call."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
-
-
-def _kv_workspace(geo, q, prefix_len, stream):
+def _kv_workspace(key, q, stream):
     """As _default_workspace: one per device, stream and call shape, zero-filled once."""
-    fmt, _, _, heads, D = geo
-    B, T, Hq, _ = q.shape
-    key = (q.device.index, _stream(stream), "kv", fmt, heads, D, B, T, Hq, prefix_len)
-    ws = _ws_cache.get(key)
-    if ws is None:
-        n = kv_attention_workspace_bytes(fmt, heads, D, B, T, Hq, prefix_len)
-        if n == 0:
-            return None
-        if len(_ws_cache) >= 64:
-            _ws_cache.clear()
+    n = kv_attention_workspace_bytes(*key[3:])
+    if n == 0:
+        return None
+    if len(_ws_cache) >= 64:
+        _ws_cache.clear()
+    if stream is None:
+        ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
+    else:
         with _on(stream):
             ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
-        _ws_cache[key] = ws
+    _ws_cache[key] = ws
     return ws
 
 
-def _kv_attention(q, cache, prefix, page_table, lengths, fmt, scale, out, workspace, stream):
-    row = _rows(q, "q", 4)
-    B, T, Hq, D = q.shape
+def _kv_attention(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, scale, out, workspace,
+                  stream):
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must be [batch, tokens, q_heads, D], got {tuple(shape)}")
+    row = _kv_rows(q, "q", shape)
+    B, T, Hq, D = shape
     geo = _kv_cache(cache, fmt, D)
-    _table(page_table, lengths, B)
+    batch, width = _kv_ints(page_table, "page_table", 2)
+    if batch != B or _kv_ints(lengths, "lengths", 1)[0] != B:
+        raise ValueError(f"page_table must be [batch, width] and lengths [batch], q has {B} sequences")
     if out is None:
-        with _on(stream):
-            out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    elif tuple(_cuda(out, "out", torch.bfloat16).shape) != (B, T, Hq, D):
-        raise ValueError(f"out must be {(B, T, Hq, D)}, got {tuple(out.shape)}")
-    if out.numel() == 0:
+        out = _kv_empty(shape, q, stream)
+    elif _cuda(out, "out", torch.bfloat16).shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    if B * T * Hq == 0:
         return out
-    prefix_len = prefix[1] if prefix else 0
+    handle = _kv_stream(stream, q)
     if workspace is None:
-        workspace = _kv_workspace(geo, q, prefix_len, stream)
+        key = (q.get_device(), handle, "kv", fmt, geo[3], D, B, T, Hq, prefix_len)
+        workspace = _ws_cache.get(key)
+        if workspace is None:
+            workspace = _kv_workspace(key, q, stream)
     wp, wn = _ws_args(workspace)
     s = D ** -0.5 if scale is None else float(scale)
-    tail = (_ptr(page_table), page_table.shape[1], _ptr(lengths), B, T, Hq, s, _ptr(out), wp, wn,
-            _stream(stream))
-    if prefix:
-        _check(load().q4_kv_attention_shared(_ptr(q), row, _ptr(cache), *geo, _ptr(prefix[0]),
-                                             prefix_len, *tail))
+    lib = _lib or load()
+    if prefix_pages is not None:
+        status = lib.q4_kv_attention_shared(q.data_ptr(), row, cache.data_ptr(), *geo, prefix_pages.data_ptr(),
+                                            prefix_len, page_table.data_ptr(), width, lengths.data_ptr(), B, T,
+                                            Hq, s, out.data_ptr(), wp, wn, handle)
     else:
-        _check(load().q4_kv_attention(_ptr(q), row, _ptr(cache), *geo, *tail))
+        status = lib.q4_kv_attention(q.data_ptr(), row, cache.data_ptr(), *geo, page_table.data_ptr(), width,
+                                     lengths.data_ptr(), B, T, Hq, s, out.data_ptr(), wp, wn, handle)
+    if status:
+        _check(status)
     return out
 
 
@@ -496,7 +535,7 @@ def q4_kv_attention(q, cache, page_table, lengths, fmt, scale=None, out=None, wo
     """out [batch, tokens, q_heads, D] (bf16) = softmax(scale q K^T) V over the cached tokens of
     each sequence; the query tokens q (bf16, same shape) are the sequence's last ones.
     scale: D ** -0.5 if None; lengths int32 [batch], page_table int32 [batch, width]."""
-    return _kv_attention(q, cache, None, page_table, lengths, fmt, scale, out, workspace, stream)
+    return _kv_attention(q, cache, None, 0, page_table, lengths, fmt, scale, out, workspace, stream)
 
 
 def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, scale=None,
@@ -504,10 +543,9 @@ def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengt
     """As q4_kv_attention where every sequence begins with the prefix_len tokens of the pages
     prefix_pages (int32): they are read and multiplied once for the whole batch.  page_table and
     lengths describe each sequence's own tokens behind them."""
-    _cuda(prefix_pages, "prefix_pages", torch.int32)
+    n = _kv_ints(prefix_pages, "prefix_pages", 1)[0]
     page = 16 * cache.shape[2]
-    if prefix_len < 1 or prefix_pages.numel() * page < prefix_len:
-        raise ValueError(f"prefix_pages holds {prefix_pages.numel()} pages of {page}, the prefix has "
-                         f"{prefix_len} tokens")
-    return _kv_attention(q, cache, (prefix_pages, prefix_len), page_table, lengths, fmt, scale, out,
+    if prefix_len < 1 or n * page < prefix_len:
+        raise ValueError(f"prefix_pages holds {n} pages of {page}, the prefix has {prefix_len} tokens")
+    return _kv_attention(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, scale, out,
                          workspace, stream)

@@ -21,7 +21,7 @@ def lib():
 def test_block_bytes(lib):
     for fmt in (0, 1):
         for D in (64, 128):
-            assert lib.q4_kv_block_bytes(fmt, D) == R.block_bytes(fmt, D)
+            assert lib.q4_kv_block_bytes(fmt, D) == R.block_bytes(fmt, D) == q4.kv_block_bytes(fmt, D)
     assert lib.q4_kv_block_bytes(2, 64) == 0
     assert lib.q4_kv_block_bytes(0, 96) == 0
     assert lib.q4_kv_block_bytes(1, 0) == 0
