@@ -179,24 +179,33 @@ __device__ __forceinline__ bool elect_one()
 struct KvDead {
     unsigned *err;
     volatile int *flag;
+    uint32_t flag_at;            // its shared-memory address
 };
 
-// Bounded wait of a whole warp, every lane polling: a phase that is complete costs 57
-// cycles so, and 252 with one lane polling for the others.  The loop is kept rolled, and
-// the callers' code does not depend on the outcome: these kernels wait in some twenty
-// places, and their roles' loops have to stay in the instruction cache together.
+// Bounded wait of a whole warp, every lane polling (a phase that is complete costs some 15
+// cycles so, and more with one lane polling for the others; waiting warps do not slow
+// each other).  Written as one block, for the roles' loops wait in some twenty places
+// and have to stay short: the usual way through is two instructions.
 __device__ __forceinline__ void kv_wait(uint32_t bar, uint32_t parity, const KvDead &dead)
 {
-    uint32_t n = 0;
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (++n == kMbarSpinLimit) {
-            atomicOr(dead.err, kErrBarrierTimeout);
-            *dead.flag = 1;
-        }
-        if (*dead.flag)
-            break;
-    }
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n, d;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+                 "@p bra KV_DONE_%=;\n\t"
+                 "mov.u32 n, 0;\n"
+                 "KV_POLL_%=:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+                 "@p bra KV_DONE_%=;\n\t"
+                 "ld.volatile.shared.u32 d, [%2];\n\t"
+                 "setp.ne.u32 p, d, 0;\n\t"
+                 "@p bra KV_DONE_%=;\n\t"
+                 "add.u32 n, n, 1;\n\t"
+                 "setp.lt.u32 p, n, %4;\n\t"
+                 "@p bra KV_POLL_%=;\n\t"
+                 "st.volatile.shared.u32 [%2], 1;\n\t"
+                 "red.global.or.b32 [%3], %5;\n"
+                 "KV_DONE_%=:\n\t}"
+                 ::"r"(bar), "r"(parity), "r"(dead.flag_at), "l"(dead.err), "n"(kMbarSpinLimit), "n"(kErrBarrierTimeout)
+                 : "memory");
     __syncwarp();
 }
 
@@ -304,8 +313,8 @@ __device__ __forceinline__ float4 kv_scales(uint32_t blk, int r)
     return s;
 }
 
-// Where a thread finds its token's row of codes in a staged tile, computed once: the row's
-// 16-byte pieces lie at `base` plus the offsets of `piece` (see KvLayout).
+// Where a thread finds its token's row of codes in a staged tile, computed once: its 16-byte
+// pieces lie at `base` plus the offsets of `piece` (see KvLayout).
 template <int FMT, int D>
 struct KvRowAt {
     using L = KvLayout<FMT, D>;
@@ -322,26 +331,26 @@ struct KvRowAt {
     }
 };
 
-// A token's row of fp16 values in a tile of 128 tokens: 64-column halves of 128 rows x 128
-// bytes, 128-byte swizzle.  As an MMA operand that is K-major with tokens as rows and M- or
-// N-major with tokens as K.
+// Where the token's row of fp16 values goes in a tile of 128 tokens: 64-column halves of 128
+// rows x 128 bytes, 128-byte swizzle.  As an MMA operand that is K-major with tokens as rows
+// and M- or N-major with tokens as K.
 struct KvRowTo {
-    uint32_t base, chunk[8];
+    uint32_t at[8];              // chunks of 8 columns (chunk c + 8 is 16 KB behind chunk c)
     __device__ __forceinline__ explicit KvRowTo(int tok)
     {
-        base = (uint32_t)tok * 128u;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            chunk[j] = (uint32_t)((j ^ tok) & 7) << 4;
+            at[j] = (uint32_t)tok * 128u + ((uint32_t)((j ^ tok) & 7) << 4);
     }
 };
 
 template <int FMT, int D>
-__device__ __forceinline__ void kv_row_to_tile(uint32_t codes, const KvRowAt<FMT, D> &from, uint32_t tile, const KvRowTo &to)
+__device__ __forceinline__ void kv_row_to_tile(uint32_t codes, const KvRowAt<FMT, D> &from, uint32_t tile,
+                                               const KvRowTo &to)
 {
     using L = KvLayout<FMT, D>;
     constexpr int OUT = L::I8 ? 2 : 4;             // 8-column chunks of a piece
-    const uint32_t src = codes + from.base, dst = tile + to.base;
+    const uint32_t src = codes + from.base;
 #pragma unroll
     for (int j = 0; j < KvRowAt<FMT, D>::PIECES; ++j) {
         const uint4 c = lds128(src + from.piece[j]);
@@ -351,7 +360,7 @@ __device__ __forceinline__ void kv_row_to_tile(uint32_t codes, const KvRowAt<FMT
             uint32_t v[4];
             kv_decode8<L::I8>(L::I8 ? w[2 * x] : w[x], L::I8 ? w[2 * x + 1] : 0u, v);
             const int ch = OUT * j + x;
-            sts128(dst + to.chunk[ch & 7] + (uint32_t)(ch >> 3) * (KT_TOKENS * 128u), v[0], v[1], v[2], v[3]);
+            sts128(tile + to.at[ch & 7] + (uint32_t)(ch >> 3) * (KT_TOKENS * 128u), v[0], v[1], v[2], v[3]);
         }
     }
 }
@@ -498,7 +507,9 @@ __device__ __forceinline__ KvUnit kv_next_unit(const KvTileParams &p, KvWalk &w,
 
 // The copying warp: walks the list, describes each unit to the other warps (slot
 // u % KT_UNITS, barrier unit_full), and copies the blocks of each tile into the ring
-// (one 1-D bulk copy per block of 16 tokens of one head: codes and scales together).
+// (a block is 16 tokens of one head, codes and scales together; the blocks of a page follow
+// one another and take one 1-D bulk copy: an SM starts one in some 120 cycles, so that
+// single int4 blocks of 2,176 bytes arrive at 5.2 TB/s at most, runs of 8 at 7.1).
 // Pages are looked up for four tiles of a unit at once, a block per lane, while the four
 // before them are being copied: a look-up takes about as long as the copy of a tile.
 // s_valid[stage] says which blocks of the tile there are.
@@ -523,6 +534,8 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
     int k = 0, k1 = 0, u = 0, ntok = 0, head = 0;
     const int32_t *table = p.table;
     int page = -1, at_block = 0, at_head = 0, n = 0;       // lane's block of the next tiles, and how many those are
+    const int run = p.cache.blocks < KT_BLOCKS ? p.cache.blocks : KT_BLOCKS;     // blocks of a copy
+    const bool starts = (lane & (run - 1)) == 0;
     int s = 0, issued = 0;
     uint32_t round = 1u;                           // parity of the slot's previous release
 #pragma unroll 1
@@ -568,8 +581,9 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
                 mbar_arrive_expect_tx(raw_full + 8u * s, (uint32_t)__popc(blocks) * L::BLOCK);
             }
             __syncwarp();
-            if (from && (lane >> 3) == j)
-                bulk_copy_g2s(ring + (uint32_t)s * RAW + (uint32_t)(lane & 7) * L::BLOCK, from, L::BLOCK, raw_full + 8u * s);
+            if (from && starts && (lane >> 3) == j)        // (a run's missing blocks are its last)
+                bulk_copy_g2s(ring + (uint32_t)s * RAW + (uint32_t)(lane & 7) * L::BLOCK, from,
+                              (uint32_t)__popc((blocks >> (lane & 7)) & ((1u << run) - 1u)) * L::BLOCK, raw_full + 8u * s);
             issued = i + 1;
             if (++s == NS)
                 s = 0, round ^= 1u;

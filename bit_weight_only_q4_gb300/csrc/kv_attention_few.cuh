@@ -11,7 +11,7 @@
 // = 4, 8 or 16, the least that holds the rows, are ever computed.
 //
 // One CTA per SM, 24 warps: one copies blocks, two issue the MMAs, one loads queries;
-// four decode K, four V; two groups of four take the tiles' softmax in turn, each with
+// four decode K, four V (a thread a token); two groups of four take the tiles' softmax in turn, each with
 // references, sums and an accumulator of its own; four put the two together at the end of
 // a unit and store, while the others are at the next one.  A tile's MMAs take some 660
 // cycles (D = 128), its decoding and softmax some 2,500 warp instructions.
@@ -22,7 +22,7 @@
 namespace q4 {
 
 constexpr int KF_N = 16;
-constexpr int KF_COPY = 0, KF_MMA_S = 1, KF_K = 2, KF_V = 6, KF_S = 10, KF_E = 18, KF_Q = 22, KF_MMA_O = 23,
+constexpr int KF_COPY = 0, KF_MMA_S = 1, KF_Q = 2, KF_MMA_O = 3, KF_K = 4, KF_V = 8, KF_S = 12, KF_E = 20,
               KF_WARPS = 24;
 constexpr int KF_ROW_SLOTS = 8;                    // units whose rows are described at a time
 
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     const uint32_t tmem = s_tmem;
     pdl_wait();
     const KvShare sh = kv_share<KF_N>(p);
-    const KvDead dead = {p.err, &s_dead};
+    const KvDead dead = {p.err, &s_dead, smem_u32(&s_dead)};
     auto gone = [&]() { return *dead.flag != 0; };
     // unit u of this CTA, once it has been described
     auto unit_wait = [&](int u) { kv_wait(unit_full + 8u * (u & (KT_UNITS - 1)), (u / KT_UNITS) & 1, dead); };
@@ -244,87 +244,6 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             }
             __syncwarp();
             begun |= 1u << g;
-        }
-    } else if (warp < KF_V) {
-        // ------------------------------------------- K: codes to tensor memory
-        const int tok = (warp & 3) * 32 + lane;            // TMEM lane
-        const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
-        const int r = tok & (KV_BLOCK - 1);
-        const KvRowAt<FMT, D> from(tok);
-        int k = 0, k1 = 0, ntok = 0, u = 0, s = 0;
-        uint32_t round = 0u;                               // parity of the ring's round
-#pragma unroll 1
-        for (int i = 0; i < sh.tiles && !gone(); ++i, ++k) {
-            if (k == k1) {
-                unit_wait(u);
-                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-                k = un.k0, k1 = un.k1, ntok = un.ntok;
-                ++u;
-            }
-            kv_wait(raw_full + 8u * s, round, dead);
-            if (i >= 2)
-                kv_wait(s_full + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
-            tc_fence_after();
-            const uint32_t raw = sm + (uint32_t)s * RAW;
-            // blocks of the tile that are there and hold tokens; bit 8: all of them do, wholly
-            uint32_t mask = s_valid[s];
-            if (mask == 0xffu && (k + 1) * KT_TOKENS <= ntok)
-                mask |= 0x100u;
-            const bool here = ((mask >> (tok / KV_BLOCK)) & 1u) && k * KT_TOKENS + tok < ntok;
-            s_info[(i & 3) * KT_TOKENS + tok] =
-                here ? kv_scales<FMT, D>(raw + (uint32_t)(tok / KV_BLOCK) * L::BLOCK, r) : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (warp == KF_K && lane == 0)
-                s_vmask[i & 3] = mask;
-            const uint32_t src = raw + from.base, dst = tmem + t_lane + (uint32_t)(i & 1) * (D / 2);
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {             // 32 columns: 16 packed
-                uint32_t v[4][4];
-                if constexpr (L::I8) {
-                    const uint4 a = lds128(src + from.piece[2 * j]), b = lds128(src + from.piece[2 * j + 1]);
-                    kv_decode8<true>(a.x, a.y, v[0]);
-                    kv_decode8<true>(a.z, a.w, v[1]);
-                    kv_decode8<true>(b.x, b.y, v[2]);
-                    kv_decode8<true>(b.z, b.w, v[3]);
-                } else {
-                    const uint4 a = lds128(src + from.piece[j]);
-                    kv_decode8<false>(a.x, 0u, v[0]);
-                    kv_decode8<false>(a.y, 0u, v[1]);
-                    kv_decode8<false>(a.z, 0u, v[2]);
-                    kv_decode8<false>(a.w, 0u, v[3]);
-                }
-                tmem_st16(dst + 16u * j, reinterpret_cast<const uint32_t(&)[16]>(v));
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(k_full + 8u * (i & 1));
-                mbar_arrive(raw_empty + 8u * s);
-            }
-            if (++s == NS)
-                s = 0, round ^= 1u;
-        }
-    } else if (warp < KF_S) {
-        // ------------------------------------------- V: fp16 to shared memory
-        const int tok = (warp - KF_V) * 32 + lane;
-        const KvRowAt<FMT, D> from(tok);
-        const KvRowTo to(tok);
-        int s = 0;
-        uint32_t round = 0u;
-#pragma unroll 1
-        for (int i = 0; i < sh.tiles && !gone(); ++i) {
-            kv_wait(raw_full + 8u * s, round, dead);
-            if (i >= 2)
-                kv_wait(pv_done + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
-            kv_row_to_tile<FMT, D>(sm + (uint32_t)s * RAW + L::V_CODES, from, sm + off.v + (uint32_t)(i & 1) * V_BYTES, to);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(v_full + 8u * (i & 1));
-                mbar_arrive(raw_empty + 8u * s);
-            }
-            if (++s == NS)
-                s = 0, round ^= 1u;
         }
     } else if (warp == KF_Q) {
         // ----------------------------------------- q: prescaled fp16, row data
@@ -408,6 +327,87 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(q_full + 8u * (u & 1));
+        }
+    } else if (warp < KF_V) {
+        // ------------------------------------------- K: codes to tensor memory
+        const int tok = (warp & 3) * 32 + lane;            // TMEM lane
+        const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
+        const int r = tok & (KV_BLOCK - 1);
+        const KvRowAt<FMT, D> from(tok);
+        int k = 0, k1 = 0, ntok = 0, u = 0, s = 0;
+        uint32_t round = 0u;                               // parity of the ring's round
+#pragma unroll 1
+        for (int i = 0; i < sh.tiles && !gone(); ++i, ++k) {
+            if (k == k1) {
+                unit_wait(u);
+                const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
+                k = un.k0, k1 = un.k1, ntok = un.ntok;
+                ++u;
+            }
+            kv_wait(raw_full + 8u * s, round, dead);
+            if (i >= 2)
+                kv_wait(s_full + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
+            tc_fence_after();
+            const uint32_t raw = sm + (uint32_t)s * RAW;
+            // blocks of the tile that are there and hold tokens; bit 8: all of them do, wholly
+            uint32_t mask = s_valid[s];
+            if (mask == 0xffu && (k + 1) * KT_TOKENS <= ntok)
+                mask |= 0x100u;
+            const bool here = ((mask >> (tok / KV_BLOCK)) & 1u) && k * KT_TOKENS + tok < ntok;
+            s_info[(i & 3) * KT_TOKENS + tok] = here ? kv_scales<FMT, D>(raw + (uint32_t)(tok / KV_BLOCK) * L::BLOCK, r)
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (warp == KF_K && lane == 0)
+                s_vmask[i & 3] = mask;
+            const uint32_t src = raw + from.base, dst = tmem + t_lane + (uint32_t)(i & 1) * (D / 2);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {             // 32 columns: 16 packed
+                uint32_t v[4][4];
+                if constexpr (L::I8) {
+                    const uint4 a = lds128(src + from.piece[2 * j]), b = lds128(src + from.piece[2 * j + 1]);
+                    kv_decode8<true>(a.x, a.y, v[0]);
+                    kv_decode8<true>(a.z, a.w, v[1]);
+                    kv_decode8<true>(b.x, b.y, v[2]);
+                    kv_decode8<true>(b.z, b.w, v[3]);
+                } else {
+                    const uint4 a = lds128(src + from.piece[j]);
+                    kv_decode8<false>(a.x, 0u, v[0]);
+                    kv_decode8<false>(a.y, 0u, v[1]);
+                    kv_decode8<false>(a.z, 0u, v[2]);
+                    kv_decode8<false>(a.w, 0u, v[3]);
+                }
+                tmem_st16(dst + 16u * j, reinterpret_cast<const uint32_t(&)[16]>(v));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(k_full + 8u * (i & 1));
+                mbar_arrive(raw_empty + 8u * s);
+            }
+            if (++s == NS)
+                s = 0, round ^= 1u;
+        }
+    } else if (warp < KF_S) {
+        // ------------------------------------------- V: fp16 to shared memory
+        const int tok = (warp & 3) * 32 + lane;
+        const KvRowAt<FMT, D> from(tok);
+        const KvRowTo to(tok);
+        int s = 0;
+        uint32_t round = 0u;
+#pragma unroll 1
+        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+            kv_wait(raw_full + 8u * s, round, dead);
+            if (i >= 2)
+                kv_wait(pv_done + 8u * (i & 1), ((i >> 1) - 1) & 1, dead);
+            kv_row_to_tile<FMT, D>(sm + (uint32_t)s * RAW + L::V_CODES, from, sm + off.v + (uint32_t)(i & 1) * V_BYTES, to);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(v_full + 8u * (i & 1));
+                mbar_arrive(raw_empty + 8u * s);
+            }
+            if (++s == NS)
+                s = 0, round ^= 1u;
         }
     } else if (warp < KF_E) {
         // --------------------------------------------------- softmax of a tile
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             if (lane == 0)
                 mbar_arrive(sums_full + 8u * (u & 1));
         }
-    } else if (warp < KF_Q) {
+    } else {
         // --------------------------------------------- the results of a unit
         const int quad = warp & 3;
         const int tok = quad * 32 + lane;                  // TMEM lane: a column of O^T

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     const uint32_t tmem = s_tmem;
     pdl_wait();
     const KvShare sh = kv_share<KM_ROWS>(p);
-    const KvDead dead = {p.err, &s_dead};
+    const KvDead dead = {p.err, &s_dead, smem_u32(&s_dead)};
     auto gone = [&]() { return *dead.flag != 0; };
     auto unit_wait = [&](int u) { kv_wait(unit_full + 8u * (u & (KT_UNITS - 1)), (u / KT_UNITS) & 1, dead); };
 
