@@ -89,6 +89,23 @@ size_t kv_attention_workspace_bytes(const DeviceInfo &dev, const KvCacheDesc &c,
 q4_status launch_kv_attention(const DeviceInfo &dev, const KvCacheDesc &c, const KvAttnArgs &a, cudaStream_t st,
                               bool pdl);
 
+// Division of 0 <= n < 2^31 by a divisor that a whole launch shares: with 2^s >= d and
+// f = ceil(2^(31 + s) / d) < 2^32 the error of n f / 2^(31 + s) stays below 1 / d.
+struct KvDivisor {
+    uint32_t f, s;
+    __host__ __device__ KvDivisor() : f(0), s(0) {}
+    __host__ explicit KvDivisor(uint32_t d) : s(0)
+    {
+        while ((1u << s) < d)
+            ++s;
+        f = (uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return (int)(((uint64_t)(uint32_t)n * f) >> (31 + s));
+    }
+};
+
 // What the kernels know of a cache.
 struct KvCache {
     uint8_t *data;

@@ -141,8 +141,8 @@ q4_status q4_kv_read(const uint8_t *cache, int format, int pages, int page_size,
     if (batch < 1 || max_len < 1 || table_width < 1)
         return fail(Q4_ERR_SHAPE, "batch=%d, max_len=%d and table_width=%d must be >= 1", batch, max_len,
                     table_width);
-    if (((int64_t)max_len + 15) / 16 * batch > kMaxBlocks)
-        return fail(Q4_ERR_SHAPE, "batch * max_len is too large");
+    if (((int64_t)max_len + 15) / 16 * batch > kMaxBlocks / kv_heads)
+        return fail(Q4_ERR_SHAPE, "batch * max_len * kv_heads is too large");
     if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(table, 4) || !aligned_to(lengths, 4))
         return fail(Q4_ERR_ALIGN, "k and v must be 16-byte, table and lengths 4-byte aligned");
     DeviceInfo dev;
