@@ -113,11 +113,11 @@ struct KvCache {
     int page_shift;            // log2(page_size)
     int blocks;                // page_size / 16
 
-    // First byte of the block that holds token `slot` (slot = page * page_size +
-    // token within the page) of head h.  64-bit: a cache may exceed 2^32 bytes.
+    // First byte of block blk of a page, of head h.  The number of blocks fits in 31 bits (a
+    // check of the host's), their bytes do not.
     __device__ __forceinline__ const uint8_t *block(int page, int blk, int h, int block_bytes) const
     {
-        return data + (((int64_t)page * heads + h) * blocks + blk) * block_bytes;
+        return data + (uint64_t)(uint32_t)((page * heads + h) * blocks + blk) * (uint32_t)block_bytes;
     }
 };
 

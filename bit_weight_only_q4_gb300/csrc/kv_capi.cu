@@ -6,6 +6,8 @@ namespace q4 {
 
 static bool aligned_to(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+constexpr int64_t kMaxBlocks = 0x7fffffff;
+
 static int log2_exact(int v)
 {
     int s = 0;
@@ -29,6 +31,8 @@ static q4_status kv_describe(const uint8_t *cache, int format, int pages, int pa
     const int shift = page_size >= 16 && page_size <= 1024 ? log2_exact(page_size) : -1;
     if (shift < 0)
         return fail(Q4_ERR_SHAPE, "page_size must be a power of two from 16 to 1024 (got %d)", page_size);
+    if ((int64_t)pages * kv_heads > kMaxBlocks >> (shift - 4))
+        return fail(Q4_ERR_SHAPE, "the cache has more than 2^31 - 1 blocks of 16 tokens and a head");
     if (!aligned_to(cache, 16))
         return fail(Q4_ERR_ALIGN, "cache must be 16-byte aligned");
     d = KvCacheDesc{const_cast<uint8_t *>(cache), format, pages, shift, kv_heads, head_dim};
@@ -36,8 +40,6 @@ static q4_status kv_describe(const uint8_t *cache, int format, int pages, int pa
 }
 
 static bool pdl_on() { return (q4_get_launch_flags() & Q4_FLAG_PDL) != 0; }
-
-constexpr int64_t kMaxBlocks = 0x7fffffff;
 
 static q4_status kv_attention(const void *q, int64_t q_stride, const uint8_t *cache, int format, int pages,
                               int page_size, int kv_heads, int head_dim, const int32_t *prefix_pages,

@@ -48,6 +48,13 @@ __device__ __forceinline__ uint32_t min2_bf16(uint32_t a, uint32_t b)
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// 1 / x to within 2^-22 of itself (x normal).
+__device__ __forceinline__ float rcp_near(float x)
+{
+    float d;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+    return d;
+}
 __device__ __forceinline__ float bf16_of(const uint32_t (&e)[8], int j)
 {
     return (j & 1) ? __uint_as_float(e[j / 2] & 0xffff0000u) : bf16_bits_to_f32(e[j / 2] & 0xffffu);
@@ -56,12 +63,15 @@ __device__ __forceinline__ float bf16_of(const uint32_t (&e)[8], int j)
 // Quantises 16 values of a row (bf16 pairs e; the row's other threads are the lanes that
 // differ in the low bits) and stores codes and, by thread 0 of the row, scales.
 //
-// The codes are those of IEEE divisions, found with a multiplication by r = 1 / s:
+// The codes are those of IEEE divisions, found with a multiplication by r, which is 1 / s to
+// within 2^-22 of itself:
 // int8   x has 8 significant bits and s has 11 (S < 2048 in units of its last bit), so x / s
 //        is a half-integer or at least 1 / (2 S) > 2^-12 away from every one.  x r is within
-//        127 * 2^-24 of x / s; rounded to a multiple of 2^-12 (by adding 1.5 * 2^11) it
+//        127 * 2^-22 < 2^-14 of x / s; rounded to a multiple of 2^-12 (by adding 1.5 * 2^11) it
 //        is the half-integer where x / s is one, and on the right side of it elsewhere, so the
-//        second rounding, to an integer, ends where rint(x / s) does.
+//        second rounding, to an integer, ends where rint(x / s) does.  In the same way amax / 127
+//        is 2^-19 of itself or more away from every value halfway between two of fp16, so that a
+//        product with 1 / 127 rounds to the fp16 that the quotient does.
 // int4   x - m may have all 24 bits.  n = rint((x - m) r) is right if |(x - m) - n s| < s / 2,
 //        which one fused operation judges exactly; else (a tie, or a quotient within an error
 //        of one) the thread's codes are computed again with divisions.
@@ -85,9 +95,9 @@ __device__ __forceinline__ void kv_quantise(const uint32_t (&e)[8], uint8_t *cod
         if (!store)
             return;
         const bool bad = top >= 0x7f80u;                   // an infinity or a NaN
-        const __half s16 = __float2half_rn(fminf(__fdiv_rn(bf16_bits_to_f32(top), 127.f), 65504.f));
+        const __half s16 = __float2half_rn(fminf(__fmul_rn(bf16_bits_to_f32(top), 1.f / 127.f), 65504.f));
         const float s = __half2float(s16);
-        const float rs = s > 0.f && !bad ? __frcp_rn(s) : 0.f;
+        const float rs = s > 0.f ? rcp_near(s) : 0.f;
         const bool cut = s < 0x1p-14f || s == 65504.f;
         uint32_t w[4];
 #pragma unroll
@@ -95,7 +105,7 @@ __device__ __forceinline__ void kv_quantise(const uint32_t (&e)[8], uint8_t *cod
             float u[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                u[j] = __fadd_rn(__fmaf_rn(bad ? 0.f : bf16_of(e, 4 * g + j), rs, 0x1.8p11f), 0x1.8p23f - 0x1.8p11f);
+                u[j] = __fadd_rn(__fmaf_rn(bf16_of(e, 4 * g + j), rs, 0x1.8p11f), 0x1.8p23f - 0x1.8p11f);
             if (cut)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -103,6 +113,8 @@ __device__ __forceinline__ void kv_quantise(const uint32_t (&e)[8], uint8_t *cod
             w[g] = __byte_perm(__byte_perm(__float_as_uint(u[0]), __float_as_uint(u[1]), 0x0040),
                                __byte_perm(__float_as_uint(u[2]), __float_as_uint(u[3]), 0x0040), 0x5410);
         }
+        if (bad)
+            w[0] = w[1] = w[2] = w[3] = 0u;
         *reinterpret_cast<uint2 *>(codes + L::place(r, piece * 8)) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2 *>(codes + L::place(r, D / 2 + piece * 8)) = make_uint2(w[2], w[3]);
         if (piece == 0)
@@ -128,7 +140,7 @@ __device__ __forceinline__ void kv_quantise(const uint32_t (&e)[8], uint8_t *cod
         const float s = __half2float(s16), m = __half2float(m16);
         uint32_t w[2] = {0u, 0u};
         if (s > 0.f && !bad) {
-            const float rs = __frcp_rn(s);
+            const float rs = rcp_near(s);
             float off = 0.f;                               // largest |(x - m) - n s|
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
