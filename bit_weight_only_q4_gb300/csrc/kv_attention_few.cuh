@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         }
     } else if (warp == KF_Q) {
         // ----------------------------------------- q: prescaled fp16, row data
+        // (of the first NR rows: a column of S^T or O^T takes nothing from another one's q)
         int done = 0;
 #pragma unroll 1
         for (int u = 0; done < sh.tiles; ++u) {
@@ -264,16 +265,16 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             constexpr int LPR = D / 8;                     // lanes of a row, 8 columns each
             constexpr int RPP = 32 / LPR;                  // rows of a step
             const int sub = lane % LPR;
-            uint4 v[KF_N / RPP];
+            uint4 v[NR / RPP];
 #pragma unroll
-            for (int j = 0; j < KF_N / RPP; ++j) {
+            for (int j = 0; j < NR / RPP; ++j) {
                 const int n = lane / LPR + j * RPP;
                 v[j] = n < nrows ? __ldg(reinterpret_cast<const uint4 *>(kv_q_row(p, grow0 + n, un.h, D)) + sub)
                                  : make_uint4(0u, 0u, 0u, 0u);
             }
             uint32_t top = 0u;                             // largest finite |q| of the tile
 #pragma unroll
-            for (int j = 0; j < KF_N / RPP; ++j) {
+            for (int j = 0; j < NR / RPP; ++j) {
                 const uint32_t e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             ex = ex > 126 ? 126 : ex;
             const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
 #pragma unroll
-            for (int j = 0; j < KF_N / RPP; ++j) {
+            for (int j = 0; j < NR / RPP; ++j) {
                 const int n = lane / LPR + j * RPP;
                 const uint32_t e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
                 float x[8], sum = 0.f;
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                 }
             }
             int least = 0x7fffffff;
-            if (lane < KF_N) {                             // rows that fill the tile up: no limit, never stored
+            if (lane < NR) {                               // rows that fill the tile up: no limit, never stored
                 least = lane < nrows ? kv_row_limit(p, grow0 + lane, un.len) : 0x7fffffff;
                 rows.lim[lane] = least;
             }
