@@ -516,7 +516,8 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
     int64_t f = sh.c0;
     int k = 0, k1 = 0, u = 0, ntok = 0, head = 0;
     const int32_t *table = p.table;
-    int page = -1, at_block = 0, at_head = 0, n = 0;       // lane's block of the next tiles, and how many those are
+    int page = 0, at_block = 0, at_head = 0, n = 0;        // lane's block of the next tiles, and how many those are
+    bool has = false;                              // (not judged by before it is used: the load is on its way)
     const int run = p.cache.blocks < KT_BLOCKS ? p.cache.blocks : KT_BLOCKS;     // blocks of a copy
     const bool starts = (lane & (run - 1)) == 0;
     int s = 0, issued = 0;
@@ -525,9 +526,9 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
     for (int i = 0; i < sh.tiles && !*dead.flag;) {
         // the blocks looked up in the last round
         const uint8_t *from = nullptr;
-        if (page >= 0 && page < p.cache.pages)
+        if (has && page >= 0 && page < p.cache.pages)
             from = p.cache.block(page, at_block, at_head, L::BLOCK);
-        else if (page != -1)
+        else if (has)
             atomicOr(p.err, kErrIndex);
         const unsigned valid = __ballot_sync(0xffffffffu, from != nullptr);
         const int m = n;
@@ -545,12 +546,9 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
         }
         n = k1 - k < 4 ? k1 - k : 4;
         const int pos = k * KT_TOKENS + lane * KV_BLOCK;
-        page = -1;
-        if (lane < n * KT_BLOCKS && pos < ntok) {
+        has = lane < n * KT_BLOCKS && pos < ntok;
+        if (has)
             page = __ldg(table + (pos >> p.cache.page_shift));
-            if (page == -1)                        // (an invalid id as any other)
-                page = -2;
-        }
         at_block = (pos & ((1 << p.cache.page_shift) - 1)) / KV_BLOCK;
         at_head = head;
         k += n;
