@@ -159,11 +159,15 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     pdl_wait();
     const KvShare sh = kv_share<KF_N>(p);
     const KvDead dead = {p.err, &s_dead, smem_u32(&s_dead)};
     auto gone = [&]() { return *dead.flag != 0; };
+    // The warps that issue MMAs branch on values that are known to be the warp's, so that
+    // descriptors can be kept in uniform registers.
+    auto gone_all = [&]() { return __any_sync(0xffffffffu, *dead.flag != 0); };
+    const int tiles = __shfl_sync(0xffffffffu, sh.tiles, 0);
     // unit u of this CTA, once it has been described
     auto unit_wait = [&](int u) { kv_wait(unit_full + 8u * (u & (KT_UNITS - 1)), (u / KT_UNITS) & 1, dead); };
 
@@ -174,12 +178,12 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(KF_N >> 3) << 17) | (8u << 24);    // f16, f32 sums, M = 128
         int u = -1, left = 0;
 #pragma unroll 1
-        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+        for (int i = 0; i < tiles && !gone_all(); ++i) {
             if (left == 0) {
                 ++u;
                 unit_wait(u);
                 const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-                left = un.k1 - un.k0;
+                left = __shfl_sync(0xffffffffu, un.k1 - un.k0, 0);
                 kv_wait(q_full + 8u * (u & 1), (u >> 1) & 1, dead);
             }
             --left;
@@ -212,13 +216,13 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         int u = -1, left = 0;
         uint32_t begun = 0u;                               // groups that have begun the unit
 #pragma unroll 1
-        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+        for (int i = 0; i < tiles && !gone_all(); ++i) {
             const int g = i & 1;
             if (left == 0) {
                 ++u;
                 unit_wait(u);
                 const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-                left = un.k1 - un.k0;
+                left = __shfl_sync(0xffffffffu, un.k1 - un.k0, 0);
                 begun = 0u;
                 if (u >= 2)                                // its accumulators have been read
                     kv_wait(o_empty + 8u * (u & 1), ((u >> 1) - 1) & 1, dead);
