@@ -16,8 +16,8 @@
 // [2^14, 2^15); f undoes it.  p vs enters the second product in fp16 (11 bits).  The
 // reference m_i is the largest score so far plus E - 6, with 2^E the power of two below
 // the largest vs so far: the largest p vs is then about 2^6.  It moves (and what has been
-// summed is rescaled) only when that exceeds it by more than 8, so products stay below
-// 2^15 and keep their 11 bits down to 2^-20 of the largest.  Scores, statistics and sums
+// summed is rescaled) only when that exceeds it by more than 8, so products stay in the
+// range of fp16 and keep their 11 bits down to 2^-20 of the largest.  Scores, statistics and sums
 // are fp32; pieces of a row are added up by their references, whatever those are.
 // A row of the cache whose V scale is not finite counts as one whose K scale is NaN: it
 // poisons the query rows that see it and, being kept out of the V operand, no others.
@@ -627,8 +627,8 @@ __device__ __forceinline__ int64_t kv_piece_slot(const KvUnit &un)
 }
 
 // The piece is written: if it is the unit's last to arrive, join all of them in order and
-// store the rows.  Called by NT threads that meet at barrier `bar`.
-template <int D, int TILE, int NT>
+// store the rows.  Called by NT threads that meet at barrier `bar`, with IT items a thread in flight.
+template <int D, int TILE, int NT, int IT>
 __device__ __forceinline__ void kv_join(const KvTileParams &p, const KvShare &sh, const KvUnit &un, int nrows, int grow0,
                                         int *s_last, int t, int bar)
 {
@@ -647,10 +647,9 @@ __device__ __forceinline__ void kv_join(const KvTileParams &p, const KvShare &sh
     if (!*s_last)
         return;
     __threadfence();
-    // Four items (four columns of a row) at a time, two pieces of each: the loads are what
+    // IT items (four columns of a row) at a time, two pieces of each: the loads are what
     // this takes, and they have to be in flight together.  Piece j lies in slot
     // 2 (first + j), the first one in the slot behind.
-    constexpr int IT = 4;
     const int total = nrows * (D / 4);
 #pragma unroll 1
     for (int item = t; item < total; item += NT * IT) {

@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                     *reinterpret_cast<float2 *>(p.piece_ml + (slot + n) * 2) = s_ml[n];
             }
             if (!whole)
-                kv_join<D, KF_N, 128>(p, sh, un, nrows, grow0, &s_last, t, 3);
+                kv_join<D, KF_N, 128, 4>(p, sh, un, nrows, grow0, &s_last, t, 3);
             bar_sync(3, 128);                              // s_o, s_ml and s_e may be written again
         }
     }

@@ -106,11 +106,15 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     pdl_wait();
     const KvShare sh = kv_share<KM_ROWS>(p);
     const KvDead dead = {p.err, &s_dead, smem_u32(&s_dead)};
     auto gone = [&]() { return *dead.flag != 0; };
+    // The warps that issue MMAs branch on values that are known to be the warp's, so that
+    // descriptors can be kept in uniform registers.
+    auto gone_all = [&]() { return __any_sync(0xffffffffu, *dead.flag != 0); };
+    const int tiles = __shfl_sync(0xffffffffu, sh.tiles, 0);
     auto unit_wait = [&](int u) { kv_wait(unit_full + 8u * (u & (KT_UNITS - 1)), (u / KT_UNITS) & 1, dead); };
 
     if (warp < KM_K) {
@@ -229,12 +233,11 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                 const bool masked = !(mask & 0x100u) || pos0 + KM_HALF > least;
                 uint32_t ph[KM_HALF / 2];
                 // With every token seen and every reference set, go by the references as they are;
-                // if some product then reaches 2^15, go again the careful way.
+                // if some product may then be out of range, go again the careful way.
                 bool careful = masked || __any_sync(0xffffffffu, m == -INFINITY);
                 if (!careful) {
                     const f32x2 n2 = pack2(-m, -m);
                     f32x2 la = 0ull, lb = 0ull, oa = 0ull, ob = 0ull;
-                    uint32_t high[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                     for (int j = 0; j < KM_HALF; j += 4) {
                         f32x2 ka, kb, va, vb;
@@ -271,11 +274,12 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                         const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
                         ph[j / 2] = *reinterpret_cast<const uint32_t *>(&h0);
                         ph[j / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
-                        high[(j / 2) & 3] = __vmaxu2(high[(j / 2) & 3], ph[j / 2]);
-                        high[(j / 2 + 1) & 3] = __vmaxu2(high[(j / 2 + 1) & 3], ph[j / 2 + 1]);
                     }
-                    const uint32_t hi = __vmaxu2(__vmaxu2(high[0], high[1]), __vmaxu2(high[2], high[3]));
-                    careful = __any_sync(0xffffffffu, (hi & 0xffffu) >= 0x7800u || hi >= 0x78000000u);
+                    // (no p vs is above the sum of p times the largest vs)
+                    float sa, sb;
+                    unpack2(add2(la, lb), sa, sb);
+                    const float wm = fmaxf(s_wmax[i & 3][2 * g], s_wmax[i & 3][2 * g + 1]);
+                    careful = __any_sync(0xffffffffu, !((sa + sb) * wm < 65000.f));
                     if (!careful) {
                         l2 = add2(l2, la);
                         l2b = add2(l2b, lb);
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
             if (!whole && !leave) {
                 if (mine && g == 0)
                     *reinterpret_cast<float2 *>(p.piece_ml + (slot + row) * 2) = make_float2(r.m, r.l);
-                kv_join<D, KM_ROWS, 256>(p, sh, un, nrows, grow0, &s_last, t, 1);
+                kv_join<D, KM_ROWS, 256, 4>(p, sh, un, nrows, grow0, &s_last, t, 1);
             }
             tc_fence_before();
             bar_sync(1, 256);                              // O and s_sum may be written again
@@ -521,12 +525,12 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
         constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(KM_HALF >> 3) << 17) | (8u << 24);       // f16, f32 sums, M = 128
         int u = -1, left = 0;
 #pragma unroll 1
-        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+        for (int i = 0; i < tiles && !gone_all(); ++i) {
             if (left == 0) {
                 ++u;
                 unit_wait(u);
                 const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-                left = un.k1 - un.k0;
+                left = __shfl_sync(0xffffffffu, un.k1 - un.k0, 0);
                 kv_wait(q_full, u & 1, dead);
             }
             --left;
@@ -557,13 +561,13 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
         constexpr uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);   // B is N-major
         int u = -1, left = 0;
 #pragma unroll 1
-        for (int i = 0; i < sh.tiles && !gone(); ++i) {
+        for (int i = 0; i < tiles && !gone_all(); ++i) {
             const bool first = left == 0;
             if (first) {
                 ++u;
                 unit_wait(u);
                 const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
-                left = un.k1 - un.k0;
+                left = __shfl_sync(0xffffffffu, un.k1 - un.k0, 0);
             }
             --left;
             kv_wait(v_full + 8u * (i & 1), (i >> 1) & 1, dead);
