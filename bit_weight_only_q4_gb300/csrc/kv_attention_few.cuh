@@ -28,10 +28,10 @@ constexpr int KF_ROW_SLOTS = 8;                    // units whose rows are descr
 
 struct KfRows {
     int lim[KF_N];               // tokens that each row sees
-    float qsum[KF_N];            // sum of q' (int4)
-    float f;                     // scale * log2 e over the queries' power of two
+    float f[KF_N];               // scale * log2 e over the row's power of two
+    float qsum[KF_N];            // sum of q' times f (int4)
     int least;                   // fewest tokens that a row sees
-    int pad[2];
+    int pad[3];
 };
 
 // A softmax group's sums of one unit.
@@ -276,25 +276,28 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                 v[j] = n < nrows ? __ldg(reinterpret_cast<const uint4 *>(kv_q_row(p, grow0 + n, un.h, D)) + sub)
                                  : make_uint4(0u, 0u, 0u, 0u);
             }
-            uint32_t top = 0u;                             // largest finite |q| of the tile
 #pragma unroll
             for (int j = 0; j < NR / RPP; ++j) {
+                const int n = lane / LPR + j * RPP;
                 const uint32_t e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                uint32_t top = 0u;                         // largest finite |q| of the row
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint32_t lo = e[x] & 0x7fffu, hi = (e[x] >> 16) & 0x7fffu;
                     top = lo < 0x7f80u && lo > top ? lo : top;
                     top = hi < 0x7f80u && hi > top ? hi : top;
                 }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            int ex = 141 - (int)(top >> 7);                // the largest goes to [2^14, 2^15)
-            ex = ex > 126 ? 126 : ex;
-            const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
 #pragma unroll
-            for (int j = 0; j < NR / RPP; ++j) {
-                const int n = lane / LPR + j * RPP;
-                const uint32_t e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                for (int y = LPR / 2; y >= 1; y >>= 1) {
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, top, y);
+                    top = other > top ? other : top;
+                }
+                int ex = 141 - (int)(top >> 7);            // the largest goes to [2^14, 2^15)
+                ex = ex > 126 ? 126 : ex;
+                const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+                const float f = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+                if (sub == 0)
+                    rows.f[n] = f;
                 float x[8], sum = 0.f;
                 uint32_t o[4];
 #pragma unroll
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                     for (int y = LPR / 2; y >= 1; y >>= 1)
                         sum += __shfl_xor_sync(0xffffffffu, sum, y);
                     if (sub == 0)
-                        rows.qsum[n] = sum;
+                        rows.qsum[n] = sum * f;
                 }
             }
             int least = 0x7fffffff;
@@ -324,10 +327,8 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                 rows.lim[lane] = least;
             }
             least = __reduce_min_sync(0xffffffffu, least);
-            if (lane == 0) {
-                rows.f = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+            if (lane == 0)
                 rows.least = least;
-            }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0)
@@ -455,8 +456,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                 int pos = (k0 + it) * KT_TOKENS + tok;
                 if (masked && (pos >= ntok || !((mask >> (tok / KV_BLOCK)) & 1u)))
                     pos = 0x7fffffff;
-                const float ks = info.x * rows.f;
-                const f32x2 ks2 = pack2(ks, ks), vs2 = pack2(info.z, info.z);
+                const f32x2 ks2 = pack2(info.x, info.x), vs2 = pack2(info.z, info.z);
                 // Products over the references as they are (what = 0).  If one reaches 2^15, or the
                 // unit begins, the group goes round with scores over zero (1), from which the new
                 // references are taken, and then over those (2).
@@ -469,17 +469,17 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                     const uint32_t nm = what == 1 ? zero_at : nm_at + (uint32_t)nmb * (KF_N * 4);
 #pragma unroll
                     for (int j = 0; j < NR / 4; ++j) {
-                        f32x2 na, nb;
+                        f32x2 na, nb, fa, fb;
                         lds_f32x4(nm + 16u * j, na, nb);
+                        lds_f32x4(smem_u32(rows.f) + 16u * j, fa, fb);
                         if constexpr (!L::I8) {
-                            const float km = info.y * rows.f;
                             f32x2 qa, qb;
                             lds_f32x4(smem_u32(rows.qsum) + 16u * j, qa, qb);
-                            na = fma2(pack2(km, km), qa, na);
-                            nb = fma2(pack2(km, km), qb, nb);
+                            na = fma2(pack2(info.y, info.y), qa, na);
+                            nb = fma2(pack2(info.y, info.y), qb, nb);
                         }
-                        x2[2 * j] = fma2(pack2(__uint_as_float(acc[4 * j]), __uint_as_float(acc[4 * j + 1])), ks2, na);
-                        x2[2 * j + 1] = fma2(pack2(__uint_as_float(acc[4 * j + 2]), __uint_as_float(acc[4 * j + 3])), ks2, nb);
+                        x2[2 * j] = fma2(pack2(__uint_as_float(acc[4 * j]), __uint_as_float(acc[4 * j + 1])), mul2(ks2, fa), na);
+                        x2[2 * j + 1] = fma2(pack2(__uint_as_float(acc[4 * j + 2]), __uint_as_float(acc[4 * j + 3])), mul2(ks2, fb), nb);
                     }
                     if (masked) {
 #pragma unroll

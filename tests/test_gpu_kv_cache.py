@@ -370,6 +370,23 @@ def test_scales_of_any_sign(q4, scale, Hq):
     check(out, q, cache, table, [200, 131], 0, float(np.float32(scale)))
 
 
+@pytest.mark.parametrize("T", [1, 9])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_query_rows_of_very_different_size(q4, fmt, T):
+    """Rows of one key head whose sizes lie 2^48 apart: no row takes another one's digits."""
+    rng = np.random.default_rng([14, fmt, T])
+    lens = [300, 140]
+    cache, table, _ = filled(rng, fmt, 64, 2, 16, lens)
+    q = bf16(1.5 * rng.standard_normal((2, T, 4, 64))).float().numpy()
+    q[:, :, 1] *= np.float32(2.0**-48)
+    out = call(q4, q, cache, table, lens, fmt)
+    check(out, q, cache, table, lens, fmt, 0.125)
+    q[:, :, 0] *= np.float32(2.0**48)                       # (one token takes all: any rounding may pick another)
+    out = call(q4, q, cache, table, lens, fmt)[:, :, 1:2]
+    # head 1 alone, as the head of a cache that has only its key head
+    check(out, q[:, :, 1:2], np.ascontiguousarray(cache[:, :1]), table, lens, fmt, 0.125)
+
+
 def test_query_rows_of_a_fused_projection(q4):
     rng = np.random.default_rng(11)
     D, H, Hq, page, lens = 64, 2, 6, 32, [70, 20]
