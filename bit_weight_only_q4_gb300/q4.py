@@ -477,17 +477,17 @@ def kv_attention_workspace_bytes(fmt, kv_heads, head_dim, batch, tokens, q_heads
 
 
 def _kv_workspace(key, q, stream):
-    """As _default_workspace: one per device, stream and call shape, zero-filled once."""
+    """As _default_workspace: one per device, stream and call shape, zero-filled once (and one of
+    its own for a call that is captured before any has made it)."""
     n = kv_attention_workspace_bytes(*key[3:])
     if n == 0:
         return None
+    with _on(stream) if stream is not None else contextlib.nullcontext():
+        ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
+        if torch.cuda.is_current_stream_capturing():
+            return ws                    # its fill is part of the graph, and has not run yet
     if len(_ws_cache) >= 64:
         _ws_cache.clear()
-    if stream is None:
-        ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
-    else:
-        with _on(stream):
-            ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
     _ws_cache[key] = ws
     return ws
 
