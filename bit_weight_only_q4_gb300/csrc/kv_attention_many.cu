@@ -32,6 +32,13 @@ struct KmScales {
     float ks[KT_TOKENS], km[KT_TOKENS], vs[KT_TOKENS], vm[KT_TOKENS];
 };
 
+// What a whole unit's row needs to be stored: its sums become a sum + b (prefix's sum) and go
+// to `at` (elements of the output, or of the prefix's results).
+struct __align__(16) KmRow {
+    float a, b;
+    int64_t at;
+};
+
 // Shared memory: [raw ring][K: 2][V: 2][token scales: 4][results: 2 KB a softmax warp]
 struct KmSmem {
     uint32_t k, v, scales, stage, total;
@@ -63,7 +70,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 17 + KT_UNITS];
     __shared__ KvUnit s_unit[KT_UNITS];
     __shared__ float s_wmax[4][4];                         // largest V scale of 32 tokens
-    __shared__ float2 s_ml[KM_ROWS];
+    __shared__ __align__(16) KmRow s_row[KM_ROWS];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
     __shared__ int s_last, s_dead;
     const int NS = p.stages;
@@ -414,8 +421,30 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
             const float offset = s0.z * c0 + s1.z * c1;
             const bool whole = un.k0 == 0 && un.k1 == un.n;
             const int64_t slot = kv_piece_slot(un) * KM_ROWS;
-            if (g == 0)
-                s_ml[row] = make_float2(r.m, r.l);
+            if (g == 0 && mine && whole) {
+                const int grow = grow0 + row;
+                const int64_t n = (int64_t)un.h * p.all_rows + grow;
+                KmRow w = {1.f, 0.f, n * D};
+                if (p.prefix_len > 0) {                    // a piece for the launch over the sequences' own tokens
+                    *reinterpret_cast<float2 *>(p.prefix_out_ml + n * 2) = make_float2(r.m, r.l);
+                } else {
+                    float l = r.l;
+                    if (p.prefix_in_o) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.prefix_in_ml + n * 2));
+                        const float top = fmaxf(r.m, ml.x);
+                        w.a = r.m == -INFINITY ? 0.f : ex2(r.m - top);
+                        w.b = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+                        l = l * w.a + ml.y * w.b;
+                    }
+                    // a row that sees nothing has l = 0 and gives zeros
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    w.a *= inv;
+                    w.b *= inv;
+                    const int token = p.by_group(grow);
+                    w.at = ((int64_t)token * p.cache.heads * p.group + un.h * p.group + grow - token * p.group) * D;
+                }
+                s_row[row] = w;
+            }
             const bool leave = bar_or(1, 256, gone());     // (s_sum has been read)
             if (warp_rows && !leave) {
                 // 16 columns at a time through the warp's 2 KB of shared memory: written by row,
@@ -438,18 +467,33 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                         sts128(w_at + ((((uint32_t)y) ^ w_key) << 4), __float_as_uint(x[4 * y]), __float_as_uint(x[4 * y + 1]),
                                __float_as_uint(x[4 * y + 2]), __float_as_uint(x[4 * y + 3]));
                     __syncwarp();
-#pragma unroll 1
+#pragma unroll
                     for (int n = lane >> 2; n < 32; n += 8) {
                         const int nn = quad * 32 + n, c = lane & 3;
                         const uint4 v = lds128(st + (uint32_t)n * 64u + (((uint32_t)c ^ ((uint32_t)n >> 1 & 3u)) << 4));
+                        float4 o = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                                               __uint_as_float(v.w));
                         if (nn >= nrows)
                             continue;
-                        const float4 o = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                                                     __uint_as_float(v.w));
-                        if (whole)
-                            kv_store4<D>(p, grow0 + nn, un.h, j / 4 + c, KvRowSum{s_ml[nn].x, s_ml[nn].y, o});
-                        else
+                        if (!whole) {
                             *reinterpret_cast<float4 *>(p.piece_o + (slot + nn) * D + j + 4 * c) = o;
+                            continue;
+                        }
+                        const KmRow w = s_row[nn];
+                        if (p.prefix_len > 0) {
+                            *reinterpret_cast<float4 *>(p.prefix_out_o + w.at + j + 4 * c) = o;
+                            continue;
+                        }
+                        o.x *= w.a, o.y *= w.a, o.z *= w.a, o.w *= w.a;
+                        if (p.prefix_in_o) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(
+                                p.prefix_in_o + ((int64_t)un.h * p.all_rows + grow0 + nn) * D + j + 4 * c));
+                            o.x = fmaf(x.x, w.b, o.x), o.y = fmaf(x.y, w.b, o.y);
+                            o.z = fmaf(x.z, w.b, o.z), o.w = fmaf(x.w, w.b, o.w);
+                        }
+                        *reinterpret_cast<uint2 *>(p.out + w.at + j + 4 * c) =
+                            make_uint2((uint32_t)f32_to_bf16_bits(o.x) | ((uint32_t)f32_to_bf16_bits(o.y) << 16),
+                                       (uint32_t)f32_to_bf16_bits(o.z) | ((uint32_t)f32_to_bf16_bits(o.w) << 16));
                     }
                     __syncwarp();
                 }
@@ -609,8 +653,8 @@ static KvKernel km_describe(const DeviceInfo &dev)
     k.fn = reinterpret_cast<const void *>(&kv_many_rows_kernel<FMT, D>);
     k.tile = KM_ROWS;
     k.threads = KM_WARPS * 32;
-    // 1024: alignment; 4096: static arrays and the CTA's reserve
-    const size_t budget = dev.smem_optin - 1024 - 4096;
+    // 1024: alignment; 6144: static arrays and the CTA's reserve
+    const size_t budget = dev.smem_optin - 1024 - 6144;
     for (k.stages = KT_MAX_STAGES; k.stages > 1 && km_smem<FMT, D>(k.stages).total > budget;)
         --k.stages;
     k.smem = km_smem<FMT, D>(k.stages).total + 1024;
