@@ -17,6 +17,10 @@ static KvPlan kv_plan(const DeviceInfo &dev, const KvCacheDesc &c, int seqs, int
 {
     KvPlan t = {};
     t.rows = rows;
+    // More rows than the few-row kernel's tile of 16: it would read and decode every token once
+    // per 16 rows.  16,384 to 65,536 cached tokens, 8 key heads (us, few / many): 20 or 32 rows
+    // 64 - 92 / 56 - 69 (int8 and int4, heads of 128), 53 - 59 / 43 - 61 (of 64); 48 rows
+    // 73 - 113 / 44 - 72; 64 rows 91 - 175 / 45 - 74.
     if (rows > 16)
         t.k = kv_many_kernel(dev, c.format, c.head_dim);
     else

@@ -15,6 +15,15 @@
 // references, sums and an accumulator of its own; four put the two together at the end of
 // a unit and store, while the others are at the next one.  A tile's MMAs take some 660
 // cycles (D = 128), its decoding and softmax some 2,500 warp instructions.
+//
+// What bounds it.  int8: HBM on long contexts (eight of 131,072 tokens, 8 heads of 128, 4
+// query heads each: 368 us, 5.9 TB/s).  int4, or heads of 64: the decoding warps, whose
+// instructions issue one in some four cycles beside the other roles' (the same in int4: 333 us,
+// 3.4 TB/s; 3,650 warp instructions a tile use 40 to 48% of the issue slots).  Short
+// contexts: the chain of a unit (queries, first references, sums, results), 2.7 us for one
+// tile, partly hidden behind the next unit's (48 streams of 37 to 4,096 tokens: 59 us).
+// Tried and left: 32 warps, with K and V decoded by two groups each, gained 10 to 20% on
+// units of two to four tiles and lost 14% on long ones to spills (64 registers a thread).
 #pragma once
 
 #include "kv_attention.cuh"
@@ -697,6 +706,9 @@ template <int FMT, int D>
 static KvKernel kf_describe(const DeviceInfo &dev, int rows)
 {
     KvKernel k = {};
+    // The softmax's work goes by the columns that are computed.  With all 16 of them for 1, 4 and 8
+    // rows (us, against the least that holds the rows): one stream of 2,047 tokens 18.0 (14.5),
+    // 48 streams 89 (59), eight of 131,071 207 (166).
     k.fn = rows <= 4   ? reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 4>)
            : rows <= 8 ? reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 8>)
                        : reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 16>);

@@ -1,14 +1,19 @@
 // Quantising K and V rows into the paged cache, and reading cached tokens back.
 //
 // Both are pure streams: 4 D bytes of bf16 K and V in, 2 D + 4 (int8) or D + 8
-// (int4) bytes of cache out per token and head, or the reverse.  Every arithmetic
-// step is one IEEE fp32 operation rounded to nearest even, so a row's codes and
-// scales are the same whichever kernel or launch shape wrote them:
+// (int4) bytes of cache out per token and head, or the reverse.  Codes and scales are
+// those of single IEEE fp32 operations rounded to nearest even:
 //   int8   s = fp16(min(amax / 127, 65504)); code = clamp(rint(x / s), -127, 127)
 //   int4   s = fp16(min((hi - lo) / 15, 65504)); m = fp16(clamp(lo, +-65504));
 //          code = clamp(rint((x - m) / s), 0, 15)
 // with code 0 where the fp16 scale is 0.  A row that holds an infinity or a NaN has
 // no such scale; its scale (and min) is stored as NaN, so it reads back as NaN.
+//
+// What bounds them: HBM.  Measured alone in int8, 64,900 tokens of 16 heads of 64 (K and V):
+// writing 66 us (402 MB, 6.1 TB/s; 390 warp instructions per 2 KB of rows keep two of three
+// issue slots busy, with IEEE divisions it was 148 us), reading 64 us; sixteen contexts of
+// 9,000 to 16,384 tokens of 8 heads of 128 read back in 224 us (1.50 GB, 6.7 TB/s).  A
+// step's 48 rows of 16 heads of 128: 2.0 us.
 #include "kv_cache.cuh"
 
 namespace q4 {

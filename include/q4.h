@@ -269,10 +269,10 @@ q4_status q4_quantize_nvfp4(const void *w_bf16, uint8_t *codes, uint8_t *scale_e
  * r & 6 for 64 and (r >> 1) & 2 for 32.
  *
  * Common requirements: head_dim 64 or 128; page_size a power of two, 16 .. 1024;
- * pages, kv_heads >= 1; cache 16-byte aligned.  A slot is page * page_size + token
- * within the page.  Page tables are int32 device arrays: entry j of a sequence's row
- * is the page of its tokens j * page_size and on.  Entries that hold no token are
- * never read.  A token whose page id lies outside 0 .. pages - 1, or whose position
+ * pages, kv_heads >= 1, at most 2^31 - 1 blocks; cache 16-byte aligned.  A slot is
+ * page * page_size + token within the page.  Page tables are int32 device arrays: entry j
+ * of a sequence's row is the page of its tokens j * page_size and on.  Entries that hold
+ * no token are never read.  A token whose page id lies outside 0 .. pages - 1, or whose position
  * lies past the table's width, is left out (read back as zeros, not attended to) and
  * Q4_DEVERR_INDEX is set.  Neither the unused part of a page nor a page outside the
  * tables influences any result.
@@ -290,7 +290,7 @@ size_t q4_kv_block_bytes(int format, int head_dim);
  *           (strides in elements, multiples of 8; a fused q|k|v row works as it is)
  *   slots   int32 [tokens]; a negative slot leaves its token out, a slot past the
  *           cache does too and sets Q4_DEVERR_INDEX.  No slot may occur twice.
- * Every step is one IEEE fp32 operation, rounded to nearest even:
+ * The result is that of single IEEE fp32 operations, rounded to nearest even:
  *   int8: s = fp16(min(amax / 127, 65504)); code = clamp(rint(x / s), -127, 127)
  *   int4: s = fp16(min((max - min) / 15, 65504)); m = fp16(clamp(min, +-65504));
  *         code = clamp(rint((x - m) / s), 0, 15)
@@ -322,8 +322,9 @@ q4_status q4_kv_read(const uint8_t *cache, int format, int pages, int page_size,
  *         h * head_dim + d (q_stride in elements, a multiple of 8)
  *   out   bf16 [batch, tokens, q_heads, head_dim]
  * q_heads is a multiple of kv_heads: query heads h * q_heads / kv_heads and on share
- * the keys of head h.  Scores, softmax statistics and sums are fp32; q and the codes
- * enter the products exactly, the probabilities (times their row's V scale) as fp16.
+ * the keys of head h.  Scores, softmax statistics and sums are fp32; the codes enter the
+ * products exactly, q does too (but for elements 2^31 times smaller than the largest of
+ * their row), the probabilities (times their row's V scale) as fp16.
  * lengths is read on the device: nothing on the host depends on it.  batch <= 8192.
  *
  * workspace: at least q4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,
