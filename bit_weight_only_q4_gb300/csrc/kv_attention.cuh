@@ -434,7 +434,7 @@ __device__ __forceinline__ KvWalk kv_find(const KvTileParams &p, int64_t c0)
     KvWalk w = {};
     int64_t before = 0;
 #pragma unroll 1
-    for (int i0 = 0; i0 < p.seqs; i0 += 32) {
+    for (int i0 = 0; i0 < p.seqs && p.seqs > 1; i0 += 32) {
         const int64_t mine = i0 + lane < p.seqs ? kv_tiles_of_sequence<N>(p, kv_length(p, i0 + lane)) : 0;
         int64_t incl = mine;
 #pragma unroll
