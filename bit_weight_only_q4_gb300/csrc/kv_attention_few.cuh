@@ -17,11 +17,12 @@
 // cycles (D = 128), its decoding and softmax some 2,500 warp instructions.
 //
 // What bounds it.  int8: HBM on long contexts (eight of 131,072 tokens, 8 heads of 128, 4
-// query heads each: 368 us, 5.9 TB/s).  int4, or heads of 64: the decoding warps, whose
-// instructions issue one in some four cycles beside the other roles' (the same in int4: 333 us,
-// 3.4 TB/s; 3,650 warp instructions a tile use 40 to 48% of the issue slots).  Short
-// contexts: the chain of a unit (queries, first references, sums, results), 2.7 us for one
-// tile, partly hidden behind the next unit's (48 streams of 37 to 4,096 tokens: 59 us).
+// query heads each: 351 us, 6.2 TB/s).  int4: the decoding warps, whose instructions
+// issue one in some four cycles beside the other roles' (the same in int4: 325 us, 3.5 TB/s;
+// 3,650 warp instructions a tile use 40 to 48% of the issue slots).  Heads of 64 in pages of
+// 16 tokens: the starting of copies (305 us; 8 copies a tile).  Short contexts: the chain
+// of a unit (queries, first references, sums, results), 3.4 us for one tile, partly hidden
+// behind the next unit's (48 streams of 37 to 4,096 tokens: 57 us).
 // Tried and left: 32 warps, with K and V decoded by two groups each, gained 10 to 20% on
 // units of two to four tiles and lost 14% on long ones to spills (64 registers a thread).
 #pragma once
@@ -51,9 +52,16 @@ struct KfSums {
     int pad[3];
 };
 
-// Shared memory: [raw ring][V: 2][q: 2][P: 2][o][token scales: 4]
+// What a row's results need: o = ca o_0 + cb o_1 + off, plus cp times the prefix's, goes to
+// `at` (elements of the output, of the pieces or of the prefix's results).
+struct __align__(16) KfResult {
+    float ca, cb, off, cp;
+    int64_t at, pad;
+};
+
+// Shared memory: [raw ring][V: 2][q: 2][P: 2][token scales: 4]
 struct KfSmem {
-    uint32_t v, q, p, o, info, total;
+    uint32_t v, q, p, info, total;
 };
 
 template <int FMT, int D>
@@ -65,7 +73,6 @@ __host__ __device__ inline KfSmem kf_smem(int stages)
     s.v = at, at += 2u * KT_TOKENS * D * 2;
     s.q = at, at += 2u * KF_N * D * 2;
     s.p = at, at += 2u * KF_N * KT_TOKENS * 2;
-    s.o = at, at += KF_N * D * 4u;
     s.info = at, at += 4u * KT_TOKENS * 16;
     s.total = at;
     return s;
@@ -118,9 +125,9 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     __shared__ __align__(16) KfRows s_rows[KF_ROW_SLOTS];
     __shared__ __align__(16) KfSums s_sums[2][2];          // [unit][group]
     __shared__ __align__(16) float s_nm[2][2][KF_N];       // minus the references: [group][by turns]
-    __shared__ __align__(16) float s_zero[KF_N], s_e[3][KF_N];
+    __shared__ __align__(16) float s_zero[KF_N];
     __shared__ float s_red[2][4][KF_N], s_wred[2][4], s_c[2][KF_N];
-    __shared__ float2 s_ml[KF_N];
+    __shared__ KfResult s_result[2][KF_N];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
     __shared__ int s_last, s_dead;
     const int NS = p.stages;
@@ -626,71 +633,104 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
         const int t = (warp - KF_E) * 32 + lane;
         const int d = kv_column<L::I8>(tok);
-        float *s_o = reinterpret_cast<float *>(smem + off.o);
         int done = 0;
 #pragma unroll 1
         for (int u = 0; done < sh.tiles; ++u) {
             unit_wait(u);
-            kv_wait(sums_full + 8u * (u & 1), (u >> 1) & 1, dead);
-            kv_wait(o_full + 8u * (u & 1), (u >> 1) & 1, dead);
-            if (bar_or(3, 128, gone()))                    // leave together
-                break;
             const KvUnit un = s_unit[u & (KT_UNITS - 1)];
-            done += un.k1 - un.k0;
-            tc_fence_after();
-            if (t < NR) {
-                const KfSums &a = s_sums[u & 1][0], &b = s_sums[u & 1][1];
-                const float m = fmaxf(a.m[t], b.m[t]);
-                const float ca = a.m[t] == -INFINITY ? 0.f : ex2(a.m[t] - m);
-                const float cb = b.m[t] == -INFINITY ? 0.f : ex2(b.m[t] - m);
-                s_ml[t] = make_float2(m, ((a.l[0][t] + a.l[1][t]) + (a.l[2][t] + a.l[3][t])) * ca +
-                                             ((b.l[0][t] + b.l[1][t]) + (b.l[2][t] + b.l[3][t])) * cb);
-                s_e[0][t] = ca;
-                s_e[1][t] = cb;
-                s_e[2][t] = L::I8 ? 0.f
-                                  : ((a.off[0][t] + a.off[1][t]) + (a.off[2][t] + a.off[3][t])) * ca +
-                                        ((b.off[0][t] + b.off[1][t]) + (b.off[2][t] + b.off[3][t])) * cb;
-            }
-            bar_sync(3, 128);
-#pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                if (!s_sums[u & 1][g].any)
-                    continue;
-                uint32_t v[NR];
-                kf_tmem_ld<NR>(tmem + t_lane + TM_O + (uint32_t)((u & 1) * 2 + g) * KF_N, v);
-                const bool add = g == 1 && s_sums[u & 1][0].any;
-                if (tok < D) {
-#pragma unroll
-                    for (int j = 0; j < NR; ++j) {
-                        float *o = s_o + j * D + d;
-                        *o = fmaf(__uint_as_float(v[j]), s_e[g][j], add ? *o : s_e[2][j]);
-                    }
-                }
-            }
-            tc_fence_before();
-            bar_sync(3, 128);
-            if (lane == 0)
-                mbar_arrive(o_empty + 8u * (u & 1));
             const int row0 = un.rt * KF_N;
             const int nrows = p.rows - row0 < KF_N ? p.rows - row0 : KF_N;
             const int grow0 = (p.prefix_len > 0 ? 0 : un.b * p.rows) + row0;      // among all rows
             const bool whole = un.k0 == 0 && un.k1 == un.n;
-            const int64_t slot = kv_piece_slot(un) * KF_N;
-#pragma unroll 1
-            for (int item = t; item < nrows * (D / 4); item += 128) {
-                const int n = item / (D / 4), c4 = item % (D / 4);
-                const float4 o = *reinterpret_cast<const float4 *>(s_o + n * D + c4 * 4);
-                if (whole) {
-                    kv_store4<D>(p, grow0 + n, un.h, c4, KvRowSum{s_ml[n].x, s_ml[n].y, o});
-                    continue;
+            const int64_t pre = (int64_t)un.h * p.all_rows + grow0;        // the rows' place in the prefix's results
+            const bool joins = whole && p.prefix_in_o != nullptr;
+            kv_wait(sums_full + 8u * (u & 1), (u >> 1) & 1, dead);
+            // A thread a row: the groups' sums together, and what is left to do for the row.
+            if (t < NR && t < nrows && !gone()) {
+                const KfSums &a = s_sums[u & 1][0], &b = s_sums[u & 1][1];
+                const float m = fmaxf(a.m[t], b.m[t]);
+                KfResult w;
+                w.ca = a.m[t] == -INFINITY ? 0.f : ex2(a.m[t] - m);
+                w.cb = b.m[t] == -INFINITY ? 0.f : ex2(b.m[t] - m);
+                float l = ((a.l[0][t] + a.l[1][t]) + (a.l[2][t] + a.l[3][t])) * w.ca +
+                          ((b.l[0][t] + b.l[1][t]) + (b.l[2][t] + b.l[3][t])) * w.cb;
+                w.off = L::I8 ? 0.f
+                              : ((a.off[0][t] + a.off[1][t]) + (a.off[2][t] + a.off[3][t])) * w.ca +
+                                    ((b.off[0][t] + b.off[1][t]) + (b.off[2][t] + b.off[3][t])) * w.cb;
+                w.cp = 0.f;
+                const int grow = grow0 + t;
+                if (!whole) {
+                    const int64_t slot = kv_piece_slot(un) * KF_N + t;
+                    *reinterpret_cast<float2 *>(p.piece_ml + slot * 2) = make_float2(m, l);
+                    w.at = slot * D;
+                } else if (p.prefix_len > 0) {             // a piece for the launch over the sequences' own tokens
+                    *reinterpret_cast<float2 *>(p.prefix_out_ml + (pre + t) * 2) = make_float2(m, l);
+                    w.at = (pre + t) * D;
+                } else {
+                    float own = 1.f;
+                    if (joins) {
+                        const float2 pml = __ldcg(reinterpret_cast<const float2 *>(p.prefix_in_ml + (pre + t) * 2));
+                        const float top = fmaxf(m, pml.x);
+                        own = m == -INFINITY ? 0.f : ex2(m - top);
+                        w.cp = pml.x == -INFINITY ? 0.f : ex2(pml.x - top);
+                        l = l * own + pml.y * w.cp;
+                    }
+                    // a row that sees nothing has l = 0 and gives zeros
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    own *= inv;
+                    w.ca *= own, w.cb *= own, w.off *= own, w.cp *= inv;
+                    const int token = p.by_group(grow);
+                    w.at = ((int64_t)token * p.cache.heads * p.group + un.h * p.group + grow - token * p.group) * D;
                 }
-                *reinterpret_cast<float4 *>(p.piece_o + (slot + n) * D + c4 * 4) = o;
-                if (c4 == 0)
-                    *reinterpret_cast<float2 *>(p.piece_ml + (slot + n) * 2) = s_ml[n];
+                s_result[u & 1][t] = w;
             }
-            if (!whole)
-                kv_join<D, KF_N, 128, 4>(p, sh, un, nrows, grow0, &s_last, t, 3);
-            bar_sync(3, 128);                              // s_o, s_ml and s_e may be written again
+            kv_wait(o_full + 8u * (u & 1), (u >> 1) & 1, dead);
+            if (bar_or(3, 128, gone()))                    // leave together
+                break;
+            done += un.k1 - un.k0;
+            tc_fence_after();
+            const bool any0 = s_sums[u & 1][0].any, any1 = s_sums[u & 1][1].any;
+            uint32_t v0[NR], v1[NR];
+            kf_tmem_ld<NR>(tmem + t_lane + TM_O + (uint32_t)((u & 1) * 2) * KF_N, v0);
+            kf_tmem_ld<NR>(tmem + t_lane + TM_O + (uint32_t)((u & 1) * 2 + 1) * KF_N, v1);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(o_empty + 8u * (u & 1));
+            // A thread a column: neighbouring lanes store neighbouring columns of a row.
+            float x[NR];
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const KfResult &w = s_result[u & 1][j];
+                x[j] = any0 ? fmaf(__uint_as_float(v0[j]), w.ca, w.off) : w.off;
+                x[j] = any1 ? fmaf(__uint_as_float(v1[j]), w.cb, x[j]) : x[j];
+            }
+            if (joins && tok < D) {
+                const float *src = p.prefix_in_o + pre * D + d;
+                float po[NR];
+#pragma unroll
+                for (int j = 0; j < NR; ++j)               // (all on their way before the first is used)
+                    po[j] = j < nrows ? __ldcg(src + j * D) : 0.f;
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+                    x[j] = fmaf(po[j], s_result[u & 1][j].cp, x[j]);
+            }
+            if (tok < D) {
+                if (!whole || p.prefix_len > 0) {
+                    float *dst = (whole ? p.prefix_out_o : p.piece_o) + d;
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+                        if (j < nrows)
+                            dst[s_result[u & 1][j].at] = x[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NR; ++j)
+                        if (j < nrows)
+                            p.out[s_result[u & 1][j].at + d] = f32_to_bf16_bits(x[j]);
+                }
+            }
+            if (!whole)                                    // (with more in flight than one it spills, which costs every role)
+                kv_join<D, KF_N, 128, 1>(p, sh, un, nrows, grow0, &s_last, t, 3);
         }
     }
     pdl_launch_dependents();
@@ -707,14 +747,14 @@ static KvKernel kf_describe(const DeviceInfo &dev, int rows)
 {
     KvKernel k = {};
     // The softmax's work goes by the columns that are computed.  With all 16 of them for 1, 4 and 8
-    // rows (us, against the least that holds the rows): one stream of 2,047 tokens 18.0 (14.5),
-    // 48 streams 89 (59), eight of 131,071 207 (166).
+    // rows (us, against the least that holds the rows): one stream of 2,047 tokens 15.8 (11.8),
+    // 48 streams 95 (57), eight of 131,071 200 (162).
     k.fn = rows <= 4   ? reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 4>)
            : rows <= 8 ? reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 8>)
                        : reinterpret_cast<const void *>(&kv_few_rows_kernel<FMT, D, 16>);
     k.tile = KF_N;
     k.threads = KF_WARPS * 32;
-    // 1024: alignment; 8192: static arrays and the CTA's reserve
+    // 1024: alignment; 8192: static arrays
     const size_t budget = dev.smem_optin - 1024 - 8192;
     for (k.stages = KT_MAX_STAGES; k.stages > 1 && kf_smem<FMT, D>(k.stages).total > budget;)
         --k.stages;
