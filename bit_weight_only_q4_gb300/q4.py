@@ -424,6 +424,27 @@ def _kv_rows(t, name, shape):
     return row
 
 
+# What the checks of a call found, by the shapes and strides it was made with (types, devices
+# and contiguity are looked at in every call): a small call's Python would take as long
+# as its kernel.
+_kv_plans: dict = {}
+
+
+def _kv_plan(key, plan):
+    if len(_kv_plans) >= 256:
+        _kv_plans.clear()
+    _kv_plans[key] = plan
+    return plan
+
+
+def _kv_typed(rows, cache, table, lengths):
+    """True if a call's tensors are of the kinds that all of its checks ask for."""
+    return (cache.dtype is torch.uint8 and cache.is_cuda and cache.is_contiguous() and
+            table.dtype is torch.int32 and table.is_cuda and table.is_contiguous() and
+            lengths.dtype is torch.int32 and lengths.is_cuda and lengths.is_contiguous() and
+            (rows is None or (rows.dtype is torch.bfloat16 and rows.is_cuda)))
+
+
 def q4_kv_write(k, v, cache, slots, fmt, stream=None):
     """Quantise K and V rows (bf16 [tokens, kv_heads, D]) into the cache's slots
     (int32 [tokens]; slot = page * page_size + token in the page, negative: left out)."""
@@ -448,11 +469,15 @@ def q4_kv_write(k, v, cache, slots, fmt, stream=None):
 def q4_kv_read(cache, page_table, lengths, max_len, head_dim, fmt, k=None, v=None, stream=None):
     """(k, v) bf16 [batch, max_len, kv_heads, head_dim] of the first lengths[b] cached tokens
     of each sequence, zeros behind them."""
-    geo = _kv_cache(cache, fmt, head_dim)
-    batch, width = _kv_ints(page_table, "page_table", 2)
-    if _kv_ints(lengths, "lengths", 1)[0] != batch:
-        raise ValueError("page_table must be [batch, width] and lengths [batch]")
-    shape = (batch, max_len, geo[3], head_dim)
+    key = (fmt, head_dim, max_len, cache.shape, page_table.shape, lengths.shape)
+    plan = _kv_plans.get(key)
+    if plan is None or not _kv_typed(None, cache, page_table, lengths):
+        geo = _kv_cache(cache, fmt, head_dim)
+        batch, width = _kv_ints(page_table, "page_table", 2)
+        if _kv_ints(lengths, "lengths", 1)[0] != batch:
+            raise ValueError("page_table must be [batch, width] and lengths [batch]")
+        plan = _kv_plan(key, (geo, batch, width, (batch, max_len, geo[3], head_dim)))
+    geo, batch, width, shape = plan
     if k is None:
         k = _kv_empty(shape, cache, stream)
     elif tuple(_cuda(k, "k", torch.bfloat16).shape) != shape:
@@ -495,14 +520,19 @@ def _kv_workspace(key, q, stream):
 def _kv_attention(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, scale, out, workspace,
                   stream):
     shape = q.shape
-    if len(shape) != 4:
-        raise ValueError(f"q must be [batch, tokens, q_heads, D], got {tuple(shape)}")
-    row = _kv_rows(q, "q", shape)
-    B, T, Hq, D = shape
-    geo = _kv_cache(cache, fmt, D)
-    batch, width = _kv_ints(page_table, "page_table", 2)
-    if batch != B or _kv_ints(lengths, "lengths", 1)[0] != B:
-        raise ValueError(f"page_table must be [batch, width] and lengths [batch], q has {B} sequences")
+    key = (fmt, prefix_len, shape, q.stride(), cache.shape, page_table.shape, lengths.shape)
+    plan = _kv_plans.get(key)
+    if plan is None or not _kv_typed(q, cache, page_table, lengths):
+        if len(shape) != 4:
+            raise ValueError(f"q must be [batch, tokens, q_heads, D], got {tuple(shape)}")
+        row = _kv_rows(q, "q", shape)
+        B, T, Hq, D = shape
+        geo = _kv_cache(cache, fmt, D)
+        batch, width = _kv_ints(page_table, "page_table", 2)
+        if batch != B or _kv_ints(lengths, "lengths", 1)[0] != B:
+            raise ValueError(f"page_table must be [batch, width] and lengths [batch], q has {B} sequences")
+        plan = _kv_plan(key, (row, geo, width, B, T, Hq, D, D**-0.5 if D else 1.0))
+    row, geo, width, B, T, Hq, D, s = plan
     if out is None:
         out = _kv_empty(shape, q, stream)
     elif _cuda(out, "out", torch.bfloat16).shape != shape:
@@ -516,7 +546,8 @@ def _kv_attention(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, 
         if workspace is None:
             workspace = _kv_workspace(key, q, stream)
     wp, wn = _ws_args(workspace)
-    s = D ** -0.5 if scale is None else float(scale)
+    if scale is not None:
+        s = float(scale)
     lib = _lib or load()
     if prefix_pages is not None:
         status = lib.q4_kv_attention_shared(q.data_ptr(), row, cache.data_ptr(), *geo, prefix_pages.data_ptr(),
