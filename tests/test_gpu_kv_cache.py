@@ -91,6 +91,32 @@ def test_write_stores_the_reference_bytes(q4, fmt, D, n, H, page):
     np.testing.assert_array_equal(cache.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_write_of_ties_and_of_rows_of_every_size(q4, fmt, D):
+    """Values halfway between two codes, and rows from below fp16's smallest scale to past its
+    largest: the bytes of the reference's divisions."""
+    rng = np.random.default_rng([15, fmt, D])
+    rows_ = []
+    for e in range(-40, 36):
+        half = rng.integers(-127, 127, D) + 0.5             # int8: ties at a scale of 2^e
+        half[:2] = 127, -100
+        rows_.append(half * 2.0**e)
+        half = rng.integers(0, 15, D) + 0.5 - 7             # int4: the same, from the minimum on
+        half[:2] = -7, 8
+        rows_.append(half * 2.0**e)
+        rows_.append(rng.standard_normal(D) * 2.0**e)
+        rows_.append((rng.integers(0, 16, D) - 100) * 2.0**e)                # far from zero
+    x = bf16(np.stack(rows_)).float().numpy().reshape(-1, 4, D)
+    n, H, page = *x.shape[:2], 16
+    init = np.zeros((-(-n // page), H, 1, R.block_bytes(fmt, D)), np.uint8)
+    want = init.copy()
+    R.write(want, np.arange(n), x, x[::-1].copy(), fmt, page)
+    cache = torch.from_numpy(init).cuda()
+    q4.q4_kv_write(bf16(x).cuda(), bf16(x[::-1].copy()).cuda(), cache, torch.arange(n, dtype=torch.int32, device="cuda"), fmt)
+    np.testing.assert_array_equal(cache.cpu().numpy(), want)
+
+
 def test_write_leaves_out_slots_outside_the_cache(q4):
     rng = np.random.default_rng(2)
     init = rng.integers(0, 256, (2, 2, 1, R.block_bytes(0, 64)), dtype=np.uint8)

@@ -82,6 +82,14 @@ def test_invalid_caches_are_rejected(lib, f):
     assert f(lib, cache=FAKE + 8) == 3
 
 
+@pytest.mark.parametrize("f", [_write, _read, _attend])
+def test_caches_of_too_many_blocks_are_rejected(lib, f):
+    # (one more than 2^31 - 1 blocks of 16 tokens and a head)
+    assert f(lib, pages=1 << 30, H=2) == 2
+    assert f(lib, pages=1 << 24, H=2, page=1024) == 2
+    assert b"blocks" in lib.q4_last_error_string()
+
+
 def test_invalid_write_arguments_are_rejected(lib):
     assert _write(lib, k=None) == 1 and _write(lib, v=None) == 1 and _write(lib, slots=None) == 1
     assert _write(lib, n=0) == 2
@@ -92,6 +100,7 @@ def test_invalid_write_arguments_are_rejected(lib):
 def test_invalid_read_arguments_are_rejected(lib):
     assert _read(lib, table=None) == 1 and _read(lib, lens=None) == 1 and _read(lib, k=None) == 1
     assert _read(lib, B=0) == 2 and _read(lib, most=0) == 2 and _read(lib, width=0) == 2
+    assert _read(lib, B=1 << 15, most=1 << 20) == 2         # CTAs past 2^31
     assert _read(lib, v=FAKE + 8) == 3 and _read(lib, table=FAKE + 1) == 3 and _read(lib, lens=FAKE + 2) == 3
 
 
