@@ -387,6 +387,29 @@ def test_repeated_captured_and_streamed_calls_agree(q4, shared):
 
 
 @pytest.mark.parametrize("Hq", [4, 40])
+def test_a_call_captured_before_any_has_run(q4, Hq):
+    """The workspace that such a call gets is filled in its graph; calls between capture and
+    replay have one of their own."""
+    rng = np.random.default_rng([16, Hq])
+    lens = [611, 1999, 5]
+    cache, table, _ = filled(rng, 1, 128, 2, 32, lens)
+    q = bf16(rng.standard_normal((3, 1, Hq, 128))).cuda()
+    c, t = torch.from_numpy(cache).cuda(), torch.from_numpy(table).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        captured = q4.q4_kv_attention(q, c, t, n, 1)
+    with torch.cuda.stream(stream):
+        between = bits(q4.q4_kv_attention(q, c, t, n, 1))
+        for _ in range(2):
+            graph.replay()
+            np.testing.assert_array_equal(bits(captured), between)
+        np.testing.assert_array_equal(bits(q4.q4_kv_attention(q, c, t, n, 1)), between)
+    check(captured, q.float().cpu().numpy(), cache, table, lens, 1, 128**-0.5)
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
 @pytest.mark.parametrize("scale", [0.0, -0.07, 1e-9])
 def test_scales_of_any_sign(q4, scale, Hq):
     rng = np.random.default_rng([13, Hq])
