@@ -87,10 +87,11 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sm = smem_u32(smem);
     KmScales *s_scales = reinterpret_cast<KmScales *>(smem + off.scales);
-    // exchanged between a row's two threads, where the results go later
+    // exchanged between a row's two threads, where the results go later.  s_top is read before q_full, which
+    // the first S waits for, and may lie where s_sum does; s_qs is read after it and may not.
     uint32_t (*s_top)[KM_ROWS] = reinterpret_cast<uint32_t (*)[KM_ROWS]>(smem + off.stage);
-    float (*s_qs)[KM_ROWS] = reinterpret_cast<float (*)[KM_ROWS]>(smem + off.stage + 1024);
     float4 (*s_sum)[KM_ROWS] = reinterpret_cast<float4 (*)[KM_ROWS]>(smem + off.stage);   // m, l, offset
+    float (*s_qs)[KM_ROWS] = reinterpret_cast<float (*)[KM_ROWS]>(smem + off.stage + 2 * sizeof(*s_sum));
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
