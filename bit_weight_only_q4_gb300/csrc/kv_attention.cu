@@ -1,11 +1,20 @@
 // Host side of the attention over the paged cache: choice of kernel, workspace, launches.
 // The kernels: kv_attention_few.cuh, kv_attention_many.cu; what they compute and how work
 // is dealt out: kv_attention.cuh.
+#include <atomic>
 #include <mutex>
 
 #include "kv_attention.cuh"
 
 namespace q4 {
+
+static std::atomic<int> g_give_up{-1}, g_give_up_tiles{0};
+
+void kv_set_give_up(int cta, int tiles)
+{
+    g_give_up_tiles.store(tiles);
+    g_give_up.store(cta);
+}
 
 struct KvPlan {
     KvKernel k;
@@ -155,6 +164,8 @@ q4_status launch_kv_attention(const DeviceInfo &dev, const KvCacheDesc &c, const
     p.all_rows = (int)(plans[0].rows * a.batch);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.err = device_error_flags();
+    p.give_up = g_give_up.load();
+    p.give_up_tiles = g_give_up_tiles.load();
     q4_status s;
     if (n == 2) {
         KvTileParams f = p;

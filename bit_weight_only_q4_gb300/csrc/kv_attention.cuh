@@ -63,6 +63,7 @@ struct KvTileParams {
     float *prefix_out_o, *prefix_out_ml;           // [heads][all_rows][D], [..][2]: written (prefix) ...
     const float *prefix_in_o, *prefix_in_ml;       // ... or joined
     unsigned *err;
+    int give_up, give_up_tiles;  // (tests) CTA whose copying warp gives up after so many tiles; negative: none
 };
 
 // ------------------------------------------------------------------- helpers
@@ -153,7 +154,8 @@ __device__ __forceinline__ bool elect_one()
 
 // Where a wait that has given up is noted: the error word, and a flag of the CTA that
 // lets every later wait return at once.  The roles leave their loops when they see it
-// (those whose warps meet at barriers by a vote), and nothing is stored after it.
+// (those whose warps meet at barriers by a vote after each wait for a unit: one that was
+// never described would not bring them to their end), and nothing is stored after it.
 struct KvDead {
     unsigned *err;
     volatile int *flag;
@@ -185,6 +187,16 @@ __device__ __forceinline__ void kv_wait(uint32_t bar, uint32_t parity, const KvD
                  ::"r"(bar), "r"(parity), "r"(dead.flag_at), "l"(dead.err), "n"(kMbarSpinLimit), "n"(kErrBarrierTimeout)
                  : "memory");
     __syncwarp();
+}
+
+// A CTA that has given up: the MMAs that this warp's elected lane has issued are waited for,
+// so that none runs into the CTA's end.  `bar` has a count of one and is used for this alone.
+__device__ __forceinline__ void kv_mma_drain(uint32_t bar, const KvDead &dead)
+{
+    if (elect_one())
+        mma_commit(bar);
+    __syncwarp();
+    mbar_wait(bar, 0u, dead.err);
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads)
@@ -517,8 +529,10 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
     const bool starts = (lane & (run - 1)) == 0;
     int s = 0, issued = 0;
     uint32_t round = 1u;                           // parity of the slot's previous release
+    const int last = (int)blockIdx.x == p.give_up ? p.give_up_tiles : -1;
+    int i = 0;
 #pragma unroll 1
-    for (int i = 0; i < sh.tiles && !*dead.flag;) {
+    while (i < sh.tiles && i != last && !*dead.flag) {
         // the blocks looked up in the last round
         const uint8_t *from = nullptr;
         if (has && page >= 0 && page < p.cache.pages)
@@ -548,7 +562,7 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
         at_head = head;
         k += n;
 #pragma unroll 1
-        for (int j = 0; j < m; ++j, ++i) {
+        for (int j = 0; j < m && i != last; ++j, ++i) {
             if (i >= NS)
                 kv_wait(raw_empty + 8u * s, round, dead);
             const unsigned blocks = (valid >> (8 * j)) & 0xffu;
@@ -565,11 +579,18 @@ __device__ __forceinline__ void kv_copy_warp(const KvTileParams &p, const KvShar
                 s = 0, round ^= 1u;
         }
     }
+    if (i == last) {
+        if (lane == 0) {
+            *dead.flag = 1;
+            atomicOr(p.err, kErrBarrierTimeout);
+        }
+        __syncwarp();
+    }
     // Every copy has been waited for by those who read it, unless one of them has left
     // early: then wait here, once more with a limit, before the CTA can exit.
     if (*dead.flag)
 #pragma unroll 1
-        for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+        for (i = issued > NS ? issued - NS : 0; i < issued; ++i)
 #pragma unroll 1
             for (uint32_t w = 0; w < kMbarSpinLimit / 64 && !mbar_try_wait(raw_full + 8u * (i % NS), (i / NS) & 1); ++w)
                 ;

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     // tensor memory: two K tiles (D / 2 columns), two S tiles (16), O of two units and groups (16)
     constexpr uint32_t TM_S = D, TM_O = D + 2 * KF_N, TM_COLS = 256;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 22 + KT_UNITS];
+    __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 24 + KT_UNITS];
     __shared__ KvUnit s_unit[KT_UNITS];
     __shared__ __align__(16) KfRows s_rows[KF_ROW_SLOTS];
     __shared__ __align__(16) KfSums s_sums[2][2];          // [unit][group]
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     const uint32_t k_full = raw_empty + 8u * KT_MAX_STAGES, s_full = k_full + 16, s_free = k_full + 32,
                    p_full = k_full + 48, v_full = k_full + 64, pv_done = k_full + 80, q_full = k_full + 96,
                    q_empty = k_full + 112, o_full = k_full + 128, o_empty = k_full + 144, sums_full = k_full + 160,
-                   unit_full = k_full + 176;
+                   drained = k_full + 176, unit_full = k_full + 192;
     if (warp == KF_COPY) {
         kv_init_bars(raw_full, NS, 1);
         kv_init_bars(raw_empty, NS, 8);                    // K and V warps
@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         kv_init_bars(o_full, 2, 1);                        // commit after a unit's last O
         kv_init_bars(o_empty, 2, 4);
         kv_init_bars(sums_full, 2, 8);
+        kv_init_bars(drained, 2, 1);                       // MMAs of a CTA that has given up
         kv_init_bars(unit_full, KT_UNITS, 1);
         if (lane == 0)
             s_dead = 0;
@@ -222,6 +223,8 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             }
             __syncwarp();
         }
+        if (gone_all())
+            kv_mma_drain(drained, dead);
     } else if (warp == KF_MMA_O) {
         // ------------------------------------------------ MMAs: O^T += V^T P^T
         // A is M-major: 64-column halves 16 KB apart, groups of 8 tokens 1 KB apart (D = 64 has
@@ -265,6 +268,8 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             __syncwarp();
             begun |= 1u << g;
         }
+        if (gone_all())
+            kv_mma_drain(drained + 8u, dead);
     } else if (warp == KF_Q) {
         // ----------------------------------------- q: prescaled fp16, row data
         // (of the first NR rows: a column of S^T or O^T takes nothing from another one's q)
@@ -449,6 +454,8 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
 #pragma unroll 1
         for (int u = 0; i < sh.tiles && !leave; ++u) {
             unit_wait(u);
+            if (bar_or(bar_id, 128, gone()))               // leave together
+                break;
             const KvUnit &un = s_unit[u & (KT_UNITS - 1)];
             const int ntok = un.ntok, k0 = un.k0 - i;
             const int end = i + un.k1 - un.k0;

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     // tensor memory columns: q' (D / 2), S of two halves (64), P (32), O (D)
     constexpr uint32_t TM_S = D / 2, TM_P = TM_S + 128, TM_O = TM_P + 64, TM_COLS = 512;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 17 + KT_UNITS];
+    __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 19 + KT_UNITS];
     __shared__ KvUnit s_unit[KT_UNITS];
     __shared__ float s_wmax[4][4];                         // largest V scale of 32 tokens
     __shared__ __align__(16) KmRow s_row[KM_ROWS];
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     const uint32_t raw_full = smem_u32(s_bar), raw_empty = raw_full + 8u * KT_MAX_STAGES;
     const uint32_t k_full = raw_empty + 8u * KT_MAX_STAGES, k_done = k_full + 16, v_full = k_full + 32,
                    v_done = k_full + 48, s_full = k_full + 64, s_free = k_full + 80, p_full = k_full + 96,
-                   pv_done = k_full + 112, q_full = k_full + 128, unit_full = k_full + 136;
+                   pv_done = k_full + 112, q_full = k_full + 128, drained = k_full + 136, unit_full = k_full + 152;
     if (warp == KM_COPY) {
         kv_init_bars(raw_full, NS, 1);
         kv_init_bars(raw_empty, NS, 8);                    // K and V warps
@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
         kv_init_bars(p_full, 2, 4);
         kv_init_bars(pv_done, 2, 1);
         kv_init_bars(q_full, 1, 8);
+        kv_init_bars(drained, 2, 1);                       // MMAs of a CTA that has given up
         kv_init_bars(unit_full, KT_UNITS, 1);
         if (lane == 0)
             s_dead = 0;
@@ -610,6 +611,8 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                 __syncwarp();
             }
         }
+        if (gone_all())
+            kv_mma_drain(drained, dead);
         } else if (warp == KM_O) {
         // ------------------------------------------------------- MMAs: O += P V
         constexpr uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);   // B is N-major
@@ -645,6 +648,8 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                 __syncwarp();
             }
         }
+        if (gone_all())
+            kv_mma_drain(drained + 8u, dead);
         }
     }
     pdl_launch_dependents();

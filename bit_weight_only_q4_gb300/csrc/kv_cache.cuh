@@ -80,6 +80,8 @@ struct KvAttnArgs {
     float scale;
     void *ws;
 };
+// (tests) The CTA of every later launch whose copying warp gives up after `tiles` tiles.
+void kv_set_give_up(int cta, int tiles);
 q4_status launch_kv_write(const KvCacheDesc &c, const uint16_t *k, int64_t k_stride, const uint16_t *v,
                           int64_t v_stride, const int32_t *slots, int tokens, cudaStream_t st, bool pdl);
 q4_status launch_kv_read(const KvCacheDesc &c, const int32_t *table, int table_width, const int32_t *lengths,

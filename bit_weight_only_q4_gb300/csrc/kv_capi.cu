@@ -154,6 +154,8 @@ q4_status q4_kv_read(const uint8_t *cache, int format, int pages, int page_size,
                           static_cast<uint16_t *>(v), static_cast<cudaStream_t>(stream), pdl_on());
 }
 
+void q4_test_kv_give_up(int cta, int tiles) { kv_set_give_up(cta, tiles); }
+
 size_t q4_kv_attention_workspace_bytes(int format, int kv_heads, int head_dim, int batch, int tokens,
                                        int q_heads, int prefix_len)
 {

@@ -80,6 +80,7 @@ def load() -> ctypes.CDLL:
             "q4_kv_block_bytes": ([i, i], sz),
             "q4_kv_write": ([p, i64, p, i64, p, i, p, i, i, i, i, i, p], st),
             "q4_kv_read": ([p, i, i, i, i, i, p, i, p, i, i, p, p, p], st),
+            "q4_test_kv_give_up": ([i, i], None),
             "q4_kv_attention_workspace_bytes": ([i, i, i, i, i, i, i], sz),
             "q4_kv_attention": ([p, i64, p, i, i, i, i, i, p, i, p, i, i, i, f, p, p, sz, p], st),
             "q4_kv_attention_shared": ([p, i64, p, i, i, i, i, i, p, i, p, i, p, i, i, i, f, p, p,
@@ -102,7 +103,7 @@ def symbols() -> list[str]:
             "q4_dequant_nvfp4_f32", "q4_quantize_int4g128", "q4_quantize_nvfp4",
             "q4_embedding_int8", "q4_linear_int8", "q4_kv_block_bytes", "q4_kv_write",
             "q4_kv_read", "q4_kv_attention_workspace_bytes", "q4_kv_attention",
-            "q4_kv_attention_shared"]
+            "q4_kv_attention_shared", "q4_test_kv_give_up"]
 
 
 def _check(status: int) -> None:

@@ -194,6 +194,13 @@ q4_status q4_dequant_nvfp4_f32(const uint8_t *codes, const uint8_t *scale_e4m3,
                                void *stream);
 
 /*
+ * Test helper: in every later attention call over a key/value cache, CTA `cta` of each launch
+ * gives up when `tiles` of its tiles of 128 tokens have been copied, as after a wait that has
+ * run out: it sets Q4_DEVERR_TIMEOUT and returns early.  cta < 0 (the default): none does.
+ */
+void q4_test_kv_give_up(int cta, int tiles);
+
+/*
  * INT8 weight-only linear ("Rumik TTS Fast Inference", "What Made It Faster": INT8
  * weight-only decode projections; the layout is not given there).  Reading, after
  * the int8 scheme "rumik-oss-1-int4" gives for its embedding: qweight int8 [N, K]

@@ -29,3 +29,41 @@ def test_many_short_units_of_many_rows(q4, fmt, D, T, Hq, H):
     # a sequence's units are whole here, so alone it takes the same steps in the same order
     for b in range(0, len(lens), 25):
         np.testing.assert_array_equal(bits(call(q4, q[b:b + 1], cache, table[b:b + 1], lens[b:b + 1], fmt)), first[b:b + 1])
+
+
+GIVE_UP = [  # tokens, q_heads, prefix: the few-row kernel, the many-row kernel, one after the other
+    (1, 8, 0), (5, 16, 0), (1, 8, 300)]
+
+
+def some_calls(q4, fmt, T, Hq, prefix):
+    """A batch of split and whole units and a way to attend to it: go(**kw)."""
+    rng = np.random.default_rng([21, fmt, T, Hq])
+    D, H, page, lens = 128, 2, 32, [700, 12000, 60, 9000]
+    cache, table, pp = filled(rng, fmt, D, H, page, lens, prefix=prefix)
+    c, t, p = torch.from_numpy(cache).cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(pp).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = bf16(rng.standard_normal((len(lens), T, Hq, D))).cuda()
+    size = q4.kv_attention_workspace_bytes(fmt, H, D, len(lens), T, Hq, prefix)
+
+    def go(**kw):
+        return q4.q4_kv_attention_shared(q, c, p, prefix, t, n, fmt, **kw) if prefix else \
+            q4.q4_kv_attention(q, c, t, n, fmt, **kw)
+    return go, size
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,Hq,prefix", GIVE_UP)
+@pytest.mark.parametrize("cta,tiles", [(0, 0), (0, 1), (3, 0), (1, 3)])
+def test_a_cta_that_gives_up_ends_the_call_with_a_status(q4, fmt, T, Hq, prefix, cta, tiles):
+    """Before its first unit has been described, or in the midst of one."""
+    go, size = some_calls(q4, fmt, T, Hq, prefix)
+    q4.device_error_flags(clear=True)
+    try:
+        q4.load().q4_test_kv_give_up(cta, tiles)
+        go(workspace=torch.zeros(size, dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+    finally:
+        q4.load().q4_test_kv_give_up(-1, 0)
+    assert q4.device_error_flags() == 1
+    go(workspace=torch.zeros(size, dtype=torch.uint8, device="cuda"))
+    assert q4.device_error_flags() == 0
