@@ -1,6 +1,7 @@
 // Host side of the attention over the paged cache: choice of kernel, workspace, launches.
 // The kernels: kv_attention_few.cuh, kv_attention_many.cu; what they compute and how work
 // is dealt out: kv_attention.cuh.
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -19,10 +20,12 @@ void kv_set_give_up(int cta, int tiles)
 struct KvPlan {
     KvKernel k;
     int row_tiles, grid;
-    int64_t rows, units;
+    int64_t rows;
 };
 
-static KvPlan kv_plan(const DeviceInfo &dev, const KvCacheDesc &c, int seqs, int64_t rows)
+constexpr int kMaxGrid = Q4_KV_COUNTER_BYTES / 4;          // a counter for each CTA
+
+static KvPlan kv_plan(const DeviceInfo &dev, const KvCacheDesc &c, int64_t rows)
 {
     KvPlan t = {};
     t.rows = rows;
@@ -36,15 +39,15 @@ static KvPlan kv_plan(const DeviceInfo &dev, const KvCacheDesc &c, int seqs, int
         t.k = c.format == Q4_CACHE_INT8 ? kv_few_kernel_int8(dev, c.head_dim, (int)rows)
                                         : kv_few_kernel_int4(dev, c.head_dim, (int)rows);
     t.row_tiles = (int)((rows + t.k.tile - 1) / t.k.tile);
-    t.units = (int64_t)seqs * c.heads * t.row_tiles;
-    t.grid = dev.sms;
+    t.grid = dev.sms < kMaxGrid ? dev.sms : kMaxGrid;
     return t;
 }
 
-// Workspace: counters of the units, pieces of each of the (one or two) launches, then the
-// prefix's results.
+// Workspace: counters, at the same place for calls of every shape (they have to be zero when
+// a call begins, and whatever else lies there need not be), then the pieces of the (one or
+// two) launches, which follow one another, then the prefix's results.
 struct KvWorkspace {
-    size_t tickets[2], piece_o[2], piece_ml[2], prefix_o, prefix_ml, total;
+    size_t piece_o, piece_ml, prefix_o, prefix_ml, total;
 };
 
 static KvWorkspace kv_workspace(const KvCacheDesc &c, const KvPlan *plans, int n, int64_t prefix_rows)
@@ -55,12 +58,12 @@ static KvWorkspace kv_workspace(const KvCacheDesc &c, const KvPlan *plans, int n
         w.total += (bytes + 255) / 256 * 256;
         return at;
     };
+    size_t piece_rows = 0;
     for (int i = 0; i < n; ++i)
-        w.tickets[i] = take((size_t)plans[i].units * 4);
-    for (int i = 0; i < n; ++i) {
-        w.piece_o[i] = take((size_t)2 * plans[i].grid * plans[i].k.tile * c.head_dim * 4);
-        w.piece_ml[i] = take((size_t)2 * plans[i].grid * plans[i].k.tile * 2 * 4);
-    }
+        piece_rows = std::max(piece_rows, (size_t)2 * plans[i].grid * plans[i].k.tile);
+    take(Q4_KV_COUNTER_BYTES);
+    w.piece_o = take(piece_rows * c.head_dim * 4);
+    w.piece_ml = take(piece_rows * 2 * 4);
     w.prefix_o = take((size_t)prefix_rows * c.heads * c.head_dim * 4);
     w.prefix_ml = take((size_t)prefix_rows * c.heads * 2 * 4);
     return w;
@@ -72,10 +75,10 @@ static int kv_plans(const DeviceInfo &dev, const KvCacheDesc &c, int batch, int 
                     KvPlan (&plans)[2])
 {
     const int64_t rows = (int64_t)tokens * (q_heads / c.heads);
-    plans[0] = kv_plan(dev, c, batch, rows);
+    plans[0] = kv_plan(dev, c, rows);
     if (prefix_len <= 0)
         return 1;
-    plans[1] = kv_plan(dev, c, 1, rows * batch);
+    plans[1] = kv_plan(dev, c, rows * batch);
     return 2;
 }
 
@@ -166,6 +169,9 @@ q4_status launch_kv_attention(const DeviceInfo &dev, const KvCacheDesc &c, const
     p.err = device_error_flags();
     p.give_up = g_give_up.load();
     p.give_up_tiles = g_give_up_tiles.load();
+    p.tickets = reinterpret_cast<unsigned *>(ws);
+    p.piece_o = at(w.piece_o);
+    p.piece_ml = at(w.piece_ml);
     q4_status s;
     if (n == 2) {
         KvTileParams f = p;
@@ -173,9 +179,6 @@ q4_status launch_kv_attention(const DeviceInfo &dev, const KvCacheDesc &c, const
         f.cap = a.prefix_len;
         f.seqs = 1;
         f.prefix_len = a.prefix_len;
-        f.tickets = reinterpret_cast<unsigned *>(ws + w.tickets[1]);
-        f.piece_o = at(w.piece_o[1]);
-        f.piece_ml = at(w.piece_ml[1]);
         f.prefix_out_o = at(w.prefix_o);
         f.prefix_out_ml = at(w.prefix_ml);
         if ((s = kv_tile_launch(plans[1], f, st, pdl)) != Q4_OK)
@@ -187,9 +190,6 @@ q4_status launch_kv_attention(const DeviceInfo &dev, const KvCacheDesc &c, const
     p.table_width = a.table_width;
     p.cap = (int64_t)a.table_width << c.page_shift;
     p.seqs = a.batch;
-    p.tickets = reinterpret_cast<unsigned *>(ws + w.tickets[0]);
-    p.piece_o = at(w.piece_o[0]);
-    p.piece_ml = at(w.piece_ml[0]);
     return kv_tile_launch(plans[0], p, st, pdl);
 }
 

@@ -58,7 +58,7 @@ struct KvTileParams {
     int row_tiles;
     float scale_log2;            // scale * log2(e)
     int stages;
-    unsigned *tickets;           // [unit]
+    unsigned *tickets;           // [grid]: of the unit that goes past this CTA's end, if one that begins in it does
     float *piece_o, *piece_ml;   // [2 * grid][tile rows][D], [2 * grid][tile rows][2]: o, and (m, l)
     float *prefix_out_o, *prefix_out_ml;           // [heads][all_rows][D], [..][2]: written (prefix) ...
     const float *prefix_in_o, *prefix_in_ml;       // ... or joined
@@ -653,7 +653,7 @@ __device__ __forceinline__ void kv_join(const KvTileParams &p, const KvShare &sh
     const int64_t first = un.u0 / sh.share;
     const int np = (int)((un.u0 + un.n - 1) / sh.share - first) + 1;
     if (t == 0) {
-        unsigned *tk = &p.tickets[((int64_t)un.b * p.row_tiles + un.rt) * p.cache.heads + un.h];
+        unsigned *tk = p.tickets + first;          // (of the units that begin in a CTA only its last goes on)
         const bool last = atomicAdd(tk, 1u) == (unsigned)(np - 1);
         if (last)
             *tk = 0u;

@@ -335,9 +335,11 @@ q4_status q4_kv_read(const uint8_t *cache, int format, int pages, int page_size,
  * lengths is read on the device: nothing on the host depends on it.  batch <= 8192.
  *
  * workspace: at least q4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,
- * zero-filled once after allocation (every call leaves its counters at zero); calls
- * that run concurrently must not share one.
+ * whose first Q4_KV_COUNTER_BYTES were zero-filled once after allocation (every call leaves
+ * them at zero); calls of any shapes may use one in turn, calls that run concurrently must
+ * not share one.
  */
+#define Q4_KV_COUNTER_BYTES 4096
 size_t q4_kv_attention_workspace_bytes(int format, int kv_heads, int head_dim, int batch, int tokens,
                                        int q_heads, int prefix_len);
 q4_status q4_kv_attention(const void *q_bf16, int64_t q_stride, const uint8_t *cache, int format,

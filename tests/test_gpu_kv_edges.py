@@ -67,3 +67,32 @@ def test_a_cta_that_gives_up_ends_the_call_with_a_status(q4, fmt, T, Hq, prefix,
     assert q4.device_error_flags() == 1
     go(workspace=torch.zeros(size, dtype=torch.uint8, device="cuda"))
     assert q4.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_workspace_serves_calls_of_every_shape(q4, fmt, prefix):
+    """A buffer of the largest size, zero-filled once: few sequences, many, more rows, few again."""
+    rng = np.random.default_rng([22, fmt])
+    D, H, page = 128, 16, 64
+    mixed = [100 + 97 * b % 1500 for b in range(160)]
+    shapes = [([2047], 1, 16), (mixed, 1, 16), (mixed, 2, 32), ([900, 2047], 5, 64), ([2047], 1, 16)]
+    cache, table, pp = filled(rng, fmt, D, H, page, [2047] * 2, prefix=prefix)
+    c, p = torch.from_numpy(cache).cuda(), torch.from_numpy(pp).cuda()
+
+    def go(lens, T, Hq, ws):
+        t = torch.from_numpy(np.ascontiguousarray(table[np.arange(len(lens)) % 2])).cuda()
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        q = bf16(np.random.default_rng(Hq).standard_normal((len(lens), T, Hq, D))).cuda()
+        out = torch.full_like(q, torch.nan)
+        if prefix:
+            q4.q4_kv_attention_shared(q, c, p, prefix, t, n, fmt, out=out, workspace=ws)
+        else:
+            q4.q4_kv_attention(q, c, t, n, fmt, out=out, workspace=ws)
+        return bits(out)
+
+    size = [q4.kv_attention_workspace_bytes(fmt, H, D, len(n), T, Hq, prefix) for n, T, Hq in shapes]
+    one = torch.zeros(max(size), dtype=torch.uint8, device="cuda")
+    for (lens, T, Hq), n in zip(shapes, size):
+        want = go(lens, T, Hq, torch.zeros(n, dtype=torch.uint8, device="cuda"))
+        np.testing.assert_array_equal(go(lens, T, Hq, one), want)
