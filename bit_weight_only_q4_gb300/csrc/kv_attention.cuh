@@ -642,26 +642,58 @@ __device__ __forceinline__ int64_t kv_piece_slot(const KvUnit &un)
     return 2 * (int64_t)blockIdx.x + (un.k0 == 0 ? 1 : 0);
 }
 
+// Counts this CTA in at a unit that it does not have whole; true if it is the last of them
+// and all have their piece.  Every CTA of a unit is counted, one that has given up with a mark
+// (bit 16 and up): the counter is zero again when the launch ends, whatever has happened.
+__device__ __forceinline__ bool kv_arrive(const KvTileParams &p, const KvShare &sh, const KvUnit &un, bool failed)
+{
+    const int64_t first = un.u0 / sh.share;
+    const int np = (int)((un.u0 + un.n - 1) / sh.share - first) + 1;
+    unsigned *tk = p.tickets + first;              // (of the units that begin in a CTA only its last goes on)
+    const unsigned old = atomicAdd(tk, failed ? 0x10001u : 1u);
+    if ((old & 0xffffu) != (unsigned)(np - 1))
+        return false;
+    *tk = 0u;
+    return !failed && (old >> 16) == 0u;
+}
+
+// Which of a CTA's (at most two) pieces have been counted: bit 1 for one that begins its unit, bit 0 for another.
+__device__ __forceinline__ int kv_piece_bit(const KvUnit &un) { return un.k0 == 0 ? 2 : 1; }
+
+// A CTA that has given up: counted in, with the mark, where it has not been yet (a warp).
+template <int N>
+__device__ __forceinline__ void kv_arrive_failed(const KvTileParams &p, int counted)
+{
+    const KvShare sh = kv_share<N>(p);
+    if (sh.tiles == 0)
+        return;
+    KvWalk walk = kv_find<N>(p, sh.c0);
+#pragma unroll 1
+    for (int64_t f = sh.c0; f < sh.c1;) {
+        const KvUnit un = kv_next_unit<N>(p, walk, f, sh.c1);
+        f += un.k1 - un.k0;
+        if (un.k1 - un.k0 < un.n && !(counted & kv_piece_bit(un)) && (threadIdx.x & 31) == 0)
+            kv_arrive(p, sh, un, true);
+    }
+}
+
 // The piece is written: if it is the unit's last to arrive, join all of them in order and
 // store the rows.  Called by NT threads that meet at barrier `bar`, with IT items a thread in flight.
 template <int D, int TILE, int NT, int IT>
 __device__ __forceinline__ void kv_join(const KvTileParams &p, const KvShare &sh, const KvUnit &un, int nrows, int grow0,
-                                        int *s_last, int t, int bar)
+                                        int *s_last, int *s_counted, int t, int bar)
 {
     __threadfence();
     bar_sync(bar, NT);
-    const int64_t first = un.u0 / sh.share;
-    const int np = (int)((un.u0 + un.n - 1) / sh.share - first) + 1;
     if (t == 0) {
-        unsigned *tk = p.tickets + first;          // (of the units that begin in a CTA only its last goes on)
-        const bool last = atomicAdd(tk, 1u) == (unsigned)(np - 1);
-        if (last)
-            *tk = 0u;
-        *s_last = last;
+        *s_counted |= kv_piece_bit(un);
+        *s_last = kv_arrive(p, sh, un, false);
     }
     bar_sync(bar, NT);
     if (!*s_last)
         return;
+    const int64_t first = un.u0 / sh.share;
+    const int np = (int)((un.u0 + un.n - 1) / sh.share - first) + 1;
     __threadfence();
     // IT items (four columns of a row) at a time, two pieces of each: the loads are what
     // this takes, and they have to be in flight together.  Piece j lies in slot

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     __shared__ float s_red[2][4][KF_N], s_wred[2][4], s_c[2][KF_N];
     __shared__ KfResult s_result[2][KF_N];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
-    __shared__ int s_last, s_dead;
+    __shared__ int s_last, s_dead, s_counted;
     const int NS = p.stages;
     const KfSmem off = kf_smem<FMT, D>(NS);
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
         kv_init_bars(drained, 2, 1);                       // MMAs of a CTA that has given up
         kv_init_bars(unit_full, KT_UNITS, 1);
         if (lane == 0)
-            s_dead = 0;
+            s_dead = s_counted = 0;
         if (lane < KF_N)
             s_zero[lane] = 0.f;
         mbar_init_fence();
@@ -737,12 +737,14 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                 }
             }
             if (!whole)                                    // (with more in flight than one it spills, which costs every role)
-                kv_join<D, KF_N, 128, 1>(p, sh, un, nrows, grow0, &s_last, t, 3);
+                kv_join<D, KF_N, 128, 1>(p, sh, un, nrows, grow0, &s_last, &s_counted, t, 3);
         }
     }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
+    if (warp == KF_COPY && gone())
+        kv_arrive_failed<KF_N>(p, s_counted);
     if (warp == KF_MMA_S) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     __shared__ float s_wmax[4][4];                         // largest V scale of 32 tokens
     __shared__ __align__(16) KmRow s_row[KM_ROWS];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
-    __shared__ int s_last, s_dead;
+    __shared__ int s_last, s_dead, s_counted;
     const int NS = p.stages;
     const KmSmem off = km_smem<FMT, D>(NS);
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
         kv_init_bars(drained, 2, 1);                       // MMAs of a CTA that has given up
         kv_init_bars(unit_full, KT_UNITS, 1);
         if (lane == 0)
-            s_dead = 0;
+            s_dead = s_counted = 0;
         mbar_init_fence();
     } else if (warp == KM_S) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
             if (!whole && !leave) {
                 if (mine && g == 0)
                     *reinterpret_cast<float2 *>(p.piece_ml + (slot + row) * 2) = make_float2(r.m, r.l);
-                kv_join<D, KM_ROWS, 256, 4>(p, sh, un, nrows, grow0, &s_last, t, 1);
+                kv_join<D, KM_ROWS, 256, 4>(p, sh, un, nrows, grow0, &s_last, &s_counted, t, 1);
             }
             tc_fence_before();
             bar_sync(1, 256);                              // O and s_sum may be written again
@@ -655,6 +655,8 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
+    if (warp == KM_COPY && gone())
+        kv_arrive_failed<KM_ROWS>(p, s_counted);
     if (warp == KM_S) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");

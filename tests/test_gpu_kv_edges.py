@@ -96,3 +96,23 @@ def test_one_workspace_serves_calls_of_every_shape(q4, fmt, prefix):
     for (lens, T, Hq), n in zip(shapes, size):
         want = go(lens, T, Hq, torch.zeros(n, dtype=torch.uint8, device="cuda"))
         np.testing.assert_array_equal(go(lens, T, Hq, one), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,Hq,prefix", GIVE_UP)
+def test_a_workspace_stays_usable_after_a_cta_gave_up(q4, fmt, T, Hq, prefix):
+    go, size = some_calls(q4, fmt, T, Hq, prefix)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = bits(go(workspace=ws))
+    for cta, tiles in ((0, 0), (2, 1), (60, 2), (7, 3)):
+        try:
+            q4.load().q4_test_kv_give_up(cta, tiles)
+            go(workspace=ws)
+            torch.cuda.synchronize()
+        finally:
+            q4.load().q4_test_kv_give_up(-1, 0)
+        assert q4.device_error_flags() == 1
+        assert not ws[:4096].any()
+        out = torch.full(want.shape, torch.nan, dtype=torch.bfloat16, device="cuda")
+        np.testing.assert_array_equal(bits(go(out=out, workspace=ws)), want)
+        assert q4.device_error_flags() == 0
