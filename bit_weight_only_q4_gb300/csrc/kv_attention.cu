@@ -172,6 +172,10 @@ q4_status launch_kv_attention(const DeviceInfo &dev, const KvCacheDesc &c, const
     p.tickets = reinterpret_cast<unsigned *>(ws);
     p.piece_o = at(w.piece_o);
     p.piece_ml = at(w.piece_ml);
+    // A prefix's results lie in the workspace between the two launches: no launch of another host
+    // thread's call, which may use the same stream and workspace, may come in between.
+    static std::mutex launches;
+    std::lock_guard<std::mutex> lock(launches);
     q4_status s;
     if (n == 2) {
         KvTileParams f = p;

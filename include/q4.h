@@ -355,7 +355,8 @@ q4_status q4_kv_attention(const void *q_bf16, int64_t q_stride, const uint8_t *c
  * q4_kv_attention over prefix and own tokens one after the other (query token t of
  * sequence b sees the positions below prefix_len + lengths[b] - tokens + t + 1), but the
  * prefix is read and multiplied once for the whole batch.  A sequence may have no
- * token of its own.
+ * token of its own.  The call makes two launches; no attention call of another host
+ * thread comes between them.
  */
 q4_status q4_kv_attention_shared(const void *q_bf16, int64_t q_stride, const uint8_t *cache,
                                  int format, int pages, int page_size, int kv_heads, int head_dim,

@@ -116,3 +116,36 @@ def test_a_workspace_stays_usable_after_a_cta_gave_up(q4, fmt, T, Hq, prefix):
         out = torch.full(want.shape, torch.nan, dtype=torch.bfloat16, device="cuda")
         np.testing.assert_array_equal(bits(go(out=out, workspace=ws)), want)
         assert q4.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_host_threads_on_one_stream_and_workspace(q4, T):
+    """Calls with a shared prefix (two launches) from several threads on the default stream, beside
+    calls without one: each gets its own results."""
+    import threading
+    rng = np.random.default_rng([23, T])
+    D, H, Hq, page, lens, prefix, fmt = 64, 2, 8, 16, [40, 3, 200], 500, 1
+    cache, table, pp = filled(rng, fmt, D, H, page, lens, prefix=prefix)
+    c, t, p = torch.from_numpy(cache).cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(pp).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    size = q4.kv_attention_workspace_bytes(fmt, H, D, len(lens), T, Hq, prefix)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    qs = [bf16(rng.standard_normal((len(lens), T, Hq, D))).cuda() for _ in range(4)]
+
+    def go(i):
+        if i == 3:
+            return q4.q4_kv_attention(qs[i], c, t, n, fmt, workspace=ws)
+        return q4.q4_kv_attention_shared(qs[i], c, p, prefix, t, n, fmt, workspace=ws)
+
+    want = [bits(go(i)) for i in range(4)]
+    out = [[] for _ in range(4)]
+    threads = [threading.Thread(target=lambda i=i: out[i].extend(go(i) for _ in range(300))) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    for got, w in zip(out, want):
+        assert len(got) == 300
+        for o in got:
+            np.testing.assert_array_equal(bits(o), w)
