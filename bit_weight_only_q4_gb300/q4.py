@@ -22,6 +22,7 @@ LAYOUT_INT4G128 = 0
 LAYOUT_NVFP4 = 1
 CACHE_INT8 = 0
 CACHE_INT4 = 1
+KV_COUNTER_BYTES = 4096
 FLAG_PDL = 0x1
 FLAG_FORCE_CUDA_CORE = 0x2
 FLAG_FORCE_TENSOR_CORE = 0x4
@@ -168,6 +169,53 @@ def _ws_args(ws):
     if ws is None:
         return None, 0
     return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _on(stream):
+    """Allocations made inside belong to the stream that the call runs on, so that neither
+    their fill nor their reuse by the allocator overlaps the call."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _capture_id(handle, stream):
+    """Nonzero, and the same for one capture, while the call's stream is being captured into a graph."""
+    if stream is None and not torch.cuda.is_current_stream_capturing():
+        return 0
+    if not handle:                       # (the legacy default stream cannot be)
+        return 0
+    state, number = ctypes.c_int(0), ctypes.c_ulonglong(0)
+    status = load().cudaStreamGetCaptureInfo(ctypes.c_void_p(handle), ctypes.byref(state),
+                                             ctypes.byref(number), None, None, None, None)
+    return number.value if status == 0 and state.value == 1 else 0
+
+
+# A graph keeps the addresses of the workspaces that its calls used, and nothing else of
+# them: what a captured call has been given is never freed (by its address), and what a
+# capture had to make for itself lies in the graph's own memory, filled by the graph.
+_ws_held: dict = {}
+_ws_graph: dict = {}
+
+
+def _new_workspace(n, zeroed, device, stream):
+    with _on(stream) if stream is not None else contextlib.nullcontext():
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:zeroed].zero_()
+    return ws
+
+
+def _graph_workspace(capture, key, n, zeroed, device, stream):
+    """For a call that is captured before any has made a workspace that would do: one for all such
+    calls of the capture, and for no others, for its fill has not run yet."""
+    last = _ws_graph.get(key)
+    if last is not None and last[0] == capture and last[1].numel() >= n:
+        return last[1]
+    ws = _new_workspace(n, zeroed, device, stream)
+    if len(_ws_graph) >= 64:
+        _ws_graph.clear()
+    _ws_graph[key] = capture, ws
+    return ws
 
 
 # Workspaces the binding supplies when the caller passes none: one per (device,
@@ -369,14 +417,6 @@ def _kv_stream(stream, t):
     return _stream(stream)
 
 
-def _on(stream):
-    """Allocations made inside belong to the stream that the call runs on, so that neither
-    their fill nor their reuse by the allocator overlaps the call."""
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
-
-
 def _kv_empty(shape, like, stream):
     if stream is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
@@ -502,19 +542,25 @@ def kv_attention_workspace_bytes(fmt, kv_heads, head_dim, batch, tokens, q_heads
                                                       q_heads, prefix_len))
 
 
-def _kv_workspace(key, q, stream):
-    """As _default_workspace: one per device, stream and call shape, zero-filled once (and one of
-    its own for a call that is captured before any has made it)."""
-    n = kv_attention_workspace_bytes(*key[3:])
-    if n == 0:
-        return None
-    with _on(stream) if stream is not None else contextlib.nullcontext():
-        ws = torch.zeros(n, dtype=torch.uint8, device=q.device)
-        if torch.cuda.is_current_stream_capturing():
-            return ws                    # its fill is part of the graph, and has not run yet
-    if len(_ws_cache) >= 64:
-        _ws_cache.clear()
-    _ws_cache[key] = ws
+# Workspaces of attention calls: one per (device, stream), for calls of every shape.
+_kv_ws: dict = {}
+
+
+def _kv_workspace(n, device, handle, stream):
+    key = (device.index, handle)
+    ws = _kv_ws.get(key)
+    capture = _capture_id(handle, stream)
+    if ws is not None and ws.numel() >= n:
+        if capture:
+            _ws_held[ws.data_ptr()] = ws
+        return ws
+    if capture:
+        return _graph_workspace(capture, key, n, KV_COUNTER_BYTES, device, stream)
+    # (a list of growing calls makes a few, not one for each)
+    ws = _new_workspace(n if ws is None else max(n, 2 * ws.numel()), KV_COUNTER_BYTES, device, stream)
+    if len(_kv_ws) >= 64:
+        _kv_ws.clear()
+    _kv_ws[key] = ws
     return ws
 
 
@@ -532,8 +578,9 @@ def _kv_attention(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, 
         batch, width = _kv_ints(page_table, "page_table", 2)
         if batch != B or _kv_ints(lengths, "lengths", 1)[0] != B:
             raise ValueError(f"page_table must be [batch, width] and lengths [batch], q has {B} sequences")
-        plan = _kv_plan(key, (row, geo, width, B, T, Hq, D, D**-0.5 if D else 1.0))
-    row, geo, width, B, T, Hq, D, s = plan
+        size = kv_attention_workspace_bytes(fmt, geo[3], D, B, T, Hq, prefix_len)
+        plan = _kv_plan(key, (row, geo, width, B, T, Hq, D, D**-0.5 if D else 1.0, size))
+    row, geo, width, B, T, Hq, D, s, size = plan
     if out is None:
         out = _kv_empty(shape, q, stream)
     elif _cuda(out, "out", torch.bfloat16).shape != shape:
@@ -541,11 +588,8 @@ def _kv_attention(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, 
     if B * T * Hq == 0:
         return out
     handle = _kv_stream(stream, q)
-    if workspace is None:
-        key = (q.get_device(), handle, "kv", fmt, geo[3], D, B, T, Hq, prefix_len)
-        workspace = _ws_cache.get(key)
-        if workspace is None:
-            workspace = _kv_workspace(key, q, stream)
+    if workspace is None and size:
+        workspace = _kv_workspace(size, q.device, handle, stream)
     wp, wn = _ws_args(workspace)
     if scale is not None:
         s = float(scale)

@@ -149,3 +149,63 @@ def test_host_threads_on_one_stream_and_workspace(q4, T):
         assert len(got) == 300
         for o in got:
             np.testing.assert_array_equal(bits(o), w)
+
+
+@pytest.mark.parametrize("prefix", [0, 130])
+@pytest.mark.parametrize("explicit", [False, True])
+def test_a_graph_keeps_its_workspace(q4, prefix, explicit):
+    """A call captured after an eager one, then a hundred calls of other shapes and memory that is taken and
+    filled: the replay gives the same bits and touches nothing of that memory."""
+    rng = np.random.default_rng([24, prefix])
+    D, H, Hq, page, lens, fmt = 128, 2, 8, 32, [9000, 700], 1
+    cache, table, pp = filled(rng, fmt, D, H, page, lens, prefix=prefix)
+    c, t, p = torch.from_numpy(cache).cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(pp).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = bf16(rng.standard_normal((2, 1, Hq, D))).cuda()
+    big = bf16(rng.standard_normal((2, 100, 4 * Hq, D))).cuda()
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    kw = dict(stream=side) if explicit else {}
+
+    def go(q, prefix, **kw):
+        return q4.q4_kv_attention_shared(q, c, p, prefix, t, n, fmt, **kw) if prefix else \
+            q4.q4_kv_attention(q, c, t, n, fmt, **kw)
+
+    with torch.cuda.stream(side):
+        want = bits(go(q, prefix, **kw))
+        with torch.cuda.graph(graph, stream=side):
+            out = go(q, prefix, **kw)
+            assert q4._capture_id(side.cuda_stream, kw.get("stream")) != 0
+        assert q4._capture_id(side.cuda_stream, kw.get("stream")) == 0
+        for T in range(1, 101):                             # more rows, and more room, from call to call
+            go(big[:, :T].contiguous(), max(0, prefix - T), **kw)
+        side.synchronize()
+        torch.cuda.empty_cache()
+        taken = [torch.full((m << 20,), 0x5a, dtype=torch.uint8, device="cuda") for m in (1, 2, 4, 8, 16, 20, 24, 40) * 3]
+        for _ in range(2):
+            graph.replay()
+            np.testing.assert_array_equal(bits(out), want)
+        assert all(bool((x == 0x5a).all()) for x in taken)
+        np.testing.assert_array_equal(bits(go(q, prefix, **kw)), want)
+
+
+def test_calls_of_one_cold_capture(q4):
+    """Several shapes captured before any call has run on the stream, beside eager calls of theirs."""
+    rng = np.random.default_rng(25)
+    D, H, page, lens, fmt = 64, 2, 16, [3000, 90], 0
+    cache, table, _ = filled(rng, fmt, D, H, page, lens)
+    c, t = torch.from_numpy(cache).cuda(), torch.from_numpy(table).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    qs = [bf16(rng.standard_normal((2, T, 8, D))).cuda() for T in (1, 20, 2, 60, 1)]
+    want = [bits(q4.q4_kv_attention(q, c, t, n, fmt)) for q in qs]
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = [q4.q4_kv_attention(q, c, t, n, fmt) for q in qs]
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            for q, w in zip(qs, want):
+                np.testing.assert_array_equal(bits(q4.q4_kv_attention(q, c, t, n, fmt)), w)
+            graph.replay()
+            for o, w in zip(outs, want):
+                np.testing.assert_array_equal(bits(o), w)
