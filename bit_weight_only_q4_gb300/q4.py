@@ -79,6 +79,9 @@ def load() -> ctypes.CDLL:
             "q4_linear_int8": ([p, p, p, p, i, i, i, p], st),
             "q4_quantize_nvfp4": ([p, p, p, p, i, i, p], st),
             "q4_kv_block_bytes": ([i, i], sz),
+            # of the CUDA runtime that the library is linked with
+            "cudaStreamIsCapturing": ([p, p], ctypes.c_int),
+            "cudaStreamGetCaptureInfo": ([p] * 7, ctypes.c_int),
             "q4_kv_write": ([p, i64, p, i64, p, i, p, i, i, i, i, i, p], st),
             "q4_kv_read": ([p, i, i, i, i, i, p, i, p, i, i, p, p, p], st),
             "q4_test_kv_give_up": ([i, i], None),
@@ -181,13 +184,16 @@ def _on(stream):
 
 def _capture_id(handle, stream):
     """Nonzero, and the same for one capture, while the call's stream is being captured into a graph."""
-    if stream is None and not torch.cuda.is_current_stream_capturing():
-        return 0
     if not handle:                       # (the legacy default stream cannot be)
         return 0
-    state, number = ctypes.c_int(0), ctypes.c_ulonglong(0)
-    status = load().cudaStreamGetCaptureInfo(ctypes.c_void_p(handle), ctypes.byref(state),
-                                             ctypes.byref(number), None, None, None, None)
+    lib, state = _lib or load(), ctypes.c_int()
+    if stream is None:
+        if not torch.cuda.is_current_stream_capturing():
+            return 0
+    elif lib.cudaStreamIsCapturing(handle, ctypes.byref(state)) or not state.value:
+        return 0
+    number = ctypes.c_ulonglong()
+    status = lib.cudaStreamGetCaptureInfo(handle, ctypes.byref(state), ctypes.byref(number), None, None, None, None)
     return number.value if status == 0 and state.value == 1 else 0
 
 
@@ -229,17 +235,23 @@ def _graph_workspace(capture, key, n, zeroed, device, stream):
 _ws_cache: dict = {}
 
 
-def _default_workspace(layout: int, M: int, N: int, K: int, device, stream) -> torch.Tensor | None:
+def _default_workspace(layout: int, M: int, N: int, K: int, device, handle, stream) -> torch.Tensor | None:
     n = workspace_bytes(layout, M, N, K)
     if n == 0:
         return None
-    key = (torch.device(device).index, _stream(stream), layout, M, N, K)
+    key = (device.index, handle, layout, M, N, K)
     ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < n:     # (a launch flag can change the size)
-        if len(_ws_cache) >= 64:        # many distinct shapes: start over (memory is
-            _ws_cache.clear()           # returned in stream order by the allocator)
-        ws = torch.zeros(n, dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+    capture = _capture_id(handle, stream)
+    if ws is not None and ws.numel() >= n:       # (a launch flag can change the size)
+        if capture:
+            _ws_held[ws.data_ptr()] = ws
+        return ws
+    if capture:
+        return _graph_workspace(capture, key, n, n, device, stream)
+    if len(_ws_cache) >= 64:            # many distinct shapes: start over (memory is
+        _ws_cache.clear()               # returned in stream order by the allocator)
+    ws = _new_workspace(n, n, device, stream)
+    _ws_cache[key] = ws
     return ws
 
 
@@ -253,11 +265,12 @@ def q4_linear_int4g128(x, qweight, scale, minv, y=None, workspace=None, stream=N
     N = qweight.shape[0]
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    handle = _stream(stream)
     if workspace is None:
-        workspace = _default_workspace(LAYOUT_INT4G128, M, N, K, x.device, stream)
+        workspace = _default_workspace(LAYOUT_INT4G128, M, N, K, x.device, handle, stream)
     wp, wn = _ws_args(workspace)
     _check(load().q4_linear_int4g128(_ptr(x), _ptr(qweight), _ptr(scale), _ptr(minv), _ptr(y),
-                                     M, N, K, wp, wn, _stream(stream)))
+                                     M, N, K, wp, wn, handle))
     return y
 
 
@@ -287,11 +300,12 @@ def q4_linear_nvfp4(x, codes, scale_e4m3, global_scale, y=None, workspace=None, 
     N = codes.shape[0]
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    handle = _stream(stream)
     if workspace is None:
-        workspace = _default_workspace(LAYOUT_NVFP4, M, N, K, x.device, stream)
+        workspace = _default_workspace(LAYOUT_NVFP4, M, N, K, x.device, handle, stream)
     wp, wn = _ws_args(workspace)
     _check(load().q4_linear_nvfp4(_ptr(x), _ptr(codes), _ptr(scale_e4m3), _ptr(global_scale),
-                                  _ptr(y), M, N, K, wp, wn, _stream(stream)))
+                                  _ptr(y), M, N, K, wp, wn, handle))
     return y
 
 

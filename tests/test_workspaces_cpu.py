@@ -2,6 +2,7 @@
 host tensors and a capture that is only said to be one."""
 from __future__ import annotations
 
+import contextlib
 import gc
 import weakref
 
@@ -65,3 +66,47 @@ def test_a_capture_that_comes_first_has_one_of_its_own(capture):
     assert attend(10_000) is eager
     other = attend(12_000)
     assert other is not larger and other is not eager       # another graph's
+
+
+def project(M, stream=9):
+    return q4._default_workspace(q4.LAYOUT_INT4G128, M, 2048, 2048, CPU, stream, stream)
+
+
+@pytest.fixture
+def linear(capture, monkeypatch):
+    monkeypatch.setattr(q4, "workspace_bytes", lambda layout, M, N, K: 64 * M)
+    monkeypatch.setattr(q4, "_on", lambda stream: contextlib.nullcontext())
+    return capture
+
+
+def test_a_linear_call_keeps_what_its_capture_was_given(linear):
+    a = weakref.ref(project(1))
+    linear[0] = 4
+    assert project(1) is a()
+    linear[0] = 0
+    for M in range(2, 200):
+        project(M)
+    gc.collect()
+    assert a() is not None
+
+
+def test_a_linear_call_captured_first_leaves_nothing_to_eager_calls(linear):
+    linear[0] = 4
+    a = project(3)
+    assert project(3) is a
+    linear[0] = 0
+    assert project(3) is not a                              # its fill has not run
+
+
+def test_a_workspace_is_filled_on_the_call_s_stream(linear, monkeypatch):
+    inside = []
+
+    @contextlib.contextmanager
+    def on(stream):
+        inside.append(stream)
+        yield
+        inside.append(None)
+
+    monkeypatch.setattr(q4, "_on", on)
+    project(5, 77)
+    assert inside == [77, None]
