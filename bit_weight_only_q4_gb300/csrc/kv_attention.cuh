@@ -357,7 +357,8 @@ __device__ __forceinline__ void kv_row_to_tile(uint32_t codes, const KvRowAt<FMT
 
 // ------------------------------------------------------------------ work list
 // Units in list order: sequence, tile of rows, key head.  A unit's tiles cover the
-// tokens that its last row sees.
+// tokens that its last row sees.  A sequence's length (len) may go past what its row of the table
+// holds (cap): query tokens see by the length, of the tokens that are there.
 struct KvWalk {
     int b, rt, len;
     int64_t base;                // first tile of (b, rt, head 0) in the list
@@ -367,11 +368,12 @@ struct KvWalk {
 template <int N>
 __device__ __forceinline__ int kv_unit_tokens(const KvTileParams &p, int len, int rt)
 {
-    if (p.prefix_len > 0 || p.tokens == 1)
-        return len;
-    const int last = (rt + 1) * N < p.rows ? (rt + 1) * N - 1 : p.rows - 1;
-    const int lim = len - p.tokens + p.by_group(last) + 1;
-    return lim < 0 ? 0 : lim;
+    int lim = len;
+    if (p.prefix_len <= 0 && p.tokens > 1) {
+        const int last = (rt + 1) * N < p.rows ? (rt + 1) * N - 1 : p.rows - 1;
+        lim += p.by_group(last) + 1 - p.tokens;
+    }
+    return lim < 0 ? 0 : (lim < p.cap ? lim : (int)p.cap);
 }
 
 __device__ __forceinline__ int kv_tiles_of(int ntok)
@@ -382,7 +384,7 @@ __device__ __forceinline__ int kv_tiles_of(int ntok)
 // What a CTA has of one unit: tiles k0 .. k1 - 1 of its n.
 struct KvUnit {
     int b, rt, h, ntok, k0, k1, n;
-    int len;                     // cached tokens of the sequence (of the prefix)
+    int len;                     // length of the sequence (of the prefix)
     int64_t u0;                  // the unit's first tile in the list
 };
 
@@ -397,7 +399,7 @@ __device__ __forceinline__ int kv_length(const KvTileParams &p, int b)
     if (p.prefix_len > 0)
         return p.prefix_len;
     const int len = p.lengths[b];
-    return len < 0 ? 0 : (len < p.cap ? len : (int)p.cap);
+    return len < 0 ? 0 : len;
 }
 
 // Tiles of all units of a sequence.
@@ -741,7 +743,7 @@ __device__ __forceinline__ void kv_join(const KvTileParams &p, const KvShare &sh
     }
 }
 
-// Cached tokens of the list that row `grow` (among all rows) sees; len: those of its sequence.
+// Tokens of the list that row `grow` (among all rows) sees, at most; len: the length of its sequence.
 __device__ __forceinline__ int kv_row_limit(const KvTileParams &p, int grow, int len)
 {
     const int token = p.by_group(grow);

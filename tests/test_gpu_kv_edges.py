@@ -209,3 +209,39 @@ def test_calls_of_one_cold_capture(q4):
             graph.replay()
             for o, w in zip(outs, want):
                 np.testing.assert_array_equal(bits(o), w)
+
+
+def past_the_table(q, cache, table, lens, fmt, scale, prefix_pages=(), prefix=0):
+    """The definition where a length goes past the table: query token t sees the positions below
+    prefix + lengths[b] - tokens + t + 1 of those that the table holds."""
+    B, T, Hq, D = q.shape
+    cap = table.shape[1] * cache.shape[2] * 16
+    out, mag = np.zeros(q.shape), np.zeros(q.shape)
+    for b in range(B):
+        n = min(max(int(lens[b]), 0), cap)
+        k, v, ok = R.read(cache, table[b], n, fmt, D)
+        if prefix:
+            kp, vp, okp = R.read(cache, prefix_pages, prefix, fmt, D)
+            k, v, ok = np.concatenate((kp, k)), np.concatenate((vp, v)), np.concatenate((okp, ok))
+        limits = [prefix + max(int(lens[b]), 0) - T + t + 1 for t in range(T)]
+        out[b], mag[b] = R.attention(q[b], k, v, ok, limits, scale)
+    return out, mag
+
+
+@pytest.mark.parametrize("T,Hq", [(3, 4), (20, 2), (20, 20)])
+@pytest.mark.parametrize("prefix", [0, 70])
+@pytest.mark.parametrize("D", [64, 128])
+def test_query_tokens_of_lengths_past_the_table(q4, D, prefix, T, Hq):
+    """The table holds 48 tokens of each sequence: all of them are seen where the length lets the
+    query token see them, and the token's own place may lie past the table."""
+    rng = np.random.default_rng([26, D, T, Hq])
+    fmt, H, page = 0, 2, 16
+    cache, table, pp = filled(rng, fmt, D, H, page, [48] * 7, prefix=prefix)
+    lens = [100, 48, 49, 48 + T, 48 + T - 1, 2**31 - 1, -5]
+    q = bf16(1.5 * rng.standard_normal((7, T, Hq, D))).float().numpy()
+    q4.device_error_flags(clear=True)
+    out = call(q4, q, cache, table, lens, fmt, None, pp, prefix)
+    assert q4.device_error_flags() == 4
+    got = out.float().cpu().numpy().astype(np.float64)
+    want, mag = past_the_table(q, cache, table, lens, fmt, D**-0.5, pp, prefix)
+    assert (np.abs(got - want) <= 2.0**-8 * np.abs(want) + 2.0**-9 * mag + 2.0**-126).all()
