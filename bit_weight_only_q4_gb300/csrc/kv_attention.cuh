@@ -644,16 +644,22 @@ __device__ __forceinline__ int64_t kv_piece_slot(const KvUnit &un)
     return 2 * (int64_t)blockIdx.x + (un.k0 == 0 ? 1 : 0);
 }
 
+// The CTA that a unit begins in, and how many share it.
+struct KvSharers {
+    int64_t first;
+    int n;
+    __device__ __forceinline__ KvSharers(const KvShare &sh, const KvUnit &un)
+        : first(un.u0 / sh.share), n((int)((un.u0 + un.n - 1) / sh.share - first) + 1) {}
+};
+
 // Counts this CTA in at a unit that it does not have whole; true if it is the last of them
 // and all have their piece.  Every CTA of a unit is counted, one that has given up with a mark
 // (bit 16 and up): the counter is zero again when the launch ends, whatever has happened.
-__device__ __forceinline__ bool kv_arrive(const KvTileParams &p, const KvShare &sh, const KvUnit &un, bool failed)
+__device__ __forceinline__ bool kv_arrive(const KvTileParams &p, const KvSharers &by, bool failed)
 {
-    const int64_t first = un.u0 / sh.share;
-    const int np = (int)((un.u0 + un.n - 1) / sh.share - first) + 1;
-    unsigned *tk = p.tickets + first;              // (of the units that begin in a CTA only its last goes on)
+    unsigned *tk = p.tickets + by.first;           // (of the units that begin in a CTA only its last goes on)
     const unsigned old = atomicAdd(tk, failed ? 0x10001u : 1u);
-    if ((old & 0xffffu) != (unsigned)(np - 1))
+    if ((old & 0xffffu) != (unsigned)(by.n - 1))
         return false;
     *tk = 0u;
     return !failed && (old >> 16) == 0u;
@@ -675,7 +681,7 @@ __device__ __forceinline__ void kv_arrive_failed(const KvTileParams &p, int coun
         const KvUnit un = kv_next_unit<N>(p, walk, f, sh.c1);
         f += un.k1 - un.k0;
         if (un.k1 - un.k0 < un.n && !(counted & kv_piece_bit(un)) && (threadIdx.x & 31) == 0)
-            kv_arrive(p, sh, un, true);
+            kv_arrive(p, KvSharers(sh, un), true);
     }
 }
 
@@ -686,16 +692,17 @@ __device__ __forceinline__ void kv_join(const KvTileParams &p, const KvShare &sh
                                         int *s_last, int *s_counted, int t, int bar)
 {
     __threadfence();
+    const KvSharers by(sh, un);                    // (before the barrier: two long divisions)
     bar_sync(bar, NT);
     if (t == 0) {
         *s_counted |= kv_piece_bit(un);
-        *s_last = kv_arrive(p, sh, un, false);
+        *s_last = kv_arrive(p, by, false);
     }
     bar_sync(bar, NT);
     if (!*s_last)
         return;
-    const int64_t first = un.u0 / sh.share;
-    const int np = (int)((un.u0 + un.n - 1) / sh.share - first) + 1;
+    const int64_t first = by.first;
+    const int np = by.n;
     __threadfence();
     // IT items (four columns of a row) at a time, two pieces of each: the loads are what
     // this takes, and they have to be in flight together.  Piece j lies in slot

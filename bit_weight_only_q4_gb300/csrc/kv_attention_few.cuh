@@ -223,8 +223,6 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             }
             __syncwarp();
         }
-        if (gone_all())
-            kv_mma_drain(drained, dead);
     } else if (warp == KF_MMA_O) {
         // ------------------------------------------------ MMAs: O^T += V^T P^T
         // A is M-major: 64-column halves 16 KB apart, groups of 8 tokens 1 KB apart (D = 64 has
@@ -268,8 +266,6 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
             __syncwarp();
             begun |= 1u << g;
         }
-        if (gone_all())
-            kv_mma_drain(drained + 8u, dead);
     } else if (warp == KF_Q) {
         // ----------------------------------------- q: prescaled fp16, row data
         // (of the first NR rows: a column of S^T or O^T takes nothing from another one's q)
@@ -743,8 +739,14 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (warp == KF_COPY && gone())
-        kv_arrive_failed<KF_N>(p, s_counted);
+    if (gone()) {                // (here, not in the warps' roles: there it cost the MMA loops their uniform registers)
+        if (warp == KF_COPY)
+            kv_arrive_failed<KF_N>(p, s_counted);
+        else if (warp == KF_MMA_S || warp == KF_MMA_O)
+            kv_mma_drain(drained + (warp == KF_MMA_O ? 8u : 0u), dead);
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == KF_MMA_S) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");

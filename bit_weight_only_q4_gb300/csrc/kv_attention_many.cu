@@ -611,8 +611,6 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                 __syncwarp();
             }
         }
-        if (gone_all())
-            kv_mma_drain(drained, dead);
         } else if (warp == KM_O) {
         // ------------------------------------------------------- MMAs: O += P V
         constexpr uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);   // B is N-major
@@ -648,15 +646,19 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                 __syncwarp();
             }
         }
-        if (gone_all())
-            kv_mma_drain(drained + 8u, dead);
         }
     }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (warp == KM_COPY && gone())
-        kv_arrive_failed<KM_ROWS>(p, s_counted);
+    if (gone()) {                // (here, not in the warps' roles: there it cost the MMA loops their uniform registers)
+        if (warp == KM_COPY)
+            kv_arrive_failed<KM_ROWS>(p, s_counted);
+        else if (warp == KM_S || warp == KM_O)
+            kv_mma_drain(drained + (warp == KM_O ? 8u : 0u), dead);
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == KM_S) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");
