@@ -14,9 +14,10 @@
 // so scales never touch codes, and both products run on codes that are exact in fp16.
 // q' is q times a power of two that brings the largest finite value into
 // [2^14, 2^15); f undoes it.  p vs enters the second product in fp16 (11 bits).  The
-// reference m_i is the largest score so far plus E - 6, with 2^E the power of two below
-// the largest vs so far: the largest p vs is then about 2^6.  It moves (and what has been
-// summed is rescaled) only when that exceeds it by more than 8, so products stay in the
+// reference m_i is the largest s_ij + E_j - 6 so far among the tokens that the row sees, with 2^E_j
+// the power of two below vs_j: the largest p vs is then about 2^6, whatever scores and scales it is
+// made of, and no token that the row does not see has a part in it.  It moves (and what has
+// been summed is rescaled) only when that exceeds it by more than 8, so products stay in the
 // range of fp16 and keep their 11 bits down to 2^-20 of the largest.  Scores, statistics and sums
 // are fp32; pieces of a row are added up by their references, whatever those are.
 // A row of the cache whose V scale is not finite counts as one whose K scale is NaN: it
@@ -217,7 +218,7 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool v)
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// E - 6 for a largest V scale of v >= 0 (-36 for 0), see above.
+// E - 6 for a V scale of v >= 0 (-36 for 0), see above.
 __device__ __forceinline__ float kv_scale_level(float v)
 {
     return v > 0.f ? (float)((int)(__float_as_uint(v) >> 23) - 133) : -36.f;

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
     __shared__ __align__(16) KfSums s_sums[2][2];          // [unit][group]
     __shared__ __align__(16) float s_nm[2][2][KF_N];       // minus the references: [group][by turns]
     __shared__ __align__(16) float s_zero[KF_N];
-    __shared__ float s_red[2][4][KF_N], s_wred[2][4], s_c[2][KF_N];
+    __shared__ float s_red[2][4][KF_N], s_c[2][KF_N];
     __shared__ KfResult s_result[2][KF_N];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
     __shared__ int s_last, s_dead, s_counted;
@@ -463,7 +463,6 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
 #pragma unroll
             for (int j = 0; j < (L::I8 ? 1 : NR / 2); ++j)
                 off2[j] = 0ull;
-            float level = -36.f;                           // E - 6
             bool first = true;
 #pragma unroll 1
             for (int it = i + ((i ^ grp) & 1); it < end && !leave; it += 2) {
@@ -530,29 +529,19 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                     // Move the references; rescale what has been summed.
                     {
                         float z[NR];
+                        const float level = kv_scale_level(fabsf(info.z));
 #pragma unroll
                         for (int j = 0; j < NR / 2; ++j)
-                            unpack2(x2[j], z[2 * j], z[2 * j + 1]);
+                            unpack2(add2(x2[j], pack2(level, level)), z[2 * j], z[2 * j + 1]);
                         int idx;
                         const float top = warp_max_transpose<NR>(z, lane, idx);
                         s_red[grp][gw][idx] = top;         // lanes of one idx hold one value
                     }
-                    // (magnitudes order as their bits do)
-                    const uint32_t wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(info.z)));
-                    if (lane == 0)
-                        s_wred[grp][gw] = gone() ? -1.f : __uint_as_float(wtop);
-                    bar_sync(bar_id, 128);
-                    float wm = 0.f;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        leave = leave || s_wred[grp][w] < 0.f;
-                        wm = fmaxf(wm, s_wred[grp][w]);
-                    }
-                    level = fmaxf(level, kv_scale_level(wm));
+                    leave = bar_or(bar_id, 128, gone());
                     if (gtid < NR) {
                         const float old = first ? -INFINITY : -s_nm[grp][nmb][gtid];
                         const float m = fmaxf(fmaxf(fmaxf(s_red[grp][0][gtid], s_red[grp][1][gtid]),
-                                                    fmaxf(s_red[grp][2][gtid], s_red[grp][3][gtid])) + level, old);
+                                                    fmaxf(s_red[grp][2][gtid], s_red[grp][3][gtid])), old);
                         s_nm[grp][nmb ^ 1][gtid] = -m;
                         s_c[grp][gtid] = old == -INFINITY ? 0.f : ex2(old - m);
                     }

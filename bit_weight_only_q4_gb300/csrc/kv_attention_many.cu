@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 19 + KT_UNITS];
     __shared__ KvUnit s_unit[KT_UNITS];
     __shared__ float s_wmax[4][4];                         // largest V scale of 32 tokens
+    __shared__ __align__(16) float s_level[4][KT_TOKENS];  // see kv_scale_level
     __shared__ __align__(16) KmRow s_row[KM_ROWS];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
     __shared__ int s_last, s_dead, s_counted;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
             }
             const int lim = mine ? kv_row_limit(p, grow0 + row, un.len) : 0x7fffffff;
             const int least = __reduce_min_sync(0xffffffffu, lim);
-            float m = -INFINITY, level = -36.f;            // reference; E - 6
+            float m = -INFINITY;                           // reference
             f32x2 l2 = 0ull, l2b = 0ull, off2 = 0ull, off2b = 0ull;        // (two chains each)
             const f32x2 qs2 = pack2(qs, qs), f2 = pack2(f, f);
             bool first = true;
@@ -306,8 +307,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                     }
                 }
                 if (careful) {
-                    // scores over f, and their maximum
-                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};      // (short chains)
+                    // scores over f, then what the reference goes by
 #pragma unroll
                     for (int j = 0; j < KM_HALF; j += 4) {
                         f32x2 ka, kb;
@@ -327,27 +327,34 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                         unpack2(a, x[0], x[1]);
                         unpack2(b, x[2], x[3]);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            tops[y] = fmaxf(tops[y], x[y]);
+                        for (int y = 0; y < 4; ++y)
                             v[j + y] = __float_as_uint(x[y]);
-                        }
                     }
                     if (masked) {
                         const uint32_t blocks = mask >> (4 * g);
                         const int lim1 = lim < ntok ? lim : ntok;
-                        tops[0] = tops[1] = tops[2] = tops[3] = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < KM_HALF; ++j) {
+                        for (int j = 0; j < KM_HALF; ++j)
                             if (pos0 + j >= lim1 || !((blocks >> (j / KV_BLOCK)) & 1u))
                                 v[j] = 0xff800000u;
-                            tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(v[j]));
-                        }
                     }
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    level = fmaxf(level, kv_scale_level(fmaxf(s_wmax[i & 3][2 * g], s_wmax[i & 3][2 * g + 1])));
-                    const float want = fmaf(top, f, level);
-                    const bool move = want > m + 8.f || (first && top > -INFINITY);
-                    if (__any_sync(0xffffffffu, move)) {
+                    const uint32_t lv = smem_u32(s_level[i & 3]) + (uint32_t)g * (KM_HALF * 4);
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};      // (short chains)
+#pragma unroll
+                    for (int j = 0; j < KM_HALF; j += 4) {
+                        f32x2 a, b;
+                        lds_f32x4(lv + 4u * j, a, b);
+                        a = fma2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2, a);
+                        b = fma2(pack2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f2, b);
+                        float x[4];
+                        unpack2(a, x[0], x[1]);
+                        unpack2(b, x[2], x[3]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            tops[y] = fmaxf(tops[y], x[y]);
+                    }
+                    const float want = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    if (__any_sync(0xffffffffu, want > m + 8.f)) {
                         const float old = m;
                         m = fmaxf(m, want);
                         const float c = old == -INFINITY ? 0.f : ex2(old - m);
@@ -551,6 +558,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                 KmScales &out = s_scales[i & 3];
                 out.ks[tok] = sc.x;
                 out.vs[tok] = sc.z;
+                s_level[i & 3][tok] = kv_scale_level(fabsf(sc.z));
                 if constexpr (!L::I8) {
                     out.km[tok] = sc.y;
                     out.vm[tok] = sc.w;

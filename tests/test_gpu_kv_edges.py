@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import kv_reference as R
-from tests.test_gpu_kv_cache import FMTS, bf16, bits, call, filled, q4  # noqa: F401
+from tests.test_gpu_kv_cache import FMTS, bf16, bits, call, filled, q4, rows  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -245,3 +245,53 @@ def test_query_tokens_of_lengths_past_the_table(q4, D, prefix, T, Hq):
     got = out.float().cpu().numpy().astype(np.float64)
     want, mag = past_the_table(q, cache, table, lens, fmt, D**-0.5, pp, prefix)
     assert (np.abs(got - want) <= 2.0**-8 * np.abs(want) + 2.0**-9 * mag + 2.0**-126).all()
+
+
+def within(out, q, caches, table, lens, fmt, scale):
+    """The bound of test_gpu_kv_cache.py, in units of which the worst element is off."""
+    got = out.float().cpu().numpy().astype(np.float64)
+    want, mag = past_the_table(q, caches, table, lens, fmt, scale)
+    return float((np.abs(got - want) / (2.0**-8 * np.abs(want) + 2.0**-9 * mag + 2.0**-126)).max())
+
+
+def put(cache, pages, page, at, k, v, fmt):
+    """Rows k, v [n, H, D] as tokens at, at + 1, ... of a list of pages."""
+    pos = at + np.arange(len(k))
+    R.write(cache, pages[pos // page].astype(np.int64) * page + pos % page, k, v, fmt, page)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq", [(4, 4), (40, 4)])
+@pytest.mark.parametrize("power", [14, 22, 30])
+def test_later_tokens_take_no_digits_from_earlier_rows(q4, fmt, D, T, Hq, power):
+    """A chunk whose last token's V is 2^power times the others': the rows that do not see it give
+    the bits that they give without it."""
+    rng = np.random.default_rng([27, fmt, D, T])
+    H, page, n = 2, 16, 100
+    cache, table, _ = filled(rng, fmt, D, H, page, [n])
+    k, v = rows(rng, n, H, D), rows(rng, n, H, D) * np.float32(2.0**-14)
+    put(cache, table[0], page, 0, k, v, fmt)
+    q = bf16(1.5 * rng.standard_normal((1, T, Hq, D))).float().numpy()
+    want = bits(call(q4, q, cache, table, [n], fmt))[:, :-1]
+    put(cache, table[0], page, n - 1, k[-1:], v[-1:] * np.float32(2.0**power), fmt)
+    np.testing.assert_array_equal(bits(call(q4, q, cache, table, [n], fmt))[:, :-1], want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq", [(1, 4), (1, 40), (9, 4)])
+@pytest.mark.parametrize("small,weight,up", [(-6, 24, 0), (-14, 24, 0), (-20, 24, 0), (-24, 40, 8), (-28, 44, 10)])
+def test_the_token_that_counts_may_have_the_smallest_values(q4, D, T, Hq, small, weight, up):
+    """One token outweighs all others by far and has a V 2^small times theirs
+    (which are of the size 2^up)."""
+    rng = np.random.default_rng([28, D, T, Hq])
+    fmt, H, page, n = 0, 2, 32, 400
+    cache, table, _ = filled(rng, fmt, D, H, page, [n])
+    k, v = 0.1 * rows(rng, n, H, D), rows(rng, n, H, D) * np.float32(2.0**up)
+    k[77] = 1.0
+    v[77] *= np.float32(2.0**small)
+    put(cache, table[0], page, 0, k, v, fmt)
+    q = bf16(0.1 * rng.standard_normal((1, T, Hq, D)) + 1.0).float().numpy()
+    scale = weight * np.log(2.0) / D                        # 2^weight times the others' weight
+    out = call(q4, q, cache, table, [n], fmt, scale)
+    assert within(out, q, cache, table, [n], fmt, float(np.float32(scale))) <= 1.0
