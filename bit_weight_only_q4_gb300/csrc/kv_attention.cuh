@@ -218,11 +218,16 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool v)
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// E - 6 for a V scale of v >= 0 (-36 for 0), see above.
+// E - 6 for a V scale of v >= 0, see above.  A scale of 0 (a row of one value) makes no product
+// that could leave fp16's range, but p alone has a range too: it is added up in l and, times
+// vm, in the offset.  At -68 such a p is 2^68 at most, and references move before one reaches 2^76
+// (KT_P_TOP): l stays below 2^107 and the offset below 2^123 for any number of tokens.  What weighs
+// 2^68 times less than such a row is lost to fp16, no sooner.
 __device__ __forceinline__ float kv_scale_level(float v)
 {
-    return v > 0.f ? (float)((int)(__float_as_uint(v) >> 23) - 133) : -36.f;
+    return v > 0.f ? (float)((int)(__float_as_uint(v) >> 23) - 133) : -68.f;
 }
+constexpr float KT_P_TOP = 0x1p76f;
 
 // Largest of each of V values over the 32 lanes (see warp_sum_transpose).
 template <int V>

@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                 if (masked && (pos >= ntok || !((mask >> (tok / KV_BLOCK)) & 1u)))
                     pos = 0x7fffffff;
                 const f32x2 ks2 = pack2(info.x, info.x), vs2 = pack2(info.z, info.z);
-                // Products over the references as they are (what = 0).  If one reaches 2^15, or the
-                // unit begins, the group goes round with scores over zero (1), from which the new
+                // Products over the references as they are (what = 0).  If one reaches 2^15 (or, for
+                // a V scale of 0, its p KT_P_TOP), or the unit begins, the group goes round with scores over zero (1), from which the new
                 // references are taken, and then over those (2).
                 f32x2 x2[NR / 2];
                 uint32_t h[NR / 2];
@@ -521,6 +521,13 @@ __global__ void __launch_bounds__(KF_WARPS * 32, 1) kv_few_rows_kernel(const KvT
                             h[j] = *reinterpret_cast<const uint32_t *>(&hh);
                             high = __vmaxu2(high, h[j]);
                         }
+                        if (info.z == 0.f)
+#pragma unroll
+                            for (int j = 0; j < NR / 2; ++j) {
+                                float a, b;
+                                unpack2(x2[j], a, b);
+                                high = fmaxf(a, b) >= KT_P_TOP ? 0x7800u : high;
+                            }
                         if (what == 0 &&
                             !bar_or(bar_id, 128, (high & 0xffffu) >= 0x7800u || high >= 0x78000000u || gone()))
                             break;

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ uint64_t s_bar[2 * KT_MAX_STAGES + 19 + KT_UNITS];
     __shared__ KvUnit s_unit[KT_UNITS];
-    __shared__ float s_wmax[4][4];                         // largest V scale of 32 tokens
+    __shared__ float s_wmax[4][4];                         // largest V scale of 32 tokens, 2^-60 at least
     __shared__ __align__(16) float s_level[4][KT_TOKENS];  // see kv_scale_level
     __shared__ __align__(16) KmRow s_row[KM_ROWS];
     __shared__ uint32_t s_tmem, s_valid[KT_MAX_STAGES], s_vmask[4];
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                         ph[j / 2] = *reinterpret_cast<const uint32_t *>(&h0);
                         ph[j / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
                     }
-                    // (no p vs is above the sum of p times the largest vs)
+                    // (no p vs is above the sum of p times the largest vs, nor a p above KT_P_TOP where that is 0)
                     float sa, sb;
                     unpack2(add2(la, lb), sa, sb);
                     const float wm = fmaxf(s_wmax[i & 3][2 * g], s_wmax[i & 3][2 * g + 1]);
@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(KM_WARPS * 32, 1) kv_many_rows_kernel(const Kv
                     out.km[tok] = sc.y;
                     out.vm[tok] = sc.w;
                 }
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(sc.z)));
+                static_assert(KT_P_TOP * 0x1p-60f >= 65000.f, "the range of p ends with that of the products");
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(sc.z), 0x1p-60f)));
                 if (lane == 0)
                     s_wmax[i & 3][warp & 3] = __uint_as_float(top);
                 if (warp == KM_K && lane == 0)

@@ -331,7 +331,11 @@ q4_status q4_kv_read(const uint8_t *cache, int format, int pages, int page_size,
  * q_heads is a multiple of kv_heads: query heads h * q_heads / kv_heads and on share
  * the keys of head h.  Scores, softmax statistics and sums are fp32; the codes enter the
  * products exactly, q does too (but for elements 2^31 times smaller than the largest of
- * their row), the probabilities (times their row's V scale) as fp16.
+ * their row), the probabilities (times their row's V scale) as fp16: a result's error is
+ * at most 2^-11 of the weighted mean of |code * scale| (int4: |(code - 8) * scale|; what is
+ * left of a value is its row's and is weighted in fp32), and bf16's rounding.  That holds down
+ * to 2^-20 of a row's largest product of probability and V scale, and beside V rows of scale
+ * 0 down to 2^-68 of their probability.
  * lengths is read on the device: nothing on the host depends on it.  batch <= 8192.
  *
  * workspace: at least q4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned,

@@ -295,3 +295,46 @@ def test_the_token_that_counts_may_have_the_smallest_values(q4, D, T, Hq, small,
     scale = weight * np.log(2.0) / D                        # 2^weight times the others' weight
     out = call(q4, q, cache, table, [n], fmt, scale)
     assert within(out, q, cache, table, [n], fmt, float(np.float32(scale))) <= 1.0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq", [(1, 4), (1, 40), (9, 4)])
+@pytest.mark.parametrize("rise,value", [(20, 1.0), (60, -300.0), (84, 1.0), (87, 300.0), (90, -1.0), (91, 300.0), (130, 1.0)])
+def test_constant_values_under_rising_scores(q4, fmt, D, T, Hq, rise, value):
+    """V rows that are one value throughout (int4: scale 0, the minimum says it all), and scores that rise
+    by 2^rise from the first tiles to later ones: the result is that value.  A hundred sequences on
+    the same pages, so that a CTA meets the rise within a unit."""
+    rng = np.random.default_rng([29, fmt, D, T])
+    H, page, n, B = 2, 32, 1000, 100
+    cache, table, _ = filled(rng, fmt, D, H, page, [n])
+    k, v = 0.01 * rows(rng, n, H, D), np.full((n, H, D), value, np.float32)
+    k[500:] += 1.0
+    put(cache, table[0], page, 0, k, v, fmt)
+    table = np.repeat(table, B, 0)
+    q = bf16(0.01 * rng.standard_normal((B, T, Hq, D)) + 1.0).float().numpy()
+    scale = rise * np.log(2.0) / D
+    out = call(q4, q, cache, table, [n] * B, fmt, scale)
+    got = out.float().cpu().numpy()
+    # (weights that add up to one: the bound is 2^-8 |value| + 2^-9 |value|)
+    assert np.isfinite(got).all() and (np.abs(got - value) <= 1.5 * 2.0**-8 * abs(value)).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq", [(1, 4), (1, 40)])
+@pytest.mark.parametrize("weight", [30, 60, 72])
+def test_values_of_zero_beside_others(q4, D, T, Hq, weight):
+    """Tokens whose V is zero outweigh the others by 2^weight: what is left is the others' share."""
+    rng = np.random.default_rng([30, D, T])
+    fmt, H, page, n, B = 0, 2, 32, 1000, 40
+    cache, table, _ = filled(rng, fmt, D, H, page, [n])
+    k, v = np.zeros((n, H, D), np.float32), rows(rng, n, H, D)
+    k[500:] = 1.0
+    v[500:] = 0.0
+    put(cache, table[0], page, 0, k, v, fmt)
+    table = np.repeat(table, B, 0)
+    q = np.ones((B, T, Hq, D), np.float32)
+    scale = weight * np.log(2.0) / D
+    out = call(q4, q, cache, table, [n] * B, fmt, scale)
+    some = slice(0, B, 8)
+    assert within(out[some], q[some], cache, table[some], [n] * len(q[some]), fmt, float(np.float32(scale))) <= 1.0
