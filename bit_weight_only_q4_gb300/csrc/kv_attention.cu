@@ -122,9 +122,6 @@ static q4_status kv_allow_smem(const KvKernel &k)
 
 static q4_status kv_tile_launch(const KvPlan &plan, KvTileParams &p, cudaStream_t st, bool pdl)
 {
-    // a group of units of one (sequence, row tile) is counted in 32 bits
-    if ((p.cap / KT_TOKENS + 1) * p.cache.heads > 0x7fffffff)
-        return fail(Q4_ERR_SHAPE, "table_width * page_size * kv_heads is too large");
     p.rows = (int)plan.rows;
     p.row_tiles = plan.row_tiles;
     p.stages = plan.k.stages;

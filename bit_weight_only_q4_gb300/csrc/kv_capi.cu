@@ -1,5 +1,7 @@
 // C ABI of the paged key/value cache (include/q4.h): host-side validation, then the
 // launches of kv_store.cu and kv_attention.cu.
+#include <algorithm>
+
 #include "kv_cache.cuh"
 
 namespace q4 {
@@ -64,6 +66,10 @@ static q4_status kv_attention(const void *q, int64_t q_stride, const uint8_t *ca
         return fail(Q4_ERR_SHAPE, "batch * tokens * q_heads is too large");
     if (((int64_t)table_width << c.page_shift) > kMaxBlocks - prefix_len)
         return fail(Q4_ERR_SHAPE, "table_width * page_size + prefix_len must stay below 2^31");
+    // the units of one (sequence, row tile), in tiles of 128 tokens, are counted in 31 bits
+    const int64_t most = std::max((int64_t)table_width << c.page_shift, (int64_t)prefix_len);
+    if ((most / 128 + 1) * kv_heads > kMaxBlocks)
+        return fail(Q4_ERR_SHAPE, "table_width * page_size * kv_heads or prefix_len * kv_heads is too large");
     if (!(scale - scale == 0.f))
         return fail(Q4_ERR_ARG, "scale must be finite");
     if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(table, 4) || !aligned_to(lengths, 4) ||

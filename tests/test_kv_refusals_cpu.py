@@ -1,0 +1,35 @@
+"""Refusals of the attention entry points that come before any launch (fake pointers are never
+dereferenced, and no device is asked for)."""
+import ctypes
+
+import pytest
+
+from bit_weight_only_q4_gb300 import build as q4build
+from bit_weight_only_q4_gb300 import q4
+
+FAKE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    q4build.build()
+    return q4.load()
+
+
+def shared(lib, heads, width, page=16, prefix=20, D=128):
+    return lib.q4_kv_attention_shared(FAKE, heads * D, FAKE, 0, 4, page, heads, D, FAKE, prefix, FAKE, width, FAKE, 1, 1,
+                                      heads, ctypes.c_float(0.1), FAKE, None, 0, None)
+
+
+def single(lib, heads, width, page=16, D=128):
+    return lib.q4_kv_attention(FAKE, heads * D, FAKE, 0, 4, page, heads, D, FAKE, width, FAKE, 1, 1, heads,
+                               ctypes.c_float(0.1), FAKE, None, 0, None)
+
+
+def test_tables_of_too_many_tiles_are_refused_before_the_first_launch(lib):
+    """128 tokens a tile: (capacity / 128 + 1) * kv_heads has to stay below 2^31, for the table and the prefix."""
+    wide = (1 << 27) - 32                                   # 2^31 - 512 tokens
+    assert single(lib, 256, wide) == 2 and shared(lib, 256, wide) == 2
+    assert b"kv_heads" in lib.q4_last_error_string()
+    assert shared(lib, 256, 1, prefix=(1 << 31) - 1000) == 2
+    assert b"kv_heads" in lib.q4_last_error_string()
