@@ -412,11 +412,11 @@ __device__ __forceinline__ int kv_length(const KvTileParams &p, int b)
 template <int N>
 __device__ __forceinline__ int64_t kv_tiles_of_sequence(const KvTileParams &p, int len)
 {
-    int n = 0;
+    int64_t n = 0;                                 // (a prompt of some millions in one call passes 31 bits)
 #pragma unroll 1
     for (int rt = 0; rt < p.row_tiles; ++rt)
         n += kv_tiles_of(kv_unit_tokens<N>(p, len, rt));
-    return (int64_t)n * p.cache.heads;
+    return n * p.cache.heads;
 }
 
 // Every warp counts the tiles of all units for itself: no warp waits for another before
