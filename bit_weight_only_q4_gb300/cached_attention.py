@@ -7,7 +7,8 @@ single tokens from a captured CUDA graph.
 The layer is two projections around three calls: the rows of K and V are written into the
 cache straight from the fused q|k|v projection's output, attention reads them where they
 lie (what the streams share once for all of them), and the output projection follows.
-Positions are the caller's: a model with rotary positions turns q and k in between.
+Positions are the caller's: a model with rotary positions calls project(), turns q and k, and
+hands them to attend().
 """
 from __future__ import annotations
 
@@ -36,10 +37,13 @@ class CachedAttention:
         return y[:, :n].view(B, T, n, D), y[:, n:n + H], y[:, n + H:]
 
     def __call__(self, x, slots, table, lengths, prefix_pages=None, prefix_len=0):
+        """project() and attend()."""
+        return self.attend(*self.project(x), slots, table, lengths, prefix_pages, prefix_len)
+
+    def attend(self, q, k, v, slots, table, lengths, prefix_pages=None, prefix_len=0):
         """The new tokens' rows go to `slots` (int32 [batch * tokens]; negative: not cached again);
         `lengths` counts them.  With a prefix, table and lengths describe what lies behind it."""
-        B, T, _ = x.shape
-        q, k, v = self.project(x)
+        B, T = q.shape[:2]
         q4.q4_kv_write(k, v, self.cache, slots, self.fmt)
         if prefix_pages is None:
             a = q4.q4_kv_attention(q, self.cache, table, lengths, self.fmt)

@@ -338,3 +338,43 @@ def test_values_of_zero_beside_others(q4, D, T, Hq, weight):
     out = call(q4, q, cache, table, [n] * B, fmt, scale)
     some = slice(0, B, 8)
     assert within(out[some], q[some], cache, table[some], [n] * len(q[some]), fmt, float(np.float32(scale))) <= 1.0
+
+
+def test_layer_with_rotary_positions(q4):
+    """project(), a turn of q and k by their positions, attend(): a prompt of two chunks and a single
+    token give what one chunk of all gives, and what plain attention over the turned rows gives."""
+    from bit_weight_only_q4_gb300 import cached_attention as C
+    gen = torch.Generator("cuda").manual_seed(5)
+    H, Hq, D, page, n = 2, 4, 64, 16, 45
+    weights = C._weights((Hq + 2 * H) * D, 256, gen), C._weights(256, Hq * D, gen)
+    x = torch.randn(1, n, 256, device="cuda", generator=gen).bfloat16()
+    table = torch.arange(3, dtype=torch.int32, device="cuda").view(1, 3)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+
+    def turn(t, pos):                                       # [..., tokens, heads, D]
+        angle = pos.view(-1, 1, 1) * 10.0 ** (-torch.arange(D // 2, device="cuda") / 8)
+        a, b = t.float().chunk(2, -1)
+        return torch.cat((a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin()), -1).bfloat16()
+
+    seen = []
+
+    def run(cuts):
+        layer = C.CachedAttention(*weights, Hq, q4.alloc_kv_cache(0, 3, page, H, D), 0, D)
+        out = []
+        for a, b in zip(cuts, cuts[1:]):
+            pos = torch.arange(a, b, device="cuda").float()
+            q, k, v = layer.project(x[:, a:b].contiguous())
+            q, k = turn(q, pos), turn(k, pos)
+            if cuts[1] == n:
+                seen.extend((q, k, v))
+            out.append(layer.attend(q, k, v, slots[a:b], table, torch.tensor([b], dtype=torch.int32, device="cuda")))
+        return layer, torch.cat(out, 1)
+
+    layer, whole = run((0, n))
+    _, parts = run((0, 20, n - 1, n))
+    # two roundings of the attention's output to bf16 apart, through one projection of 256 columns
+    assert (parts.float() - whole.float()).abs().max() <= 2.0**-6 * whole.float().abs().max()
+    q = seen[0].float().cpu().numpy()
+    length = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = q4.q4_kv_attention(seen[0], layer.cache, table, length, 0)
+    assert within(got, q, layer.cache.cpu().numpy(), table.cpu().numpy(), [n], 0, D**-0.5) <= 1.0
