@@ -419,7 +419,7 @@ def alloc_kv_cache(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim
     """An uninitialised K/V cache: uint8 [pages, kv_heads, page_size / 16, block bytes].
     Tokens are written with q4_kv_write; what no write has reached is never used."""
     n = kv_block_bytes(fmt, head_dim)
-    if n == 0 or page_size < 16 or page_size & (page_size - 1):
+    if n == 0 or not 16 <= page_size <= 1024 or page_size & (page_size - 1):
         raise ValueError(f"no cache of format {fmt}, head_dim {head_dim}, page_size {page_size}")
     return torch.empty((pages, kv_heads, page_size // 16, n), dtype=torch.uint8,
                        device=device or "cuda")
@@ -634,6 +634,8 @@ def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengt
     prefix_pages (int32): they are read and multiplied once for the whole batch.  page_table and
     lengths describe each sequence's own tokens behind them."""
     n = _kv_ints(prefix_pages, "prefix_pages", 1)[0]
+    if cache.dim() != 4:
+        raise ValueError(f"cache must be [pages, kv_heads, page_size / 16, block bytes], got {tuple(cache.shape)}")
     page = 16 * cache.shape[2]
     if prefix_len < 1 or n * page < prefix_len:
         raise ValueError(f"prefix_pages holds {n} pages of {page}, the prefix has {prefix_len} tokens")
