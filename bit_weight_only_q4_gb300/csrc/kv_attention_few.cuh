@@ -16,13 +16,13 @@
 // a unit and store, while the others are at the next one.  A tile's MMAs take some 660
 // cycles (D = 128), its decoding and softmax some 2,500 warp instructions.
 //
-// What bounds it.  int8: HBM on long contexts (eight of 131,072 tokens, 8 heads of 128, 4
-// query heads each: 351 us, 6.2 TB/s).  int4: the decoding warps, whose instructions
-// issue one in some four cycles beside the other roles' (the same in int4: 325 us, 3.5 TB/s;
-// 3,650 warp instructions a tile use 40 to 48% of the issue slots).  Heads of 64 in pages of
-// 16 tokens: the starting of copies (305 us; 8 copies a tile).  Short contexts: the chain
-// of a unit (queries, first references, sums, results), 3.4 us for one tile, partly hidden
-// behind the next unit's (48 streams of 37 to 4,096 tokens: 57 us).
+// What bounds it (times in chains of 20 calls of a graph).  int8: HBM on long contexts (eight of
+// 131,072 tokens, 8 heads of 128, 4 query heads each: 342 us, 6.5 TB/s).  int4: the decoding
+// warps, whose instructions issue one in some four cycles beside the other roles' (the same
+// in int4: 312 us, 3.7 TB/s; 3,650 warp instructions a tile use 43 to 49% of the issue slots).
+// Heads of 64 in pages of 16 tokens: the starting of copies (308 us; 8 copies a tile).  Short
+// contexts: the chain of a unit (queries, first references, sums, results), 3.4 us for one
+// tile, partly hidden behind the next unit's (48 streams of 37 to 4,096 tokens: 57 us).
 // Tried and left: 32 warps, with K and V decoded by two groups each, gained 10 to 20% on
 // units of two to four tiles and lost 14% on long ones to spills (64 registers a thread).
 #pragma once

@@ -16,8 +16,8 @@
 // cycles (D = 128); the softmax issues about 3,000 instructions, the decoding 1,800.
 //
 // What bounds it.  A tile takes some 3,300 cycles: 509 query tokens of four sequences of up to
-// 8,190 (int8, 32 heads on 8, of 128) 316 us, 504 TFLOP/s; 256 rows of 4 on a prefix of
-// 32,768 190 us, 720 TFLOP/s.  No single part sets it: without the softmax's arithmetic a chunk takes
+// 8,190 (int8, 32 heads on 8, of 128) 321 us, 497 TFLOP/s; 256 rows of 4 on a prefix of
+// 32,768 192 us, 716 TFLOP/s.  No single part sets it: without the softmax's arithmetic a chunk takes
 // 14% less, without decoding too 21%, and with an eighth of the MMAs besides still 75% --
 // the chain of a softmax warp through barriers and tensor memory, which half as much work
 // for twice the warps (28 warps, 32 tokens a thread) did not shorten.  Shared memory's port is
