@@ -1,0 +1,68 @@
+// C ABI of the operators around a layer's projections (include/q4.h): host-side validation,
+// then the launches of norm_rope.cu.
+#include "layer_ops.h"
+
+namespace q4 {
+
+static bool aligned_to(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+static bool pdl_on() { return (q4_get_launch_flags() & Q4_FLAG_PDL) != 0; }
+
+// Rows of `heads` heads, `stride` elements apart: long enough, and 16-byte accesses.
+static bool row_stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0; }
+
+}  // namespace q4
+
+using namespace q4;
+
+extern "C" {
+
+q4_status q4_norm_rope(const void *q, int64_t q_stride, const void *q_weight, void *q_out, int64_t q_out_stride,
+                       int q_heads, const void *k, int64_t k_stride, const void *k_weight, void *k_out,
+                       int64_t k_out_stride, int kv_heads, const int32_t *positions, const float *inv_freq,
+                       int rotary_dim, int interleaved, float eps, int tokens, int head_dim, void *stream)
+{
+    if (head_dim != 64 && head_dim != 128)
+        return fail(Q4_ERR_SHAPE, "head_dim must be 64 or 128 (got %d)", head_dim);
+    if (tokens < 1 || q_heads < 0 || kv_heads < 0 || q_heads > 65536 || kv_heads > 65536 || q_heads + kv_heads < 1)
+        return fail(Q4_ERR_SHAPE, "tokens=%d must be >= 1, q_heads=%d and kv_heads=%d 0 .. 65536 and not both 0",
+                    tokens, q_heads, kv_heads);
+    if ((q_heads > 0 && (!q || !q_out)) || (kv_heads > 0 && (!k || !k_out)))
+        return fail(Q4_ERR_NULL, "q, q_out, k and k_out must not be NULL where there are heads");
+    if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16)
+        return fail(Q4_ERR_SHAPE, "rotary_dim must be a multiple of 16, at most head_dim (got %d)", rotary_dim);
+    if (rotary_dim > 0 && (!positions || !inv_freq))
+        return fail(Q4_ERR_NULL, "positions and inv_freq must not be NULL with a rotation");
+    if (interleaved != 0 && interleaved != 1)
+        return fail(Q4_ERR_ARG, "interleaved must be 0 or 1 (got %d)", interleaved);
+    if (!(eps >= 0.f) || !(eps - eps == 0.f))
+        return fail(Q4_ERR_ARG, "eps must be finite and not negative");
+    const int64_t qr = (int64_t)q_heads * head_dim, kr = (int64_t)kv_heads * head_dim;
+    if ((q_heads > 0 && (!row_stride_ok(q_stride, qr) || !row_stride_ok(q_out_stride, qr))) ||
+        (kv_heads > 0 && (!row_stride_ok(k_stride, kr) || !row_stride_ok(k_out_stride, kr))))
+        return fail(Q4_ERR_SHAPE, "strides must be multiples of 8, at least heads * head_dim");
+    if ((q_heads > 0 && q == q_out && q_stride != q_out_stride) || (kv_heads > 0 && k == k_out && k_stride != k_out_stride))
+        return fail(Q4_ERR_ARG, "in place, input and output have one stride");
+    if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(q_out, 16) || !aligned_to(k_out, 16) ||
+        !aligned_to(q_weight, 16) || !aligned_to(k_weight, 16) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 4))
+        return fail(Q4_ERR_ALIGN, "q, k, their outputs and weights must be 16-byte, positions and inv_freq 4-byte aligned");
+    DeviceInfo dev;
+    const q4_status s = current_device(dev);
+    if (s != Q4_OK)
+        return s;
+    NormRopeArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.k_out = static_cast<uint16_t *>(k_out);
+    a.q_stride = q_stride, a.k_stride = k_stride, a.q_out_stride = q_out_stride, a.k_out_stride = k_out_stride;
+    a.q_weight = static_cast<const uint16_t *>(q_weight);
+    a.k_weight = static_cast<const uint16_t *>(k_weight);
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.q_heads = q_heads, a.kv_heads = kv_heads, a.tokens = tokens, a.rotary = rotary_dim;
+    a.interleaved = interleaved;
+    a.eps = eps;
+    return launch_norm_rope(dev, a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
+}
+
+}  // extern "C"

@@ -1,0 +1,24 @@
+// Launch parameters of the operators around a layer's projections: norms and rotation of
+// queries and keys, attention over whole prompts, adapters (checked by layer_capi.cu).
+#pragma once
+
+#include "q4_internal.h"
+
+namespace q4 {
+
+// ---- norm_rope.cu
+struct NormRopeArgs {
+    const uint16_t *q, *k;
+    uint16_t *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;    // elements from token to token
+    const uint16_t *q_weight, *k_weight;                       // NULL: no norm
+    const int32_t *positions;
+    const float *inv_freq;
+    int q_heads, kv_heads, tokens, rotary;                     // rotary = 0: no rotation
+    int interleaved;
+    float eps;
+    int parts, part_heads;                                     // (chosen by the launch)
+};
+q4_status launch_norm_rope(const DeviceInfo &dev, NormRopeArgs a, int head_dim, cudaStream_t st, bool pdl);
+
+}  // namespace q4

@@ -89,6 +89,7 @@ def load() -> ctypes.CDLL:
             "q4_kv_attention": ([p, i64, p, i, i, i, i, i, p, i, p, i, i, i, f, p, p, sz, p], st),
             "q4_kv_attention_shared": ([p, i64, p, i, i, i, i, i, p, i, p, i, p, i, i, i, f, p, p,
                                         sz, p], st),
+            "q4_norm_rope": ([p, i64, p, p, i64, i, p, i64, p, p, i64, i, p, p, i, i, f, i, i, p], st),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -107,7 +108,7 @@ def symbols() -> list[str]:
             "q4_dequant_nvfp4_f32", "q4_quantize_int4g128", "q4_quantize_nvfp4",
             "q4_embedding_int8", "q4_linear_int8", "q4_kv_block_bytes", "q4_kv_write",
             "q4_kv_read", "q4_kv_attention_workspace_bytes", "q4_kv_attention",
-            "q4_kv_attention_shared", "q4_test_kv_give_up"]
+            "q4_kv_attention_shared", "q4_test_kv_give_up", "q4_norm_rope"]
 
 
 def _check(status: int) -> None:
@@ -641,3 +642,68 @@ def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengt
         raise ValueError(f"prefix_pages holds {n} pages of {page}, the prefix has {prefix_len} tokens")
     return _kv_attention(q, cache, prefix_pages, prefix_len, page_table, lengths, fmt, scale, out,
                          workspace, stream)
+
+
+# ------------------------------------------------- around a layer's projections
+def _here(t, name):
+    """A tensor of the current device, where the call is launched."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _vector(t, name, n, dtype):
+    if t.dtype is not dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}], got {t.dtype} {tuple(t.shape)}")
+    _here(t, name)
+
+
+def _rope_rows(x, out, name, stream):
+    """(stride, out, its stride) of q or k and what its result goes to."""
+    _here(x, name)
+    shape = x.shape
+    row = _kv_rows(x, name, shape)
+    if out is None:
+        out = _kv_empty(shape, x, stream)
+    elif out is not x:
+        _here(out, name + "_out")
+        if out.shape != shape:
+            raise ValueError(f"{name}_out must be {tuple(shape)}, got {tuple(out.shape)}")
+    return row, out, _kv_rows(out, name + "_out", shape)
+
+
+def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, stream=None):
+    """(q_out, k_out): RMS norms of the heads of q and k (bf16 [tokens, heads, D] or [batch, tokens, heads,
+    D]; weights bf16 [D], or None for no norm), then the rotation of their first 2 * len(inv_freq)
+    columns by positions * inv_freq (int32 [batch * tokens], fp32; both None: no rotation), in adjacent
+    pairs or halves.  k may be None.  q_out=q and k_out=k work in place."""
+    if q.dim() not in (3, 4) or (k is not None and k.dim() not in (3, 4)):
+        raise ValueError("q and k must be [tokens, heads, D] or [batch, tokens, heads, D]")
+    D = q.shape[-1]
+    tokens = q.numel() // max(1, q.shape[-2] * D)
+    if k is not None and (k.shape[-1] != D or k.numel() != tokens * k.shape[-2] * D):
+        raise ValueError(f"q and k must have the same tokens and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    rotary = 0
+    if positions is not None:
+        rotary = 2 * inv_freq.numel()
+        _vector(positions, "positions", tokens, torch.int32)
+        _vector(inv_freq, "inv_freq", rotary // 2, torch.float32)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _vector(w, name, D, torch.bfloat16)
+    qs, q_out, qos = _rope_rows(q, q_out, "q", stream)
+    if k is not None:
+        ks, k_out, kos = _rope_rows(k, k_out, "k", stream)
+    else:
+        ks = kos = 0
+        k_out = None
+    if tokens == 0 or q.numel() + (0 if k is None else k.numel()) == 0:
+        return q_out, k_out
+    _check(load().q4_norm_rope(_ptr(q), qs, _ptr(q_weight), _ptr(q_out), qos, q.shape[-2], _ptr(k), ks, _ptr(k_weight),
+                               _ptr(k_out), kos, 0 if k is None else k.shape[-2], _ptr(positions), _ptr(inv_freq), rotary,
+                               int(bool(interleaved)), float(eps), tokens, D, _kv_stream(stream, q)))
+    return q_out, k_out

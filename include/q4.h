@@ -369,6 +369,30 @@ q4_status q4_kv_attention_shared(const void *q_bf16, int64_t q_stride, const uin
                                  int q_heads, float scale, void *out_bf16, void *workspace,
                                  size_t workspace_bytes, void *stream);
 
+/*
+ * Norms of queries and keys for each head, and the position rotation, in one pass.  For the
+ * head_dim values x of a token's head,
+ *     y = x / sqrt(mean(x^2) + eps) * weight      (y = x where the weight is NULL: no norm)
+ * and of y's first rotary_dim columns the pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved = 1, are turned by the angle positions[token] * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin).
+ * All of it is fp32 from the bf16 inputs to one rounding to bf16; angles are right to 2^-22 for
+ * every position and |inv_freq| <= 1 (the error grows with larger ones).
+ *   q, k            bf16; token n, head h, column d at n * stride + h * head_dim + d (strides in
+ *                   elements, multiples of 8; parts of a fused q|k|v row work as they are)
+ *   q_out, k_out    the same; either in place (the input's pointer and stride) or apart from all inputs
+ *   weights         bf16 [head_dim] or NULL
+ *   positions       int32 [tokens], inv_freq fp32 [rotary_dim / 2]; unused with rotary_dim = 0
+ * head_dim 64 or 128; rotary_dim a multiple of 16, at most head_dim; q_heads or kv_heads may be 0
+ * (its pointers are not looked at then), at most 65536 each.  q, k, outputs and weights 16-byte, positions and
+ * inv_freq 4-byte aligned.  With Q4_FLAG_PDL weights and inv_freq may be read before the previous kernel has finished.
+ */
+q4_status q4_norm_rope(const void *q_bf16, int64_t q_stride, const void *q_weight_bf16, void *q_out_bf16,
+                       int64_t q_out_stride, int q_heads, const void *k_bf16, int64_t k_stride,
+                       const void *k_weight_bf16, void *k_out_bf16, int64_t k_out_stride, int kv_heads,
+                       const int32_t *positions, const float *inv_freq, int rotary_dim, int interleaved,
+                       float eps, int tokens, int head_dim, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
