@@ -67,157 +67,6 @@ struct KvTileParams {
     int give_up, give_up_tiles;  // (tests) CTA whose copying warp gives up after so many tiles; negative: none
 };
 
-// ------------------------------------------------------------------- helpers
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t kv_prmt(uint32_t a, uint32_t b, uint32_t sel)
-{
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-    return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t a)
-{
-    uint32_t r;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t lds16(uint32_t a)
-{
-    uint16_t r;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
-    return r;
-}
-
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
-// Pairs of fp32 in one 64-bit register: one instruction for two operations.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(float a, float b)
-{
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
-{
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ void lds_f32x4(uint32_t a, f32x2 &x, f32x2 &y)
-{
-    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
-}
-
-// True in one lane of a converged warp.  tcgen05 instructions issued under it take their
-// descriptors from uniform registers: an MMA then costs 30 (A in tensor memory) and 52
-// cycles (A in shared memory) at N = 16, from a branch of one thread 78 and 119.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
-// Where a wait that has given up is noted: the error word, and a flag of the CTA that
-// lets every later wait return at once.  The roles leave their loops when they see it
-// (those whose warps meet at barriers by a vote after each wait for a unit: one that was
-// never described would not bring them to their end), and nothing is stored after it.
-struct KvDead {
-    unsigned *err;
-    volatile int *flag;
-    uint32_t flag_at;            // its shared-memory address
-};
-
-// Bounded wait of a whole warp, every lane polling (a phase that is complete costs some 15
-// cycles so, and more with one lane polling for the others; waiting warps do not slow
-// each other).  Written as one block, for the roles' loops wait in some twenty places
-// and have to stay short: the usual way through is two instructions.
-__device__ __forceinline__ void kv_wait(uint32_t bar, uint32_t parity, const KvDead &dead)
-{
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n, d;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
-                 "@p bra KV_DONE_%=;\n\t"
-                 "mov.u32 n, 0;\n"
-                 "KV_POLL_%=:\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
-                 "@p bra KV_DONE_%=;\n\t"
-                 "ld.volatile.shared.u32 d, [%2];\n\t"
-                 "setp.ne.u32 p, d, 0;\n\t"
-                 "@p bra KV_DONE_%=;\n\t"
-                 "add.u32 n, n, 1;\n\t"
-                 "setp.lt.u32 p, n, %4;\n\t"
-                 "@p bra KV_POLL_%=;\n\t"
-                 "st.volatile.shared.u32 [%2], 1;\n\t"
-                 "red.global.or.b32 [%3], %5;\n"
-                 "KV_DONE_%=:\n\t}"
-                 ::"r"(bar), "r"(parity), "r"(dead.flag_at), "l"(dead.err), "n"(kMbarSpinLimit), "n"(kErrBarrierTimeout)
-                 : "memory");
-    __syncwarp();
-}
-
-// A CTA that has given up: the MMAs that this warp's elected lane has issued are waited for,
-// so that none runs into the CTA's end.  `bar` has a count of one and is used for this alone.
-__device__ __forceinline__ void kv_mma_drain(uint32_t bar, const KvDead &dead)
-{
-    if (elect_one())
-        mma_commit(bar);
-    __syncwarp();
-    mbar_wait(bar, 0u, dead.err);
-}
-
-__device__ __forceinline__ void bar_sync(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ bool bar_or(int id, int threads, bool v)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-                 "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"(id), "r"(threads), "r"((uint32_t)v)
-                 : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // E - 6 for a V scale of v >= 0, see above.  A scale of 0 (a row of one value) makes no product
 // that could leave fp16's range, but p alone has a range too: it is added up in l and, times
 // vm, in the offset.  At -68 such a p is 2^68 at most, and references move before one reaches 2^76

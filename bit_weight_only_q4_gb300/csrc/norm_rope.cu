@@ -15,11 +15,13 @@
 // Layout.  A lane holds eight adjacent columns (one 16-byte access), so a warp takes 256 / D
 // heads at a time, and the partner of a pair is a whole lane away: its values come by four
 // shuffles of bf16 pairs.  A warp takes one token's heads, or a part of them, for the angles
-// are the token's: two a lane, shared through 512 bytes of shared memory.
+// are the token's: two a lane, shared through 512 bytes of shared memory.  With them go the weights:
+//     y_j = r (x_j (w_j cos_j) + x_p (+-w_p sin_j)),    p the partner,
+// and the bracket's factors are worked out once for a token's queries and once for its keys.
 //
 // What bounds it: HBM, 4 bytes a value.
-#include "q4_device.cuh"
 #include "layer_ops.h"
+#include "tc_device.cuh"
 
 namespace q4 {
 
@@ -36,7 +38,63 @@ __device__ __forceinline__ uint64_t nr_turn(float f)
     return ((uint64_t)(uint32_t)hi << 32) + (uint64_t)lo;
 }
 
-template <int D>
+__device__ __forceinline__ f32x2 nr_widen(uint32_t bf16_pair)
+{
+    return pack2(__uint_as_float(bf16_pair << 16), __uint_as_float(bf16_pair & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t nr_narrow(f32x2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+}
+
+template <int LANES>
+__device__ __forceinline__ float nr_head_sum(float v)
+{
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o /= 2)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// What a lane multiplies its columns (own) and their partners (other) by.
+struct NrFactors {
+    f32x2 own[4], other[4];
+};
+
+// Turn and weight of a lane's columns; angle: (cos, sin) of its first column.
+template <bool PAIRS>
+__device__ __forceinline__ void nr_factors(NrFactors &f, const uint16_t *weight, int l, int partner, bool turned,
+                                           float sign, const float2 *angle)
+{
+    uint4 w = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), p = w;
+    if (weight) {
+        w = __ldg(reinterpret_cast<const uint4 *>(weight) + l);
+        p = PAIRS ? w : __ldg(reinterpret_cast<const uint4 *>(weight) + partner);
+    }
+    const uint32_t we[4] = {w.x, w.y, w.z, w.w}, pe[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f32x2 c = pack2(1.f, 1.f), s = 0ull;
+        if (turned) {
+            if (PAIRS) {
+                const float2 v = angle[j];
+                c = pack2(v.x, v.x), s = pack2(-v.y, v.y);
+            } else {
+                const float4 v = *reinterpret_cast<const float4 *>(angle + 2 * j);
+                c = pack2(v.x, v.z), s = pack2(sign * v.y, sign * v.w);
+            }
+        }
+        const uint32_t o = PAIRS ? __funnelshift_l(pe[j], pe[j], 16) : pe[j];
+        f.own[j] = mul2(nr_widen(we[j]), c);
+        f.other[j] = mul2(nr_widen(o), s);
+    }
+}
+
+// PAIRS: adjacent columns are turned together (interleaved).
+template <int D, bool PAIRS>
 __global__ void __launch_bounds__(NR_WARPS * 32, 3) norm_rope_kernel(const NormRopeArgs a)
 {
     constexpr int LANES = D / 8;           // of a head
@@ -46,156 +104,116 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 3) norm_rope_kernel(const NormR
     const int l = lane % LANES, sub = lane / LANES;
     const int half = a.rotary / 2;
 
-    // what a lane keeps: its columns' weights (and the partner's), its two frequencies
-    uint64_t turn[2] = {0ull, 0ull};
+    uint64_t turn[2] = {0ull, 0ull};       // of the lane's two frequencies
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (lane + 32 * i < half)
             turn[i] = nr_turn(__ldg(a.inv_freq + lane + 32 * i));
-    // partner lane and the sign of its part; columns behind R stay as they are
-    int partner = lane, first = 0;
-    float sign = 0.f;
-    const bool turned = 8 * l < a.rotary;
-    if (turned && !a.interleaved) {
-        const bool front = 8 * l < half;
+    // partner lane, and where the lane's angles begin; columns behind R stay as they are
+    const bool turned = 8 * l < a.rotary, front = 8 * l < half;
+    int partner = lane, first = 4 * l;
+    if (!PAIRS && turned) {
         partner = front ? lane + half / 8 : lane - half / 8;
-        sign = front ? -1.f : 1.f;
         first = front ? 8 * l : 8 * l - half;
-    } else if (turned) {
-        first = 4 * l;
     }
-    const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    const int pl = partner % LANES;
-    uint4 wq, wk, pq, pk;
-    wq = a.q_weight ? __ldg(reinterpret_cast<const uint4 *>(a.q_weight) + l) : ones;
-    wk = a.k_weight ? __ldg(reinterpret_cast<const uint4 *>(a.k_weight) + l) : ones;
-    pq = a.q_weight ? __ldg(reinterpret_cast<const uint4 *>(a.q_weight) + pl) : ones;
-    pk = a.k_weight ? __ldg(reinterpret_cast<const uint4 *>(a.k_weight) + pl) : ones;
     pdl_wait();
 
     const int heads = a.q_heads + a.kv_heads;
     const int64_t items = (int64_t)a.tokens * a.parts;
+#pragma unroll 1
     for (int64_t item = (int64_t)blockIdx.x * NR_WARPS + warp; item < items; item += (int64_t)gridDim.x * NR_WARPS) {
         const int64_t token = a.parts == 1 ? item : item / a.parts;
-        const int h0 = (int)(item - token * a.parts) * a.part_heads;
-        const int h1 = h0 + a.part_heads < heads ? h0 + a.part_heads : heads;
-        const int position = half > 0 ? __ldg(a.positions + token) : 0;
-        float cs[8], sn[8];
-        bool have = false;
+        const int part = a.parts == 1 ? 0 : (int)(item - token * a.parts);
+        const int h0 = part * a.part_heads, h1 = heads - h0 < a.part_heads ? heads : h0 + a.part_heads;
+        if (half > 0) {
+            __syncwarp();                  // (the last item's have been read)
+            const int position = __ldg(a.positions + token);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (32 * i < half) {
+                    const uint64_t t = (uint64_t)(int64_t)position * turn[i];
+                    float s, c;
+                    sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &s, &c);
+                    s_angle[warp][lane + 32 * i] = make_float2(c, s);
+                }
+            }
+            __syncwarp();
+        }
+        // the part's queries, then its keys
 #pragma unroll 1
-        for (int base = h0; base < h1; base += NR_BATCH * PER) {
-            uint4 x[NR_BATCH];
+        for (int kind = 0; kind < 2; ++kind) {
+            const int begin = kind ? (h0 > a.q_heads ? h0 - a.q_heads : 0) : h0;
+            const int end = kind ? h1 - a.q_heads : (h1 < a.q_heads ? h1 : a.q_heads);
+            if (begin >= end)
+                continue;
+            const uint16_t *weight = kind ? a.k_weight : a.q_weight;
+            const uint16_t *in = (kind ? a.k + token * a.k_stride : a.q + token * a.q_stride) + 8 * lane;
+            uint16_t *out = (kind ? a.k_out + token * a.k_out_stride : a.q_out + token * a.q_out_stride) + 8 * lane;
+            NrFactors f;
+            nr_factors<PAIRS>(f, weight, l, partner % LANES, turned, front ? -1.f : 1.f, &s_angle[warp][first]);
+#pragma unroll 1
+            for (int base = begin; base < end; base += NR_BATCH * PER) {
+                uint4 x[NR_BATCH];
 #pragma unroll
-            for (int i = 0; i < NR_BATCH; ++i) {
-                const int h = base + i * PER + sub;
-                x[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (h < h1) {
-                    const uint16_t *row = h < a.q_heads ? a.q + token * a.q_stride + (int64_t)h * D
-                                                        : a.k + token * a.k_stride + (int64_t)(h - a.q_heads) * D;
-                    x[i] = *reinterpret_cast<const uint4 *>(row + 8 * l);
+                for (int i = 0; i < NR_BATCH; ++i) {
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (base + i * PER + sub < end)
+                        x[i] = *reinterpret_cast<const uint4 *>(in + (int64_t)(base + i * PER) * D);
                 }
-            }
-            if (!have && half > 0) {       // (behind the first loads)
-                have = true;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (32 * i < half) {
-                        const uint64_t t = (uint64_t)(int64_t)position * turn[i];
-                        float s, c;
-                        sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &s, &c);
-                        s_angle[warp][lane + 32 * i] = make_float2(c, s);
-                    }
-                }
-                __syncwarp();
-                if (turned) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (i < 2 || !a.interleaved) {
-                            const float4 v = *reinterpret_cast<const float4 *>(&s_angle[warp][first + 2 * i]);
-                            cs[2 * i] = v.x, sn[2 * i] = v.y, cs[2 * i + 1] = v.z, sn[2 * i + 1] = v.w;
-                        }
-                    }
-                }
-                __syncwarp();
-            }
-#pragma unroll
-            for (int i = 0; i < NR_BATCH; ++i) {
-                const int h = base + i * PER + sub;
-                if (base + i * PER >= h1)  // (the whole warp's)
-                    break;
-                const bool is_k = h >= a.q_heads;
-                uint32_t e[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                float v[8], y[8];
-                float ss = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[2 * j] = __uint_as_float(e[j] << 16);
-                    v[2 * j + 1] = __uint_as_float(e[j] & 0xffff0000u);
-                    ss = fmaf(v[2 * j], v[2 * j], ss);
-                    ss = fmaf(v[2 * j + 1], v[2 * j + 1], ss);
-                }
-                const bool norm = is_k ? a.k_weight != nullptr : a.q_weight != nullptr;
-#pragma unroll
-                for (int o = LANES / 2; o >= 1; o /= 2)
-                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                float r = rsqrtf(ss * (1.f / D) + a.eps);
-                if (__any_sync(0xffffffffu, ss > 3.4e38f)) {
-                    // squares past fp32's range: a row 2^100 times smaller, beside which eps is nothing
-                    float s2 = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        s2 = fmaf(v[j] * 0x1p-100f, v[j] * 0x1p-100f, s2);
-#pragma unroll
-                    for (int o = LANES / 2; o >= 1; o /= 2)
-                        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-                    if (norm && ss > 3.4e38f) {
-                        r = rsqrtf(s2 * (1.f / D));
+                for (int i = 0; i < NR_BATCH; ++i) {
+                    if (base + i * PER >= end)
+                        break;             // (the whole warp)
+                    uint32_t e[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    float r = 1.f;
+                    if (weight) {
+                        f32x2 s2 = 0ull;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            v[2 * j] *= 0x1p-100f, v[2 * j + 1] *= 0x1p-100f;
-                            e[j] = (uint32_t)f32_to_bf16_bits(v[2 * j]) | ((uint32_t)f32_to_bf16_bits(v[2 * j + 1]) << 16);
+                            const f32x2 v = nr_widen(e[j]);
+                            s2 = fma2(v, v, s2);
                         }
-                    }
-                }
-                r = norm ? r : 1.f;
-                const uint32_t we[4] = {is_k ? wk.x : wq.x, is_k ? wk.y : wq.y, is_k ? wk.z : wq.z, is_k ? wk.w : wq.w};
-                const uint32_t pe[4] = {is_k ? pk.x : pq.x, is_k ? pk.y : pq.y, is_k ? pk.z : pq.z, is_k ? pk.w : pq.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[2 * j] = v[2 * j] * r * __uint_as_float(we[j] << 16);
-                    y[2 * j + 1] = v[2 * j + 1] * r * __uint_as_float(we[j] & 0xffff0000u);
-                }
-                if (half > 0) {
-                    if (a.interleaved) {
-                        if (turned) {
+                        float s, t;
+                        unpack2(s2, s, t);
+                        const float ss = nr_head_sum<LANES>(s + t);
+                        r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+                        if (__any_sync(0xffffffffu, ss > 3.4e38f)) {
+                            // squares past fp32's range: a row 2^100 times smaller, beside which eps is nothing
+                            uint32_t small[4];
+                            s2 = 0ull;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const float p = y[2 * j], q = y[2 * j + 1];
-                                y[2 * j] = p * cs[j] - q * sn[j];
-                                y[2 * j + 1] = q * cs[j] + p * sn[j];
+                                const f32x2 v = mul2(nr_widen(e[j]), pack2(0x1p-100f, 0x1p-100f));
+                                small[j] = nr_narrow(v);
+                                s2 = fma2(v, v, s2);
                             }
-                        }
-                    } else {
+                            unpack2(s2, s, t);
+                            const float ss_small = nr_head_sum<LANES>(s + t);
+                            if (ss > 3.4e38f) {
+                                r = rsqrtf(ss_small * (1.f / D));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t o = __shfl_sync(0xffffffffu, e[j], partner);
-                            if (turned) {
-                                const float p = __uint_as_float(o << 16) * r * __uint_as_float(pe[j] << 16);
-                                const float q = __uint_as_float(o & 0xffff0000u) * r * __uint_as_float(pe[j] & 0xffff0000u);
-                                y[2 * j] = y[2 * j] * cs[2 * j] + sign * p * sn[2 * j];
-                                y[2 * j + 1] = y[2 * j + 1] * cs[2 * j + 1] + sign * q * sn[2 * j + 1];
+                                for (int j = 0; j < 4; ++j)
+                                    e[j] = small[j];
                             }
                         }
                     }
-                }
-                if (h < h1) {
-                    uint16_t *row = is_k ? a.k_out + token * a.k_out_stride + (int64_t)(h - a.q_heads) * D
-                                         : a.q_out + token * a.q_out_stride + (int64_t)h * D;
+                    const f32x2 r2 = pack2(r, r);
                     uint32_t o[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = (uint32_t)f32_to_bf16_bits(y[2 * j]) | ((uint32_t)f32_to_bf16_bits(y[2 * j + 1]) << 16);
-                    *reinterpret_cast<uint4 *>(row + 8 * l) = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        f32x2 y = mul2(nr_widen(e[j]), f.own[j]);
+                        if (PAIRS) {
+                            if (turned)
+                                y = fma2(nr_widen(__funnelshift_l(e[j], e[j], 16)), f.other[j], y);
+                        } else {
+                            const uint32_t p = __shfl_sync(0xffffffffu, e[j], partner);
+                            if (turned)
+                                y = fma2(nr_widen(p), f.other[j], y);
+                        }
+                        o[j] = nr_narrow(mul2(y, r2));
+                    }
+                    if (base + i * PER + sub < end)
+                        *reinterpret_cast<uint4 *>(out + (int64_t)(base + i * PER) * D) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
         }
@@ -211,7 +229,7 @@ q4_status launch_norm_rope(const DeviceInfo &dev, NormRopeArgs a, int head_dim, 
     a.part_heads = (int64_t)a.tokens >= (int64_t)dev.sms * NR_WARPS * 2 ? heads : batch;
     a.parts = (heads + a.part_heads - 1) / a.part_heads;
     const int64_t ctas = ((int64_t)a.tokens * a.parts + NR_WARPS - 1) / NR_WARPS;
-    const int64_t most = (int64_t)dev.sms * 4;
+    const int64_t most = (int64_t)dev.sms * 3;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most));
     cfg.blockDim = dim3(NR_WARPS * 32);
@@ -221,8 +239,12 @@ q4_status launch_norm_rope(const DeviceInfo &dev, NormRopeArgs a, int head_dim, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = pdl ? attr : nullptr;
     cfg.numAttrs = pdl ? 1 : 0;
-    const cudaError_t e = head_dim == 64 ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<64>, a)
-                                         : cudaLaunchKernelEx(&cfg, norm_rope_kernel<128>, a);
+    void (*kernel)(NormRopeArgs) = nullptr;
+    if (a.interleaved)
+        kernel = head_dim == 64 ? norm_rope_kernel<64, true> : norm_rope_kernel<128, true>;
+    else
+        kernel = head_dim == 64 ? norm_rope_kernel<64, false> : norm_rope_kernel<128, false>;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of norm_rope_kernel");
 }
 

@@ -645,45 +645,30 @@ def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengt
 
 
 # ------------------------------------------------- around a layer's projections
-def _here(t, name):
-    """A tensor of the current device, where the call is launched."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+# The checks of these calls are kept by shape and stride as those of the cache's are; types,
+# devices and contiguity are looked at in every call.
+def _here(device, **tensors):
+    """All tensors (or None) lie on one device, the current one, where the call is launched."""
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.get_device() != device):
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _vector(t, name, n, dtype):
     if t.dtype is not dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}], got {t.dtype} {tuple(t.shape)}")
-    _here(t, name)
 
 
-def _rope_rows(x, out, name, stream):
-    """(stride, out, its stride) of q or k and what its result goes to."""
-    _here(x, name)
-    shape = x.shape
-    row = _kv_rows(x, name, shape)
-    if out is None:
-        out = _kv_empty(shape, x, stream)
-    elif out is not x:
-        _here(out, name + "_out")
-        if out.shape != shape:
-            raise ValueError(f"{name}_out must be {tuple(shape)}, got {tuple(out.shape)}")
-    return row, out, _kv_rows(out, name + "_out", shape)
-
-
-def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None,
-                 k_out=None, stream=None):
-    """(q_out, k_out): RMS norms of the heads of q and k (bf16 [tokens, heads, D] or [batch, tokens, heads,
-    D]; weights bf16 [D], or None for no norm), then the rotation of their first 2 * len(inv_freq)
-    columns by positions * inv_freq (int32 [batch * tokens], fp32; both None: no rotation), in adjacent
-    pairs or halves.  k may be None.  q_out=q and k_out=k work in place."""
+def _norm_rope_plan(key, q, k, q_weight, k_weight, positions, inv_freq):
+    """(tokens, q heads, kv heads, D, strides, rotary_dim, shapes of the results)"""
     if q.dim() not in (3, 4) or (k is not None and k.dim() not in (3, 4)):
         raise ValueError("q and k must be [tokens, heads, D] or [batch, tokens, heads, D]")
-    D = q.shape[-1]
-    tokens = q.numel() // max(1, q.shape[-2] * D)
-    if k is not None and (k.shape[-1] != D or k.numel() != tokens * k.shape[-2] * D):
+    Hq, D = q.shape[-2:]
+    tokens = q.numel() // max(1, Hq * D)
+    H = 0 if k is None else k.shape[-2]
+    if k is not None and (k.shape[-1] != D or k.numel() != tokens * H * D):
         raise ValueError(f"q and k must have the same tokens and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
@@ -695,15 +680,51 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _vector(w, name, D, torch.bfloat16)
-    qs, q_out, qos = _rope_rows(q, q_out, "q", stream)
-    if k is not None:
-        ks, k_out, kos = _rope_rows(k, k_out, "k", stream)
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    qs, ks = _kv_rows(q, "q", q.shape), 0 if k is None else _kv_rows(k, "k", k.shape)
+    return _kv_plan(key, (tokens, Hq, H, D, qs, ks, Hq * D, H * D, rotary))
+
+
+def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, stream=None):
+    """(q_out, k_out): RMS norms of the heads of q and k (bf16 [tokens, heads, D] or [batch, tokens, heads,
+    D]; weights bf16 [D], or None for no norm), then the rotation of their first 2 * len(inv_freq)
+    columns by positions * inv_freq (int32 [batch * tokens], fp32; both None: no rotation), in adjacent
+    pairs or halves.  k may be None.  q_out=q and k_out=k work in place."""
+    key = ("norm_rope", q.shape, q.stride(), None if k is None else (k.shape, k.stride()),
+           None if positions is None else (positions.shape, inv_freq.shape), q_weight is None or q_weight.shape,
+           k_weight is None or k_weight.shape)
+    plan = _kv_plans.get(key)
+    bf16 = torch.bfloat16
+    if (plan is None or q.dtype is not bf16 or (k is not None and k.dtype is not bf16) or
+            (positions is not None and not (positions.dtype is torch.int32 and positions.is_contiguous() and
+                                            inv_freq.dtype is torch.float32 and inv_freq.is_contiguous())) or
+            (q_weight is not None and not (q_weight.dtype is bf16 and q_weight.is_contiguous())) or
+            (k_weight is not None and not (k_weight.dtype is bf16 and k_weight.is_contiguous()))):
+        plan = _norm_rope_plan(key, q, k, q_weight, k_weight, positions, inv_freq)
+    tokens, Hq, H, D, qs, ks, qos, kos, rotary = plan
+    _here(q.get_device(), q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq,
+          q_out=q_out, k_out=k_out)
+    if q_out is None:
+        q_out = _kv_empty(q.shape, q, stream)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
     else:
-        ks = kos = 0
+        qos = _kv_rows(q_out, "q_out", q.shape)
+    if k is None:
         k_out = None
-    if tokens == 0 or q.numel() + (0 if k is None else k.numel()) == 0:
+    elif k_out is None:
+        k_out = _kv_empty(k.shape, k, stream)
+    elif k_out.shape != k.shape:
+        raise ValueError(f"k_out must be {tuple(k.shape)}, got {tuple(k_out.shape)}")
+    else:
+        kos = _kv_rows(k_out, "k_out", k.shape)
+    if tokens * (Hq + H) == 0:
         return q_out, k_out
-    _check(load().q4_norm_rope(_ptr(q), qs, _ptr(q_weight), _ptr(q_out), qos, q.shape[-2], _ptr(k), ks, _ptr(k_weight),
-                               _ptr(k_out), kos, 0 if k is None else k.shape[-2], _ptr(positions), _ptr(inv_freq), rotary,
-                               int(bool(interleaved)), float(eps), tokens, D, _kv_stream(stream, q)))
+    status = (_lib or load()).q4_norm_rope(_ptr(q), qs, _ptr(q_weight), _ptr(q_out), qos, Hq, _ptr(k), ks, _ptr(k_weight),
+                                           _ptr(k_out), kos, H, _ptr(positions), _ptr(inv_freq), rotary,
+                                           1 if interleaved else 0, eps, tokens, D, _kv_stream(stream, q))
+    if status:
+        _check(status)
     return q_out, k_out
