@@ -13,8 +13,6 @@
 
 namespace q4 {
 
-constexpr unsigned kErrIndex = 4u;
-
 __global__ void __launch_bounds__(256) embedding_int8_kernel(const int32_t *__restrict__ ids,
                                                              const int8_t *__restrict__ q,
                                                              const uint16_t *__restrict__ sc,

@@ -24,7 +24,6 @@
 namespace q4 {
 
 constexpr int KV_BLOCK = 16;               // tokens of a block
-constexpr unsigned kErrIndex = 4u;         // Q4_DEVERR_INDEX
 
 template <int FMT, int D>
 struct KvLayout {

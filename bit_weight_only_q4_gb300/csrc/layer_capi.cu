@@ -1,5 +1,5 @@
 // C ABI of the operators around a layer's projections (include/q4.h): host-side validation,
-// then the launches of norm_rope.cu.
+// then the launches of norm_rope.cu and prompt_attention.cu.
 #include "layer_ops.h"
 
 namespace q4 {
@@ -63,6 +63,45 @@ q4_status q4_norm_rope(const void *q, int64_t q_stride, const void *q_weight, vo
     a.interleaved = interleaved;
     a.eps = eps;
     return launch_norm_rope(dev, a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
+}
+
+q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, const int32_t *offsets, int batch, int tokens, int q_heads, int kv_heads,
+                              int head_dim, float scale, void *out, void *stream)
+{
+    if (!q || !k || !v || !offsets || !out)
+        return fail(Q4_ERR_NULL, "q, k, v, offsets and out must not be NULL");
+    if (head_dim != 64 && head_dim != 128)
+        return fail(Q4_ERR_SHAPE, "head_dim must be 64 or 128 (got %d)", head_dim);
+    if (batch < 1 || tokens < 1 || q_heads < 1 || kv_heads < 1)
+        return fail(Q4_ERR_SHAPE, "batch=%d, tokens=%d, q_heads=%d and kv_heads=%d must be >= 1", batch, tokens, q_heads,
+                    kv_heads);
+    if (q_heads % kv_heads || q_heads / kv_heads > 128)
+        return fail(Q4_ERR_SHAPE, "q_heads=%d must be a multiple of kv_heads=%d, at most 128 times", q_heads, kv_heads);
+    if ((int64_t)tokens * q_heads > 0x7fffffff || (int64_t)batch * kv_heads > 0x3fffffff || batch > 0x7fffff00)
+        return fail(Q4_ERR_SHAPE, "tokens * q_heads must stay below 2^31, batch * kv_heads below 2^30");
+    const int64_t qr = (int64_t)q_heads * head_dim, kr = (int64_t)kv_heads * head_dim, most = (int64_t)1 << 38;
+    if (!row_stride_ok(q_stride, qr) || !row_stride_ok(k_stride, kr) || !row_stride_ok(v_stride, kr) || q_stride > most ||
+        k_stride > most || v_stride > most)
+        return fail(Q4_ERR_SHAPE, "strides must be multiples of 8, at least heads * head_dim and at most 2^38");
+    if (!(scale - scale == 0.f))
+        return fail(Q4_ERR_ARG, "scale must be finite");
+    if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 16) || !aligned_to(offsets, 4))
+        return fail(Q4_ERR_ALIGN, "q, k, v and out must be 16-byte, offsets 4-byte aligned");
+    DeviceInfo dev;
+    const q4_status s = current_device(dev);
+    if (s != Q4_OK)
+        return s;
+    PromptArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.out = static_cast<uint16_t *>(out);
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.offsets = offsets;
+    a.batch = batch, a.tokens = tokens, a.q_heads = q_heads, a.kv_heads = kv_heads;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    return launch_prompt_attention(dev, a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
 }  // extern "C"

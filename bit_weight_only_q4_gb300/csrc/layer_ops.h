@@ -21,4 +21,17 @@ struct NormRopeArgs {
 };
 q4_status launch_norm_rope(const DeviceInfo &dev, NormRopeArgs a, int head_dim, cudaStream_t st, bool pdl);
 
+// ---- prompt_attention.cu
+struct PromptArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t *out;
+    int64_t q_stride, k_stride, v_stride;                      // elements from token to token
+    const int32_t *offsets;                                    // [batch + 1]
+    int batch, tokens, q_heads, kv_heads;
+    float scale_log2;                                          // scale * log2(e)
+    int group, tile_tokens;                                    // (by the launch) query heads per key head, tokens of a tile
+    unsigned *err;
+};
+q4_status launch_prompt_attention(const DeviceInfo &dev, PromptArgs a, int head_dim, cudaStream_t st, bool pdl);
+
 }  // namespace q4

@@ -1,0 +1,598 @@
+// Causal attention over whole prompts, packed one behind the other, with grouped heads:
+// for query token i of a sequence and a head that shares key head h,
+//     s_ij = scale log2(e) (q_i . k_j),  p_ij = 2^(s_ij - m_i)  for j <= i,
+//     out_i = sum_j p_ij v_j / sum_j p_ij.
+// Products are bf16 with fp32 sums, s, p and its sum fp32; p goes to the second product as bf16, as
+// wide as the v that it meets there (at most 2^-8 of each term of the sum).
+//
+// A tile is 128 rows: T = 128 / G tokens with the G query heads of one key head, token by
+// token, so that grouped heads share each tile of keys.  A unit of work is two neighbouring
+// tiles A and B (2 T tokens) of one key head; both run over the same tiles of 128 keys, from
+// their own tokens back to the first.  The order matters: only the first tile or two are cut by
+// the mask, and the reference m_i that they give serves for the others.  m_i need not be the largest
+// s_ij: p keeps its relative precision at any size, and only when a tile's sum passes 2^20 is the
+// reference raised and what was summed scaled down.  So a tile that is seen whole costs one pass over its scores and no maximum.
+//
+// One CTA per SM, 12 warps: four with the softmax of A (one thread a row), four with that of
+// B, one that copies (TMA), one that issues the MMAs.  S and O of both tiles fill the tensor
+// memory; P takes the place of its S.  MMAs run in the order
+//     .. P_A V(t)  S_A(t+1)  P_B V(t)  S_B(t+1)  P_A V(t+1) ..
+// so that the tensor cores work on one tile while the other is in its softmax, and an S
+// is overwritten by an MMA that comes behind the one that reads P in its place.
+//
+// A masked probability is 0, and 0 times a v that is not finite would be NaN: tiles cut by the
+// mask are looked through for such values, and a tile that has one is multiplied by the softmax
+// threads themselves, over the tokens that a row sees.
+#include "layer_ops.h"
+#include "tc_device.cuh"
+#include "tma.h"
+
+namespace q4 {
+
+constexpr int PA_ROWS = 128, PA_KEYS = 128;
+constexpr int PA_COPY = 8, PA_MMA = 9, PA_WARPS = 12;
+constexpr float PA_SUM_TOP = 0x1p20f;
+
+template <int D>
+struct PaSmem {
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr uint32_t TILE = PA_KEYS * D * 2;
+    static constexpr uint32_t RING = 2 * TILE;                       // [Q of A, Q of B][ring][staging]
+    static constexpr uint32_t STAGE = RING + STAGES * TILE;
+    static constexpr uint32_t TOTAL = STAGE + 8 * 2048;
+};
+
+// What a unit is.
+struct PaUnit {
+    int start, len;              // the sequence's first row and tokens
+    int first;                   // first token of tile A
+    int head;                    // key head
+    int na, nb;                  // key tiles of A and of B (0: B has no token)
+};
+
+// Hands out a warp's units in rising order of their number.  Units are numbered by sequence, then
+// from the last pair of tiles to the first, then by key head; sequences are taken in 32 at a time.
+struct PaWalk {
+    const PromptArgs &p;
+    int chunk, base, total, floor;         // first sequence of the 32 at hand, units before them and among them; rows taken
+    int start, len, before;                // this lane's sequence, units before it among the 32
+
+    __device__ explicit PaWalk(const PromptArgs &args) : p(args), chunk(-32), base(0), total(0), floor(0), start(0), len(0), before(0) {}
+
+    __device__ bool find(int number, PaUnit &u)
+    {
+        const int lane = threadIdx.x & 31;
+        const int pair = 2 * p.tile_tokens;
+        while (number >= base + total) {
+            base += total;
+            chunk += 32;
+            if (chunk >= p.batch)
+                return false;
+            const int b = chunk + lane;
+            int lo = b < p.batch ? __ldg(p.offsets + b) : 0, hi = b < p.batch ? __ldg(p.offsets + b + 1) : 0;
+            const bool outside = lo < 0 || hi < 0 || lo > p.tokens || hi > p.tokens;
+            lo = lo < 0 ? 0 : lo > p.tokens ? p.tokens : lo;
+            hi = hi < 0 ? 0 : hi > p.tokens ? p.tokens : hi;
+            // Offsets that go back: what begins before the end of a sequence in front of it is left out, so that
+            // no row is written twice and the work stays bounded.
+            int top = hi;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, top, o);
+                top = lane >= o && v > top ? v : top;
+            }
+            int under = __shfl_up_sync(0xffffffffu, top, 1);
+            under = lane > 0 && under > floor ? under : floor;
+            const bool bad = b < p.batch && (hi < lo || lo < under);
+            if ((bad || outside) && p.err)
+                atomicOr(p.err, kErrIndex);
+            start = lo;
+            len = bad || hi < lo ? 0 : hi - lo;
+            const int all = __shfl_sync(0xffffffffu, top, 31);
+            floor = all > floor ? all : floor;
+            const int units = (len + pair - 1) / pair * p.kv_heads;
+            int sum = units;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                sum += lane >= o ? v : 0;
+            }
+            before = sum - units;
+            total = __shfl_sync(0xffffffffu, sum, 31);
+        }
+        const int at = number - base;
+        const int src = 31 - __clz(__ballot_sync(0xffffffffu, before <= at));
+        u.start = __shfl_sync(0xffffffffu, start, src);
+        u.len = __shfl_sync(0xffffffffu, len, src);
+        const int mine = at - __shfl_sync(0xffffffffu, before, src);
+        const int back = mine / p.kv_heads;
+        u.head = mine - back * p.kv_heads;
+        u.first = ((u.len + pair - 1) / pair - 1 - back) * pair;
+        const int t = p.tile_tokens, rest = u.len - u.first;
+        u.na = (u.first + (rest < t ? rest : t) + PA_KEYS - 1) / PA_KEYS;
+        u.nb = rest <= t ? 0 : (u.first + (rest < pair ? rest : pair) + PA_KEYS - 1) / PA_KEYS;
+        return true;
+    }
+};
+
+// Unit number of a CTA's round: to and fro, for neighbouring numbers cost alike and fall.
+__device__ __forceinline__ int pa_number(int round)
+{
+    const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
+    return round * grid + ((round & 1) ? grid - 1 - cta : cta);
+}
+
+template <int D>
+__global__ void __launch_bounds__(PA_WARPS * 32, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                            const __grid_constant__ CUtensorMap v_map, const PromptArgs p)
+{
+    using L = PaSmem<D>;
+    constexpr int NS = L::STAGES;
+    constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;          // of A; B 128 columns behind
+    constexpr uint32_t BF16 = (1u << 7) | (1u << 10);
+    constexpr uint32_t IDESC_S = (1u << 4) | BF16 | ((uint32_t)(PA_KEYS >> 3) << 17) | (8u << 24);
+    constexpr uint32_t IDESC_O = (1u << 4) | BF16 | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ uint64_t s_bar[2 * NS + 12];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_dead, s_skip[2];
+    const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+    const uint32_t kv_full = smem_u32(s_bar), kv_free = kv_full + 8u * NS, q_full = kv_free + 8u * NS,   // q_full: A, B
+                   q_free = q_full + 16, s_full = q_full + 24, p_full = q_full + 40, o_full = q_full + 56, drained = q_full + 72;
+    if (warp == PA_COPY) {
+        if (lane == 0) {
+            for (int i = 0; i < NS; ++i) {
+                mbar_init(kv_full + 8u * i, 1);
+                mbar_init(kv_free + 8u * i, 1);
+            }
+            mbar_init(q_free, 1);
+            mbar_init(drained, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(q_full + 8u * i, 1);
+                mbar_init(s_full + 8u * i, 1);
+                mbar_init(p_full + 8u * i, 4);
+                mbar_init(o_full + 8u * i, 1);
+            }
+            s_dead = 0;
+        }
+        mbar_init_fence();
+    } else if (warp == PA_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&s_tmem)), "n"(TM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+    pdl_wait();
+    const KvDead dead = {p.err, &s_dead, smem_u32(&s_dead)};
+    auto gone_all = [&]() { return __any_sync(0xffffffffu, *dead.flag != 0); };
+    PaWalk walk(p);
+    PaUnit u;
+
+    if (warp < 8) {
+        // ------------------------------------------ softmax and results
+        const int x = warp >> 2;                           // tile: A, B
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const int row_token = row / p.group, row_head = row - row_token * p.group;
+        const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t t_s = t_lane + TM_S + 128u * x, t_o = t_lane + TM_O + 128u * x;
+        const float sl = p.scale_log2;
+        const f32x2 sl2 = pack2(sl, sl);
+        uint32_t ring = 0u, tiles = 0u, units = 0u;        // of the copies before this unit; of this tile's S and O
+#pragma unroll 1
+        for (int round = 0; walk.find(pa_number(round), u); ++round) {
+            if (bar_or(1 + x, 128, *dead.flag != 0))       // leave together
+                break;
+            const int n = u.nb > 0 ? u.nb : u.na, mine = x ? u.nb : u.na;
+            const int first = u.first + x * p.tile_tokens;
+            // the row's token within the sequence; -1: there is none
+            const int token = row_token < p.tile_tokens && first + row_token < u.len ? first + row_token : -1;
+            const int whole = (first + 1) / PA_KEYS;       // key tiles that all rows see wholly
+            float m = -INFINITY;
+            f32x2 la = 0ull, lb = 0ull;
+#pragma unroll 1
+            for (int j = mine - 1; j >= 0; --j) {
+                kv_wait(s_full + 8u * x, tiles & 1u, dead);
+                ++tiles;
+                tc_fence_after();
+                const bool masked = j >= whole;
+                uint32_t ph[PA_KEYS / 2];
+                bool careful = masked || __any_sync(0xffffffffu, token >= 0 && m == -INFINITY);
+                if (!careful) {
+                    const f32x2 n2 = pack2(-m, -m);
+                    f32x2 ta = 0ull, tb = 0ull;
+                    uint32_t v[2][32];
+                    tmem_ld32_async(t_s, v[0]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c < 3)
+                            tmem_ld32_async(t_s + 32u * (c + 1), v[(c + 1) & 1]);
+                        const uint32_t (&w)[32] = v[c & 1];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            f32x2 a = fma2(pack2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), sl2, n2);
+                            f32x2 b = fma2(pack2(__uint_as_float(w[i + 2]), __uint_as_float(w[i + 3])), sl2, n2);
+                            float e[4];
+                            unpack2(a, e[0], e[1]);
+                            unpack2(b, e[2], e[3]);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                e[y] = ex2(e[y]);
+                            ta = add2(ta, pack2(e[0], e[1]));
+                            tb = add2(tb, pack2(e[2], e[3]));
+                            ph[16 * c + i / 2] = bf16_pair(e[0], e[1]);
+                            ph[16 * c + i / 2 + 1] = bf16_pair(e[2], e[3]);
+                        }
+                        if (c < 3)
+                            tmem_wait_ld();
+                    }
+                    float sa, sb;
+                    unpack2(add2(ta, tb), sa, sb);
+                    careful = __any_sync(0xffffffffu, token >= 0 && !(sa + sb < PA_SUM_TOP));
+                    if (!careful) {
+                        la = add2(la, ta);
+                        lb = add2(lb, tb);
+                    }
+                }
+                const int seen = token - j * PA_KEYS;      // the row's last visible column
+                if (careful) {
+                    float want = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32_async(t_s + 32u * c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float s = __uint_as_float(v[i]) * sl;
+                            want = 32 * c + i <= seen ? fmaxf(want, s) : want;
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, want > m)) {
+                        const float old = m;
+                        m = fmaxf(m, want);
+                        const float f = old == -INFINITY ? 0.f : ex2(old - m);
+                        const f32x2 f2 = pack2(f, f);
+                        la = mul2(la, f2);
+                        lb = mul2(lb, f2);
+                        if (j < mine - 1) {                // (the MMAs of the tile before are done: S came behind them)
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32_async(t_o + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st32(t_o + c, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float neg = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32_async(t_s + 32u * c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float a = ex2(fmaf(__uint_as_float(v[i]), sl, neg)), b = ex2(fmaf(__uint_as_float(v[i + 1]), sl, neg));
+                            a = 32 * c + i <= seen ? a : 0.f;
+                            b = 32 * c + i + 1 <= seen ? b : 0.f;
+                            la = add2(la, pack2(a, b));
+                            ph[16 * c + i / 2] = bf16_pair(a, b);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < PA_KEYS / 2; c += 32)
+                    tmem_st32(t_s + c, reinterpret_cast<uint32_t(&)[32]>(ph[c]));
+                tmem_wait_st();
+                if (masked) {
+                    // one row of v for each thread: is there anything that is not finite?
+                    const uint32_t at = ring + 2u * (uint32_t)(n - 1 - j) + 1u;
+                    const uint32_t v = sm + L::RING + (at & (NS - 1)) * L::TILE;
+                    kv_wait(kv_full + 8u * (at & (NS - 1)), (at / NS) & 1u, dead);
+                    uint32_t bad = 0u;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 e = lds128(v + (uint32_t)(c >> 3) * 16384u + (uint32_t)row * 128u + 16u * ((uint32_t)(c ^ row) & 7u));
+                        bad |= ((e.x & 0x7f807f80u) + 0x00800080u) | ((e.y & 0x7f807f80u) + 0x00800080u) |
+                               ((e.z & 0x7f807f80u) + 0x00800080u) | ((e.w & 0x7f807f80u) + 0x00800080u);
+                    }
+                    const bool skip = bar_or(1 + x, 128, (bad & 0x80008000u) != 0u);
+                    if (skip) {
+                        // O += P V over the tokens that the row sees, 16 columns at a time
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            uint32_t w[16];
+                            if (j < mine - 1)
+                                tmem_ld16(t_o + c, w);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = j < mine - 1 ? __uint_as_float(w[i]) : 0.f;
+#pragma unroll 1
+                            for (int k = 0; k < PA_KEYS; ++k) {
+                                uint32_t pk;
+                                tmem_ld1(t_s + (k >> 1), pk);
+                                const float pf = __uint_as_float((k & 1) ? pk & 0xffff0000u : pk << 16);
+                                const uint32_t r = v + (uint32_t)(c >> 6) * 16384u + (uint32_t)k * 128u;
+                                const uint32_t piece = (uint32_t)(c >> 3) & 7u;
+                                const uint4 e0 = lds128(r + 16u * (piece ^ ((uint32_t)k & 7u)));
+                                const uint4 e1 = lds128(r + 16u * ((piece + 1u) ^ ((uint32_t)k & 7u)));
+                                const uint32_t e[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+                                if (k <= seen) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        o[2 * i] = fmaf(pf, __uint_as_float(e[i] << 16), o[2 * i]);
+                                        o[2 * i + 1] = fmaf(pf, __uint_as_float(e[i] & 0xffff0000u), o[2 * i + 1]);
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = __float_as_uint(o[i]);
+                            tmem_st16(t_o + c, w);
+                        }
+                        tmem_wait_st();
+                    }
+                    if (row == 0)
+                        s_skip[x] = skip;
+                } else if (row == 0) {
+                    s_skip[x] = 0;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_full + 8u * x);
+            }
+            ring += 2u * (uint32_t)n;
+            if (mine == 0)
+                continue;
+            // ---- the unit's results
+            kv_wait(o_full + 8u * x, units & 1u, dead);
+            ++units;
+            tc_fence_after();
+            float l0, l1;
+            unpack2(add2(la, lb), l0, l1);
+            const float inv = l0 + l1 == 0.f ? 0.f : 1.f / (l0 + l1);
+            // 32 columns at a time through the warp's 2 KB of shared memory: written by row, read four
+            // lanes to a row, so that a store fills whole sectors.  Piece c of row r lies at c ^ (r / 2 & 3).
+            const uint32_t st = sm + L::STAGE + (uint32_t)warp * 2048u;
+            const uint32_t st_row = st + (uint32_t)lane * 64u, key = (uint32_t)(lane >> 1) & 3u;
+            const int at_row = token < 0 ? -1 : (u.start + token) * p.q_heads + u.head * p.group + row_head;
+            int to[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                to[i] = __shfl_sync(0xffffffffu, at_row, (lane >> 2) + 8 * i);
+            const bool store = !gone_all();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_async(t_o + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t e[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        e[y] = bf16_pair(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
+                    sts128(st_row + (((uint32_t)i ^ key) << 4), e[0], e[1], e[2], e[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t r = (uint32_t)(lane >> 2) + 8u * i, piece = (uint32_t)lane & 3u;
+                    const uint4 e = lds128(st + r * 64u + ((piece ^ ((r >> 1) & 3u)) << 4));
+                    if (to[i] >= 0 && store)
+                        *reinterpret_cast<uint4 *>(p.out + (int64_t)to[i] * D + c + 8 * piece) = e;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();                             // (the next P of this tile lets its O be written again)
+        }
+    } else if (warp == PA_COPY) {
+        // ------------------------------------------------------- copies
+        uint32_t at = 0u;
+        uint32_t loads[2] = {0u, 0u};
+#pragma unroll 1
+        for (int round = 0; walk.find(pa_number(round), u) && !gone_all(); ++round) {
+            const int n = u.nb > 0 ? u.nb : u.na;
+#pragma unroll 1
+            for (int i = 0; i < 2 * n && !gone_all(); ++i, ++at) {
+                const uint32_t s = at & (NS - 1);
+                if (at >= NS)
+                    kv_wait(kv_free + 8u * s, (at / NS - 1u) & 1u, dead);
+                if (gone_all())
+                    break;
+                if (elect_one()) {
+                    const CUtensorMap *map = (i & 1) ? &v_map : &k_map;
+                    const uint32_t dst = sm + L::RING + s * L::TILE, bar = kv_full + 8u * s;
+                    mbar_arrive_expect_tx(bar, L::TILE);
+#pragma unroll
+                    for (int c = 0; c < D; c += 64)
+                        tma_load_3d(dst + (uint32_t)c * 256u, map, c, u.head, u.start + (n - 1 - i / 2) * PA_KEYS, bar);
+                }
+                __syncwarp();
+                if (i == 0) {                              // (behind the first keys)
+                    if (round > 0)
+                        kv_wait(q_free, (uint32_t)(round - 1) & 1u, dead);
+                    if (gone_all()) {
+                        ++at;
+                        break;
+                    }
+                    for (int x = 0; x < (u.nb > 0 ? 2 : 1); ++x, __syncwarp()) {
+                        if (elect_one()) {
+                            const uint32_t bytes = (uint32_t)(p.tile_tokens * p.group) * D * 2;
+                            mbar_arrive_expect_tx(q_full + 8u * x, bytes);
+#pragma unroll
+                            for (int c = 0; c < D; c += 64)
+                                tma_load_3d(sm + (uint32_t)x * L::TILE + (uint32_t)c * 256u, &q_map, c, u.head * p.group,
+                                            u.start + u.first + x * p.tile_tokens, q_full + 8u * x);
+                        }
+                        ++loads[x];
+                    }
+                }
+            }
+        }
+        if (gone_all()) {
+            // copies in flight land before the CTA ends
+            for (uint32_t i = at > NS ? at - NS : 0u; i < at; ++i)
+                mbar_wait(kv_full + 8u * (i & (NS - 1)), (i / NS) & 1u, p.err);
+            for (int x = 0; x < 2; ++x)
+                if (loads[x] > 0)
+                    mbar_wait(q_full + 8u * x, (loads[x] - 1u) & 1u, p.err);
+        }
+    } else if (warp == PA_MMA) {
+        // -------------------------------------------------------- MMAs
+        uint32_t at = 0u;                                  // copies before this unit
+        uint32_t qn[2] = {0u, 0u}, pn[2] = {0u, 0u};       // Q loads and P's before
+        const uint64_t qd = smem_desc_sw128(sm), kd = smem_desc_sw128(sm + L::RING);
+        const uint64_t vd = (kd & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(D == 128 ? PA_KEYS * 128 >> 4 : 0) << 16);
+        const uint32_t q_lo = (uint32_t)qd, q_hi = (uint32_t)(qd >> 32), k_lo = (uint32_t)kd, k_hi = (uint32_t)(kd >> 32),
+                       v_lo = (uint32_t)vd, v_hi = (uint32_t)(vd >> 32);
+        auto scores = [&](uint32_t x, uint32_t stage) {    // S of tile x
+            if (elect_one()) {
+                const uint32_t a = q_lo + x * (L::TILE >> 4), b = k_lo + stage * (L::TILE >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t step = (uint32_t)(kk >> 2) * (16384u >> 4) + 2u * (kk & 3);
+                    mma_f16_2(tmem + TM_S + 128u * x, a + step, q_hi, b + step, k_hi, IDESC_S, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(s_full + 8u * x);
+            }
+            __syncwarp();
+        };
+#pragma unroll 1
+        for (int round = 0; walk.find(pa_number(round), u) && !gone_all(); ++round) {
+            const int nb = __shfl_sync(0xffffffffu, u.nb, 0), na = __shfl_sync(0xffffffffu, u.na, 0);
+            const int n = nb > 0 ? nb : na;
+            bool begun[2] = {false, false};                // O holds something
+            auto active = [&](int x, int t) { return x ? nb > 0 : t >= n - na; };
+            auto score_step = [&](int x, int t) {
+                if (!active(x, t))
+                    return;
+                if (t == (x ? 0 : n - na)) {
+                    kv_wait(q_full + 8u * x, qn[x] & 1u, dead);
+                    ++qn[x];
+                }
+                tc_fence_after();
+                scores((uint32_t)x, (at + 2u * t) & (NS - 1));
+            };
+            auto keys_wait = [&](int t) {
+                const uint32_t i = at + 2u * t;
+                kv_wait(kv_full + 8u * (i & (NS - 1)), (i / NS) & 1u, dead);
+            };
+            auto release = [&](uint32_t bar) {
+                if (elect_one())
+                    mma_commit(bar);
+                __syncwarp();
+            };
+            keys_wait(0);
+            score_step(0, 0);
+            score_step(1, 0);
+            release(kv_free + 8u * (at & (NS - 1)));
+            if (n == 1)
+                release(q_free);
+#pragma unroll 1
+            for (int t = 0; t < n && !gone_all(); ++t) {
+                const uint32_t vi = at + 2u * t + 1u, vs = vi & (NS - 1);
+                kv_wait(kv_full + 8u * vs, (vi / NS) & 1u, dead);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (active(x, t)) {
+                        kv_wait(p_full + 8u * x, pn[x] & 1u, dead);
+                        ++pn[x];
+                        tc_fence_after();
+                        const bool skip = __shfl_sync(0xffffffffu, *(volatile int *)&s_skip[x], 0) != 0;
+                        if (elect_one()) {
+                            if (!skip) {
+                                const uint32_t b = v_lo + vs * (L::TILE >> 4);
+#pragma unroll
+                                for (int kk = 0; kk < PA_KEYS / 16; ++kk)
+                                    mma_f16_tmem_a(tmem + TM_O + 128u * x, tmem + TM_S + 128u * x + 8u * kk,
+                                                   b + (uint32_t)kk * (2048 >> 4), v_hi, IDESC_O, kk > 0 || begun[x] ? 1u : 0u);
+                            }
+                            if (t == n - 1)
+                                mma_commit(o_full + 8u * x);
+                        }
+                        __syncwarp();
+                        begun[x] = true;
+                    }
+                    if (t + 1 < n) {
+                        if (x == 0)
+                            keys_wait(t + 1);
+                        score_step(x, t + 1);
+                    }
+                }
+                release(kv_free + 8u * vs);
+                if (t + 1 < n)
+                    release(kv_free + 8u * ((at + 2u * t + 2u) & (NS - 1)));
+                if (t + 2 == n)
+                    release(q_free);
+            }
+            at += 2u * (uint32_t)n;
+        }
+    }
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    if (*dead.flag != 0 && warp == PA_MMA)
+        kv_mma_drain(drained, dead);
+    __syncthreads();
+    if (warp == PA_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");
+    }
+}
+
+template <int D>
+static q4_status pa_launch(const DeviceInfo &dev, const PromptArgs &a, int64_t most_units, cudaStream_t st, bool pdl)
+{
+    CUtensorMap q, k, v;
+    const uint64_t n = (uint64_t)a.tokens;
+    q4_status s = tma_heads(q, a.q, D, a.q_heads, n, a.q_stride, a.group, a.tile_tokens);
+    if (s == Q4_OK)
+        s = tma_heads(k, a.k, D, a.kv_heads, n, a.k_stride, 1, PA_KEYS);
+    if (s == Q4_OK)
+        s = tma_heads(v, a.v, D, a.kv_heads, n, a.v_stride, 1, PA_KEYS);
+    if (s != Q4_OK)
+        return s;
+    const size_t smem = PaSmem<D>::TOTAL + 1024;
+    cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaFuncSetAttribute(prompt_attention_kernel)");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(most_units < dev.sms ? most_units : dev.sms));
+    cfg.blockDim = dim3(PA_WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = pdl ? attr : nullptr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D>, q, k, v, a);
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of prompt_attention_kernel");
+}
+
+q4_status launch_prompt_attention(const DeviceInfo &dev, PromptArgs a, int head_dim, cudaStream_t st, bool pdl)
+{
+    a.group = a.q_heads / a.kv_heads;
+    a.tile_tokens = PA_ROWS / a.group;
+    a.err = device_error_flags();
+    // at most one part-filled pair of tiles a sequence
+    const int64_t units = ((int64_t)a.tokens / (2 * a.tile_tokens) + a.batch) * a.kv_heads;
+    return head_dim == 64 ? pa_launch<64>(dev, a, units, st, pdl) : pa_launch<128>(dev, a, units, st, pdl);
+}
+
+}  // namespace q4

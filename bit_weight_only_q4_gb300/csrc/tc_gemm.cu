@@ -40,6 +40,7 @@
 #include "q4_device.cuh"
 #include "q4_internal.h"
 #include "tc_device.cuh"
+#include "tma.h"
 
 namespace q4 {
 
@@ -73,16 +74,6 @@ struct TcParams {
 
 
 // ------------------------------------------------------------ PTX helpers
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                            uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-                 : "memory");
-}
-
-
 // Instruction descriptor of tcgen05.mma kind::f16: fp16 A and B (K-major),
 // fp32 accumulator, M = 128, N = n.
 __device__ __forceinline__ uint32_t idesc_f16(int n, bool bf16 = false)
@@ -957,26 +948,6 @@ __global__ void __launch_bounds__(XP_THREADS) q4_x_to_f16_kernel(const uint16_t 
 }
 
 // ------------------------------------------------------------------ host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 bool tc_eligible(int kind, int M, int N, int K)
 {
     (void)M;
@@ -1165,7 +1136,7 @@ q4_status tc_launch(int kind, const void *x, const uint8_t *codes, const void *s
     q4_status s = current_device(dev);
     if (s != Q4_OK)
         return s;
-    EncodeTiledFn enc = encode_fn();
+    EncodeTiledFn enc = tma_encode_fn();
     if (!enc)
         return fail(Q4_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     TcParams p = {};

@@ -1,0 +1,43 @@
+// Tiled copies on the TMA engine: tensor maps (host) and loads (device).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+#include "q4_internal.h"
+
+namespace q4 {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// The driver's tensor-map encoder (nullptr if there is none).
+EncodeTiledFn tma_encode_fn();
+
+// Map of bf16 rows [tokens][heads][D], token_stride elements from token to token: boxes of 64
+// columns, box_heads heads and box_tokens tokens, rows of 128 bytes in the 128-byte swizzle.
+q4_status tma_heads(CUtensorMap &map, const void *base, int D, int heads, uint64_t tokens, int64_t token_stride,
+                    int box_heads, int box_tokens);
+// Map of bf16 rows [rows][columns], stride elements from row to row: boxes of 64 columns and box_rows rows, the same
+// way.  What lies outside reads as zeros.
+q4_status tma_rows(CUtensorMap &map, const void *base, uint64_t columns, uint64_t rows, int64_t stride, int box_rows);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+                 : "memory");
+}
+#endif
+
+}  // namespace q4

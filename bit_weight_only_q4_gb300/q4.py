@@ -90,6 +90,7 @@ def load() -> ctypes.CDLL:
             "q4_kv_attention_shared": ([p, i64, p, i, i, i, i, i, p, i, p, i, p, i, i, i, f, p, p,
                                         sz, p], st),
             "q4_norm_rope": ([p, i64, p, p, i64, i, p, i64, p, p, i64, i, p, p, i, i, f, i, i, p], st),
+            "q4_prompt_attention": ([p, i64, p, i64, p, i64, p, i, i, i, i, i, f, p, p], st),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -108,7 +109,8 @@ def symbols() -> list[str]:
             "q4_dequant_nvfp4_f32", "q4_quantize_int4g128", "q4_quantize_nvfp4",
             "q4_embedding_int8", "q4_linear_int8", "q4_kv_block_bytes", "q4_kv_write",
             "q4_kv_read", "q4_kv_attention_workspace_bytes", "q4_kv_attention",
-            "q4_kv_attention_shared", "q4_test_kv_give_up", "q4_norm_rope"]
+            "q4_kv_attention_shared", "q4_test_kv_give_up", "q4_norm_rope",
+            "q4_prompt_attention"]
 
 
 def _check(status: int) -> None:
@@ -728,3 +730,43 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     if status:
         _check(status)
     return q_out, k_out
+
+
+def _prompt_plan(key, q, k, v, offsets):
+    """(tokens, batch, q heads, kv heads, D, strides, scale)"""
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError(f"q must be [tokens, q_heads, D], k and v [tokens, kv_heads, D], got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+    n = _kv_ints(offsets, "offsets", 1)[0]
+    if n < 1:
+        raise ValueError("offsets must hold the batch's sequences and one more")
+    (N, Hq, D), H = q.shape, k.shape[1]
+    return _kv_plan(key, (N, n - 1, Hq, H, D, _kv_rows(q, "q", q.shape), _kv_rows(k, "k", k.shape),
+                          _kv_rows(v, "v", v.shape), D**-0.5 if D else 1.0))
+
+
+def q4_prompt_attention(q, k, v, offsets, scale=None, out=None, stream=None):
+    """out [tokens, q_heads, D] (bf16) = causal attention within each of the packed sequences: the rows
+    offsets[b] .. offsets[b + 1] - 1 (int32 [batch + 1]) of q (bf16 [tokens, q_heads, D]) and of k and v
+    (bf16 [tokens, kv_heads, D]).  scale: D ** -0.5 if None.  Rows of no sequence are not written."""
+    key = "prompt", q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), offsets.shape
+    plan = _kv_plans.get(key)
+    bf16 = torch.bfloat16
+    if (plan is None or q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or
+            offsets.dtype is not torch.int32 or not offsets.is_contiguous()):
+        plan = _prompt_plan(key, q, k, v, offsets)
+    N, B, Hq, H, D, qs, ks, vs, s = plan
+    _here(q.get_device(), q=q, k=k, v=v, offsets=offsets, out=out)
+    if out is None:
+        out = _kv_empty(q.shape, q, stream)
+    elif _cuda(out, "out", torch.bfloat16).shape != q.shape:
+        raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    if N == 0 or B == 0:
+        return out
+    if scale is not None:
+        s = float(scale)
+    status = (_lib or load()).q4_prompt_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, offsets.data_ptr(),
+                                                  B, N, Hq, H, D, s, out.data_ptr(), _kv_stream(stream, q))
+    if status:
+        _check(status)
+    return out

@@ -393,6 +393,29 @@ q4_status q4_norm_rope(const void *q_bf16, int64_t q_stride, const void *q_weigh
                        const int32_t *positions, const float *inv_freq, int rotary_dim, int interleaved,
                        float eps, int tokens, int head_dim, void *stream);
 
+/*
+ * Causal attention over whole prompts, packed one behind the other: sequence b has the rows
+ * offsets[b] .. offsets[b + 1] - 1 of q, k and v, and each of its tokens sees those of its own
+ * sequence up to itself,
+ *     out = softmax(scale * q K^T) V.
+ *   q, k, v   bf16; token n, head h, column d at n * stride + h * head_dim + d (strides in elements,
+ *             multiples of 8; the parts of a fused q|k|v row work as they are)
+ *   offsets   int32 [batch + 1], rising, in device memory: nothing on the host depends on them.  A sequence
+ *             may be empty.  Rows that belong to no sequence are not written.  A sequence that would begin
+ *             before the end of one in front of it, or offsets outside 0 .. tokens, set Q4_DEVERR_INDEX; such
+ *             a sequence is left out, and such an offset counts as the nearest there is.
+ *   out       bf16 [tokens, q_heads, head_dim], apart from the inputs
+ * q_heads is a multiple of kv_heads, at most 128 times as many: query heads h * q_heads / kv_heads and on share the
+ * keys of head h.  head_dim 64 or 128; q, k, v, out 16-byte, offsets 4-byte aligned.
+ * Scores, softmax statistics and sums are fp32; the probabilities meet V as bf16, so that a result's error
+ * is at most 2^-8 of the weighted mean of |v|, and bf16's rounding (for values of V up to 2^100).  What a row does not see
+ * has no part in its result, whatever it holds.  Uses no workspace.
+ */
+q4_status q4_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf16, int64_t k_stride,
+                              const void *v_bf16, int64_t v_stride, const int32_t *offsets, int batch,
+                              int tokens, int q_heads, int kv_heads, int head_dim, float scale,
+                              void *out_bf16, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
