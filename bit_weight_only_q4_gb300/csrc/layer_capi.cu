@@ -1,5 +1,6 @@
 // C ABI of the operators around a layer's projections (include/q4.h): host-side validation,
-// then the launches of norm_rope.cu and prompt_attention.cu.
+// then the launches of norm_rope.cu, prompt_attention.cu, lora_few.cu and
+// lora_many.cu.
 #include "layer_ops.h"
 
 namespace q4 {
@@ -102,6 +103,49 @@ q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, in
     a.batch = batch, a.tokens = tokens, a.q_heads = q_heads, a.kv_heads = kv_heads;
     a.scale_log2 = scale * 1.44269504088896341f;
     return launch_prompt_attention(dev, a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
+}
+
+q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b, const float *scales, int adapters,
+                  int rank, const int32_t *offsets, const int32_t *ids, int batch, const void *base,
+                  int64_t base_stride, void *out, int64_t out_stride, int tokens, int N, int K, void *stream)
+{
+    if (!x || !a || !b || !scales || !offsets || !ids || !base || !out)
+        return fail(Q4_ERR_NULL, "x, a, b, scales, offsets, ids, base and out must not be NULL");
+    if (batch < 1 || tokens < 1 || adapters < 1)
+        return fail(Q4_ERR_SHAPE, "batch=%d, tokens=%d and adapters=%d must be >= 1", batch, tokens, adapters);
+    if (N < 8 || K < 8 || N % 8 || K % 8)
+        return fail(Q4_ERR_SHAPE, "N=%d and K=%d must be multiples of 8", N, K);
+    if (rank < 8 || rank > 128 || rank % 8)
+        return fail(Q4_ERR_SHAPE, "rank must be a multiple of 8 from 8 to 128 (got %d)", rank);
+    if (tokens > 0x07ffffff || batch > 0x07ffffff || N > 0x7fffff00 || K > 0x7fffff00)
+        return fail(Q4_ERR_SHAPE, "tokens=%d or batch=%d is above 2^27 - 1, or N=%d or K=%d too large", tokens, batch, N, K);
+    const int64_t most = (int64_t)1 << 38;
+    if (!row_stride_ok(x_stride, K) || !row_stride_ok(base_stride, N) || !row_stride_ok(out_stride, N) || x_stride > most ||
+        base_stride > most || out_stride > most)
+        return fail(Q4_ERR_SHAPE, "strides must be multiples of 8, at least K (x) and N (base, out) and at most 2^38");
+    if (base == out && base_stride != out_stride)
+        return fail(Q4_ERR_ARG, "in place, base and out have one stride");
+    if (!aligned_to(x, 16) || !aligned_to(a, 16) || !aligned_to(b, 16) || !aligned_to(base, 16) || !aligned_to(out, 16) ||
+        !aligned_to(scales, 4) || !aligned_to(offsets, 4) || !aligned_to(ids, 4))
+        return fail(Q4_ERR_ALIGN, "x, a, b, base and out must be 16-byte, scales, offsets and ids 4-byte aligned");
+    DeviceInfo dev;
+    const q4_status s = current_device(dev);
+    if (s != Q4_OK)
+        return s;
+    LoraArgs p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.a = static_cast<const uint16_t *>(a);
+    p.b = static_cast<const uint16_t *>(b);
+    p.base = static_cast<const uint16_t *>(base);
+    p.out = static_cast<uint16_t *>(out);
+    p.x_stride = x_stride, p.base_stride = base_stride, p.out_stride = out_stride;
+    p.scales = scales;
+    p.offsets = offsets, p.ids = ids;
+    p.batch = batch, p.tokens = tokens, p.adapters = adapters, p.rank = rank, p.N = N, p.K = K;
+    p.err = device_error_flags();
+    // Requests are judged by their mean length, for the lengths are on the device.
+    return tokens <= 8 * (int64_t)batch ? launch_lora_few(p, static_cast<cudaStream_t>(stream), pdl_on())
+                                        : launch_lora_many(p, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
 }  // extern "C"

@@ -34,4 +34,17 @@ struct PromptArgs {
 };
 q4_status launch_prompt_attention(const DeviceInfo &dev, PromptArgs a, int head_dim, cudaStream_t st, bool pdl);
 
+// ---- lora_few.cu, lora_many.cu
+struct LoraArgs {
+    const uint16_t *x, *a, *b, *base;
+    uint16_t *out;
+    int64_t x_stride, base_stride, out_stride;                 // elements from token to token
+    const float *scales;                                       // [adapters]
+    const int32_t *offsets, *ids;                              // [batch + 1], [batch]
+    int batch, tokens, adapters, rank, N, K;
+    unsigned *err;
+};
+q4_status launch_lora_few(const LoraArgs &a, cudaStream_t st, bool pdl);
+q4_status launch_lora_many(const LoraArgs &a, cudaStream_t st, bool pdl);
+
 }  // namespace q4

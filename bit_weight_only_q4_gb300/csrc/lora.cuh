@@ -1,0 +1,82 @@
+// What the two adapter kernels share: the request that a cluster works on, and clusters.
+//
+// For token m of a request with adapter a
+//     t = x_m A_a^T  (rank values),   out_m = base_m + scale_a (t B_a^T).
+// A cluster of eight CTAs takes a tile of a request's tokens through both products in one launch: each
+// CTA sums t over an eighth of K, the eight add their sums up through each other's shared memory, and
+// each then has an eighth of the output columns.  Sums are fp32; t meets B as bf16, as wide as x and B are.
+#pragma once
+
+#include "layer_ops.h"
+#include "segments.cuh"
+#include "tc_device.cuh"
+
+namespace q4 {
+
+constexpr int LR_CLUSTER = 8;
+
+__device__ __forceinline__ uint32_t lr_rank_in_cluster()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void lr_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void lr_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Address of this CTA's shared-memory address a in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t lr_map(uint32_t a, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float4 lr_load(uint32_t cluster_address)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_address));
+    return v;
+}
+
+// Part `rank` of n things shared out evenly.
+__device__ __forceinline__ int lr_share(int n, uint32_t rank) { return (int)((int64_t)n * rank / LR_CLUSTER); }
+
+// The tile of tokens that a cluster works on; false: none.
+struct LoraTile {
+    int row, rows, adapter;                // adapter < 0: base as it is
+};
+
+__device__ __forceinline__ bool lr_tile(const LoraArgs &p, int number, int span, LoraTile &t)
+{
+    SegmentWalk walk(Segments{p.offsets, p.batch, p.tokens, span, 1, p.err});
+    SegmentUnit u;
+    if (!walk.find(number, u))
+        return false;
+    const int first = u.unit * span;
+    t.row = u.start + first;
+    t.rows = u.len - first < span ? u.len - first : span;
+    t.adapter = __ldg(p.ids + u.sequence);
+    if (t.adapter >= p.adapters) {
+        if (p.err && (threadIdx.x & 31) == 0)
+            atomicOr(p.err, kErrIndex);
+        t.adapter = -1;
+    }
+    return true;
+}
+
+// A tile without an adapter: this CTA's columns of base, where out is not base itself.
+__device__ __forceinline__ void lr_copy(const LoraArgs &p, const LoraTile &t, uint32_t rank)
+{
+    if (p.out == p.base)
+        return;
+    const int c0 = lr_share(p.N / 8, rank), n = lr_share(p.N / 8, rank + 1) - c0;
+    for (int i = (int)threadIdx.x; i < t.rows * n; i += (int)blockDim.x) {
+        const int r = i / n, c = 8 * (c0 + i - r * n);
+        *reinterpret_cast<uint4 *>(p.out + (int64_t)(t.row + r) * p.out_stride + c) =
+            *reinterpret_cast<const uint4 *>(p.base + (int64_t)(t.row + r) * p.base_stride + c);
+    }
+}
+
+}  // namespace q4

@@ -24,6 +24,7 @@
 // mask are looked through for such values, and a tile that has one is multiplied by the softmax
 // threads themselves, over the tokens that a row sees.
 #include "layer_ops.h"
+#include "segments.cuh"
 #include "tc_device.cuh"
 #include "tma.h"
 
@@ -50,65 +51,26 @@ struct PaUnit {
     int na, nb;                  // key tiles of A and of B (0: B has no token)
 };
 
-// Hands out a warp's units in rising order of their number.  Units are numbered by sequence, then
-// from the last pair of tiles to the first, then by key head; sequences are taken in 32 at a time.
+// A warp's units.  Units are numbered by sequence, then from the last pair of tiles to the first, then
+// by key head.
 struct PaWalk {
     const PromptArgs &p;
-    int chunk, base, total, floor;         // first sequence of the 32 at hand, units before them and among them; rows taken
-    int start, len, before;                // this lane's sequence, units before it among the 32
+    SegmentWalk walk;
 
-    __device__ explicit PaWalk(const PromptArgs &args) : p(args), chunk(-32), base(0), total(0), floor(0), start(0), len(0), before(0) {}
+    __device__ explicit PaWalk(const PromptArgs &args)
+        : p(args), walk(Segments{args.offsets, args.batch, args.tokens, 2 * args.tile_tokens, args.kv_heads, args.err}) {}
 
     __device__ bool find(int number, PaUnit &u)
     {
-        const int lane = threadIdx.x & 31;
-        const int pair = 2 * p.tile_tokens;
-        while (number >= base + total) {
-            base += total;
-            chunk += 32;
-            if (chunk >= p.batch)
-                return false;
-            const int b = chunk + lane;
-            int lo = b < p.batch ? __ldg(p.offsets + b) : 0, hi = b < p.batch ? __ldg(p.offsets + b + 1) : 0;
-            const bool outside = lo < 0 || hi < 0 || lo > p.tokens || hi > p.tokens;
-            lo = lo < 0 ? 0 : lo > p.tokens ? p.tokens : lo;
-            hi = hi < 0 ? 0 : hi > p.tokens ? p.tokens : hi;
-            // Offsets that go back: what begins before the end of a sequence in front of it is left out, so that
-            // no row is written twice and the work stays bounded.
-            int top = hi;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int v = __shfl_up_sync(0xffffffffu, top, o);
-                top = lane >= o && v > top ? v : top;
-            }
-            int under = __shfl_up_sync(0xffffffffu, top, 1);
-            under = lane > 0 && under > floor ? under : floor;
-            const bool bad = b < p.batch && (hi < lo || lo < under);
-            if ((bad || outside) && p.err)
-                atomicOr(p.err, kErrIndex);
-            start = lo;
-            len = bad || hi < lo ? 0 : hi - lo;
-            const int all = __shfl_sync(0xffffffffu, top, 31);
-            floor = all > floor ? all : floor;
-            const int units = (len + pair - 1) / pair * p.kv_heads;
-            int sum = units;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int v = __shfl_up_sync(0xffffffffu, sum, o);
-                sum += lane >= o ? v : 0;
-            }
-            before = sum - units;
-            total = __shfl_sync(0xffffffffu, sum, 31);
-        }
-        const int at = number - base;
-        const int src = 31 - __clz(__ballot_sync(0xffffffffu, before <= at));
-        u.start = __shfl_sync(0xffffffffu, start, src);
-        u.len = __shfl_sync(0xffffffffu, len, src);
-        const int mine = at - __shfl_sync(0xffffffffu, before, src);
-        const int back = mine / p.kv_heads;
-        u.head = mine - back * p.kv_heads;
-        u.first = ((u.len + pair - 1) / pair - 1 - back) * pair;
-        const int t = p.tile_tokens, rest = u.len - u.first;
+        SegmentUnit f;
+        if (!walk.find(number, f))
+            return false;
+        const int t = p.tile_tokens, pair = 2 * t, back = f.unit / p.kv_heads;
+        u.start = f.start;
+        u.len = f.len;
+        u.head = f.unit - back * p.kv_heads;
+        u.first = ((f.len + pair - 1) / pair - 1 - back) * pair;
+        const int rest = u.len - u.first;
         u.na = (u.first + (rest < t ? rest : t) + PA_KEYS - 1) / PA_KEYS;
         u.nb = rest <= t ? 0 : (u.first + (rest < pair ? rest : pair) + PA_KEYS - 1) / PA_KEYS;
         return true;

@@ -91,6 +91,7 @@ def load() -> ctypes.CDLL:
                                         sz, p], st),
             "q4_norm_rope": ([p, i64, p, p, i64, i, p, i64, p, p, i64, i, p, p, i, i, f, i, i, p], st),
             "q4_prompt_attention": ([p, i64, p, i64, p, i64, p, i, i, i, i, i, f, p, p], st),
+            "q4_lora": ([p, i64, p, p, p, i, i, p, p, i, p, i64, p, i64, i, i, i, p], st),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -110,7 +111,7 @@ def symbols() -> list[str]:
             "q4_embedding_int8", "q4_linear_int8", "q4_kv_block_bytes", "q4_kv_write",
             "q4_kv_read", "q4_kv_attention_workspace_bytes", "q4_kv_attention",
             "q4_kv_attention_shared", "q4_test_kv_give_up", "q4_norm_rope",
-            "q4_prompt_attention"]
+            "q4_prompt_attention", "q4_lora"]
 
 
 def _check(status: int) -> None:
@@ -767,6 +768,64 @@ def q4_prompt_attention(q, k, v, offsets, scale=None, out=None, stream=None):
         s = float(scale)
     status = (_lib or load()).q4_prompt_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, offsets.data_ptr(),
                                                   B, N, Hq, H, D, s, out.data_ptr(), _kv_stream(stream, q))
+    if status:
+        _check(status)
+    return out
+
+
+def _lora_rows(t, name):
+    """Distance between the rows of a bf16 tensor [tokens, columns] whose columns are adjacent."""
+    if t.dim() != 2 or t.dtype is not torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [tokens, columns]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have adjacent columns, got strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _lora_plan(key, x, a, b, scales, offsets, ids, base):
+    """(tokens, batch, adapters, rank, N, K, strides)"""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError(f"a must be [adapters, rank, K] and b [adapters, N, rank], got {tuple(a.shape)} and {tuple(b.shape)}")
+    (n, r, K), N = a.shape, b.shape[1]
+    for t, name in ((a, "a"), (b, "b")):
+        _cuda(t, name, torch.bfloat16)
+    xs, bs = _lora_rows(x, "x"), _lora_rows(base, "base")
+    if x.shape[1] != K or base.shape[1] != N or base.shape[0] != x.shape[0]:
+        raise ValueError(f"x must be [tokens, {K}] and base [tokens, {N}], got {tuple(x.shape)} and {tuple(base.shape)}")
+    _vector(scales, "scales", n, torch.float32)
+    B = ids.numel()
+    _vector(ids, "ids", B, torch.int32)
+    _vector(offsets, "offsets", B + 1, torch.int32)
+    return _kv_plan(key, (x.shape[0], B, n, r, N, K, xs, bs))
+
+
+def q4_lora(x, a, b, scales, offsets, ids, base, out=None, stream=None):
+    """out [tokens, N] (bf16) = base + scales[i] * (x a[i]^T) b[i]^T with the adapter i = ids[r] of the
+    request r that the token belongs to (offsets[r] .. offsets[r + 1] - 1; negative: base as it is).  x bf16
+    [tokens, K]; a bf16 [adapters, rank, K]; b bf16 [adapters, N, rank]; scales fp32 [adapters]; offsets int32
+    [batch + 1]; ids int32 [batch]; base bf16 [tokens, N].  out=base works in place.  Rows of no request are not
+    written."""
+    key = "lora", x.shape, x.stride(), a.shape, b.shape, scales.shape, offsets.shape, ids.shape, base.shape, base.stride()
+    plan = _kv_plans.get(key)
+    bf16, i32 = torch.bfloat16, torch.int32
+    if (plan is None or x.dtype is not bf16 or a.dtype is not bf16 or b.dtype is not bf16 or base.dtype is not bf16 or
+            offsets.dtype is not i32 or ids.dtype is not i32 or scales.dtype is not torch.float32 or not
+            (a.is_contiguous() and b.is_contiguous() and offsets.is_contiguous() and ids.is_contiguous() and
+             scales.is_contiguous())):
+        plan = _lora_plan(key, x, a, b, scales, offsets, ids, base)
+    M, B, n, r, N, K, xs, bs = plan
+    _here(x.get_device(), x=x, a=a, b=b, scales=scales, offsets=offsets, ids=ids, base=base, out=out)
+    if out is None:
+        out, os_ = _kv_empty(base.shape, base, stream), N
+    elif out.shape != base.shape:
+        raise ValueError(f"out must be {tuple(base.shape)}, got {tuple(out.shape)}")
+    else:
+        os_ = _lora_rows(out, "out")
+    if M == 0 or B == 0:
+        return out
+    status = (_lib or load()).q4_lora(x.data_ptr(), xs, a.data_ptr(), b.data_ptr(), scales.data_ptr(), n, r,
+                                      offsets.data_ptr(), ids.data_ptr(), B, base.data_ptr(), bs, out.data_ptr(), os_, M, N,
+                                      K, _kv_stream(stream, x))
     if status:
         _check(status)
     return out

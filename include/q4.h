@@ -416,6 +416,29 @@ q4_status q4_prompt_attention(const void *q_bf16, int64_t q_stride, const void *
                               int tokens, int q_heads, int kv_heads, int head_dim, float scale,
                               void *out_bf16, void *stream);
 
+/*
+ * Low-rank adapters of many requests at once, beside a projection that they share: request b has
+ * the tokens offsets[b] .. offsets[b + 1] - 1 and the adapter a = ids[b], and for its rows
+ *     out = base + scales[a] * (x A[a]^T) B[a]^T.
+ * Requests may be of any lengths (single tokens of a decode step, drafts, prompts) and share adapters.
+ *   x         bf16 [tokens, K], x_stride elements from token to token
+ *   a, b      bf16 [adapters, rank, K] and [adapters, N, rank]; adapters of smaller ranks are filled up with zeros
+ *   scales    fp32 [adapters]
+ *   offsets   int32 [batch + 1], rising, ids int32 [batch], in device memory: nothing on the host depends on
+ *             them.  A request may be empty.  A negative id takes base as it is; an id past the
+ *             adapters does too and sets Q4_DEVERR_INDEX.  Rows of no request are not written; offsets that fall or
+ *             lie outside 0 .. tokens are taken as q4_prompt_attention takes them.
+ *   base, out bf16 [tokens, N] with their strides (columns of a wider row work as they are); either the
+ *             same (in place) or apart from all inputs
+ * N and K multiples of 8, rank a multiple of 8 from 8 to 128, strides multiples of 8; x, a, b, base and out
+ * 16-byte, scales, offsets and ids 4-byte aligned; at most 2^27 - 1 tokens and requests.  Products are bf16 with
+ * fp32 sums; x A^T is rounded to bf16 between them, the result once more.  Uses no workspace.
+ */
+q4_status q4_lora(const void *x_bf16, int64_t x_stride, const void *a_bf16, const void *b_bf16, const float *scales,
+                  int adapters, int rank, const int32_t *offsets, const int32_t *ids, int batch,
+                  const void *base_bf16, int64_t base_stride, void *out_bf16, int64_t out_stride, int tokens,
+                  int N, int K, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
