@@ -102,7 +102,7 @@ q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, in
     a.offsets = offsets;
     a.batch = batch, a.tokens = tokens, a.q_heads = q_heads, a.kv_heads = kv_heads;
     a.scale_log2 = scale * 1.44269504088896341f;
-    return launch_prompt_attention(dev, a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
+    return launch_prompt_attention(a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
 q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b, const float *scales, int adapters,

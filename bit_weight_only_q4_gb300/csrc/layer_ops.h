@@ -32,7 +32,7 @@ struct PromptArgs {
     int group, tile_tokens;                                    // (by the launch) query heads per key head, tokens of a tile
     unsigned *err;
 };
-q4_status launch_prompt_attention(const DeviceInfo &dev, PromptArgs a, int head_dim, cudaStream_t st, bool pdl);
+q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, bool pdl);
 
 // ---- lora_few.cu, lora_many.cu
 struct LoraArgs {

@@ -26,9 +26,8 @@ template <int STEPS>
 __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 32) lora_few_kernel(const LoraArgs p)
 {
     constexpr int RANKS = 16 * STEPS;
-    constexpr int KPARTS = LF_WARPS / STEPS;                // warps that share a row tile's columns of K
     constexpr int PITCH = RANKS + 8;
-    __shared__ __align__(16) float s_part[KPARTS][RANKS][LF_TOKENS], s_sum[RANKS][LF_TOKENS];
+    __shared__ __align__(16) float s_part[LF_WARPS][RANKS][LF_TOKENS], s_sum[RANKS][LF_TOKENS];
     __shared__ __align__(16) uint16_t s_t[LF_TOKENS][PITCH];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;                  // MMA: row (or token) and place within it
@@ -46,24 +45,38 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
 
     // ---- t over this CTA's columns of K
     {
-        const int m = warp % STEPS, part = warp / STEPS;
+        // 32 columns at a time for each warp: all rank values against one load of x
         const int k0 = lr_share((p.K + 31) / 32, rank), k1 = lr_share((p.K + 31) / 32, rank + 1);
-        const uint16_t *a = p.a + ((int64_t)tile.adapter * r + m * 16 + g) * p.K + 8 * t;
+        const uint16_t *a = p.a + ((int64_t)tile.adapter * r + g) * p.K + 8 * t;
         const uint16_t *x = p.x + (int64_t)(tile.row + g) * p.x_stride + 8 * t;
-        const bool row0 = m * 16 + g < r, row1 = m * 16 + g + 8 < r, token = g < tile.rows;
+        const bool token = g < tile.rows;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int k = k0 + part; k < k1; k += KPARTS) {
+        float c[STEPS][4];
+#pragma unroll
+        for (int m = 0; m < STEPS; ++m)
+            c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
+        constexpr int UNROLL = STEPS <= 2 ? 4 / STEPS : 1;
+#pragma unroll UNROLL
+        for (int k = k0 + warp; k < k1; k += LF_WARPS) {
             const bool in = 32 * k + 8 * t < p.K;
-            const uint4 a0 = in && row0 ? ld_stream_v4(a + 32 * k) : zero;
-            const uint4 a1 = in && row1 ? ld_stream_v4(a + (int64_t)8 * p.K + 32 * k) : zero;
             const uint4 b = in && token ? *reinterpret_cast<const uint4 *>(x + 32 * k) : zero;
-            lf_mma(c, a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-            lf_mma(c, a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+            uint4 w[STEPS][2];
+#pragma unroll
+            for (int m = 0; m < STEPS; ++m) {
+                w[m][0] = in && 16 * m + g < r ? ld_stream_v4(a + (int64_t)(16 * m) * p.K + 32 * k) : zero;
+                w[m][1] = in && 16 * m + g + 8 < r ? ld_stream_v4(a + (int64_t)(16 * m + 8) * p.K + 32 * k) : zero;
+            }
+#pragma unroll
+            for (int m = 0; m < STEPS; ++m) {
+                lf_mma(c[m], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, b.x, b.y);
+                lf_mma(c[m], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, b.z, b.w);
+            }
         }
-        *reinterpret_cast<float2 *>(&s_part[part][m * 16 + g][2 * t]) = make_float2(c[0], c[1]);
-        *reinterpret_cast<float2 *>(&s_part[part][m * 16 + g + 8][2 * t]) = make_float2(c[2], c[3]);
+#pragma unroll
+        for (int m = 0; m < STEPS; ++m) {
+            *reinterpret_cast<float2 *>(&s_part[warp][m * 16 + g][2 * t]) = make_float2(c[m][0], c[m][1]);
+            *reinterpret_cast<float2 *>(&s_part[warp][m * 16 + g + 8][2 * t]) = make_float2(c[m][2], c[m][3]);
+        }
     }
     // ---- the first of the B rows and base values that this warp needs are on their way during the exchange
     const int n0 = lr_share((p.N + 15) / 16, rank), n1 = lr_share((p.N + 15) / 16, rank + 1);
@@ -93,7 +106,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
     for (int i = tid; i < RANKS * LF_TOKENS / 4; i += LF_WARPS * 32) {
         float4 v = reinterpret_cast<const float4 *>(s_part[0])[i];
 #pragma unroll
-        for (int k = 1; k < KPARTS; ++k) {
+        for (int k = 1; k < LF_WARPS; ++k) {
             const float4 w = reinterpret_cast<const float4 *>(s_part[k])[i];
             v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
         }

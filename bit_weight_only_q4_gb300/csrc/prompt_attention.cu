@@ -14,11 +14,15 @@
 // reference raised and what was summed scaled down.  So a tile that is seen whole costs one pass over its scores and no maximum.
 //
 // One CTA per SM, 12 warps: four with the softmax of A (one thread a row), four with that of
-// B, one that copies (TMA), one that issues the MMAs.  S and O of both tiles fill the tensor
-// memory; P takes the place of its S.  MMAs run in the order
-//     .. P_A V(t)  S_A(t+1)  P_B V(t)  S_B(t+1)  P_A V(t+1) ..
-// so that the tensor cores work on one tile while the other is in its softmax, and an S
-// is overwritten by an MMA that comes behind the one that reads P in its place.
+// B, one that copies (TMA), one that issues the MMAs.  A step is one tile of rows on one tile of keys; A and
+// B take turns.  Step n has its S in buffer n mod BUFS of tensor memory, and P takes the place of
+// its S.  MMAs run in the order
+//     .. P(n) V  S(n + BUFS)  P(n + 1) V  S(n + 1 + BUFS) ..
+// so that the tensor cores work on one tile of rows while the other is in its softmax, and an S is
+// overwritten by an MMA that comes behind the one that reads P in its place.  With heads of 128, two S
+// and two O fill the tensor memory, and P is handed over in two halves, so that less of a step's
+// softmax lies between two MMAs of its rows; with heads of 64 there is room for a third S, and the softmax of a step
+// follows that of the rows' last one without a wait.
 //
 // A masked probability is 0, and 0 times a v that is not finite would be NaN: tiles cut by the
 // mask are looked through for such values, and a tile that has one is multiplied by the softmax
@@ -31,11 +35,13 @@
 namespace q4 {
 
 constexpr int PA_ROWS = 128, PA_KEYS = 128;
-constexpr int PA_COPY = 8, PA_MMA = 9, PA_WARPS = 12;
+constexpr int PA_COPY = 8, PA_MMA = 9, PA_NEXT = 10, PA_WARPS = 12;
+constexpr int PA_QUEUE = 2;                // units that a CTA has been given and not begun
 constexpr float PA_SUM_TOP = 0x1p20f;
 
 template <int D>
 struct PaSmem {
+    static constexpr int BUFS = D == 128 ? 2 : 3, HALVES = D == 128 ? 2 : 1;
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t TILE = PA_KEYS * D * 2;
     static constexpr uint32_t RING = 2 * TILE;                       // [Q of A, Q of B][ring][staging]
@@ -77,11 +83,58 @@ struct PaWalk {
     }
 };
 
-// Unit number of a CTA's round: to and fro, for neighbouring numbers cost alike and fall.
-__device__ __forceinline__ int pa_number(int round)
+// 32 scores of a row to probabilities: ta, tb += 2^(s sl + neg), p <- the same as bf16.  CUT: columns from `at` on
+// past `seen` count as none.
+template <bool CUT>
+__device__ __forceinline__ void pa_exp(const uint32_t (&s)[32], uint32_t *p, f32x2 sl2, f32x2 neg2, f32x2 &ta, f32x2 &tb,
+                                       int at, int seen)
 {
-    const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
-    return round * grid + ((round & 1) ? grid - 1 - cta : cta);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const f32x2 a = fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sl2, neg2);
+        const f32x2 b = fma2(pack2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), sl2, neg2);
+        float e[4];
+        unpack2(a, e[0], e[1]);
+        unpack2(b, e[2], e[3]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if (CUT)
+                e[y] = at + i + y <= seen ? e[y] : -INFINITY;
+            e[y] = ex2(e[y]);
+        }
+        ta = add2(ta, pack2(e[0], e[1]));
+        tb = add2(tb, pack2(e[2], e[3]));
+        p[i / 2] = bf16_pair(e[0], e[1]);
+        p[i / 2 + 1] = bf16_pair(e[2], e[3]);
+    }
+}
+
+// Asks for a CTA of the grid that has not begun, to have its work instead: 16 bytes at `to`, counted on `bar`.
+__device__ __forceinline__ void pa_ask(uint32_t to, uint32_t bar)
+{
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(to), "r"(bar) : "memory");
+}
+
+// The answer: that CTA's number, or -1 (no question may be asked after that).
+__device__ __forceinline__ int pa_answer(uint32_t at)
+{
+    int r;
+    asm volatile("{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+                 "ld.shared.b128 h, [%1];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+                 "mov.s32 %0, -1;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+                 : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+
+template <int BUFS>
+__device__ __forceinline__ int pa_next(int buf, int steps)
+{
+    buf += steps;
+    return buf >= BUFS ? buf - BUFS : buf;
 }
 
 template <int D>
@@ -91,19 +144,32 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
 {
     using L = PaSmem<D>;
     constexpr int NS = L::STAGES;
-    constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;          // of A; B 128 columns behind
+    constexpr int BUFS = L::BUFS, HALVES = L::HALVES, CH = PA_KEYS / HALVES;
+    constexpr uint32_t TM_S = 0, TM_O = 128 * BUFS, TM_COLS = 512;   // buffers of S, O of A and of B
+    static_assert(TM_O + 2 * D <= TM_COLS, "tensor memory");
     constexpr uint32_t BF16 = (1u << 7) | (1u << 10);
     constexpr uint32_t IDESC_S = (1u << 4) | BF16 | ((uint32_t)(PA_KEYS >> 3) << 17) | (8u << 24);
     constexpr uint32_t IDESC_O = (1u << 4) | BF16 | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 12];
+    __shared__ uint64_t s_bar[2 * NS + 4 + 2 * HALVES + BUFS * (2 + HALVES) + 2 * PA_QUEUE + 1];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_dead, s_skip[2];
+    __shared__ __align__(16) uint4 s_answer;
+    __shared__ int s_unit[PA_QUEUE];
+    __shared__ int s_dead, s_skip[BUFS];
     const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
     const uint32_t kv_full = smem_u32(s_bar), kv_free = kv_full + 8u * NS, q_full = kv_free + 8u * NS,   // q_full: A, B
-                   q_free = q_full + 16, s_full = q_full + 24, p_full = q_full + 40, o_full = q_full + 56, drained = q_full + 72;
+                   q_free = q_full + 16, drained = q_full + 24, pv_done = q_full + 32,      // pv_done: by tile and half
+                   s_full = pv_done + 16u * HALVES,            // by tile and buffer: each phase has one waiter, who misses none
+                   p_full = s_full + 16u * BUFS,               // by buffer and half
+                   unit_full = p_full + 8u * BUFS * HALVES, unit_free = unit_full + 8u * PA_QUEUE,
+                   answered = unit_free + 8u * PA_QUEUE;
+    pdl_wait();
+    PaWalk walk(p);
+    PaUnit u;
+    if (!walk.find((int)blockIdx.x, u))
+        return;                                            // (the whole CTA)
     if (warp == PA_COPY) {
         if (lane == 0) {
             for (int i = 0; i < NS; ++i) {
@@ -112,12 +178,20 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             }
             mbar_init(q_free, 1);
             mbar_init(drained, 1);
+            mbar_init(answered, 1);
+            for (int i = 0; i < PA_QUEUE; ++i) {
+                mbar_init(unit_full + 8u * i, 1);
+                mbar_init(unit_free + 8u * i, 10);
+            }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(q_full + 8u * i, 1);
-                mbar_init(s_full + 8u * i, 1);
-                mbar_init(p_full + 8u * i, 4);
-                mbar_init(o_full + 8u * i, 1);
+                for (int half = 0; half < HALVES; ++half)
+                    mbar_init(pv_done + 8u * (i * HALVES + half), 1);
             }
+            for (int i = 0; i < 2 * BUFS; ++i)
+                mbar_init(s_full + 8u * i, 1);
+            for (int i = 0; i < BUFS * HALVES; ++i)
+                mbar_init(p_full + 8u * i, 4);
             s_dead = 0;
         }
         mbar_init_fence();
@@ -130,11 +204,20 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-    pdl_wait();
     const KvDead dead = {p.err, &s_dead, smem_u32(&s_dead)};
     auto gone_all = [&]() { return __any_sync(0xffffffffu, *dead.flag != 0); };
-    PaWalk walk(p);
-    PaUnit u;
+    // The CTA's unit of a round, the first being its own; false: there is none.
+    auto unit = [&](int round) {
+        if (round == 0)
+            return true;
+        const int slot = (round - 1) % PA_QUEUE;
+        kv_wait(unit_full + 8u * slot, (uint32_t)((round - 1) / PA_QUEUE) & 1u, dead);
+        const int number = *(volatile int *)&s_unit[slot];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(unit_free + 8u * slot);
+        return number >= 0 && walk.find(number, u);
+    };
 
     if (warp < 8) {
         // ------------------------------------------ softmax and results
@@ -143,13 +226,29 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         const int row = quad * 32 + lane;
         const int row_token = row / p.group, row_head = row - row_token * p.group;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t t_s = t_lane + TM_S + 128u * x, t_o = t_lane + TM_O + 128u * x;
+        const uint32_t t_o = t_lane + TM_O + (uint32_t)(D * x);
         const float sl = p.scale_log2;
         const f32x2 sl2 = pack2(sl, sl);
-        uint32_t ring = 0u, tiles = 0u, units = 0u;        // of the copies before this unit; of this tile's S and O
+        uint32_t ring = 0u, steps = 0u, pv_count = 0u, phases = 0u;       // copies and this tile's steps before; parity of its S in each buffer
+        const uint32_t pv_first = pv_done + 8u * (uint32_t)(x * HALVES), pv_last = pv_first + 8u * (HALVES - 1);
+        // The step before is through its MMAs.  With two buffers its S is overwritten by this step's, which came behind
+        // them; with three, each step waits for the one before it, so that no barrier is ever two phases from the one
+        // that is waited for.
+        auto last_step = [&]() {
+            if (BUFS == 3 && pv_count > 0)
+                kv_wait(pv_last, (pv_count - 1u) & 1u, dead);
+        };
+        // And so are the halves of this step before half `half`.
+        auto pv_wait = [&](int half) {
+            last_step();
+            if (half > 0)
+                kv_wait(pv_first, steps & 1u, dead);
+            tc_fence_after();
+        };
 #pragma unroll 1
-        for (int round = 0; walk.find(pa_number(round), u); ++round) {
-            if (bar_or(1 + x, 128, *dead.flag != 0))       // leave together
+        for (int round = 0;; ++round) {
+            const bool have = unit(round);
+            if (bar_or(1 + x, 128, !have || *dead.flag != 0))          // leave together
                 break;
             const int n = u.nb > 0 ? u.nb : u.na, mine = x ? u.nb : u.na;
             const int first = u.first + x * p.tile_tokens;
@@ -158,136 +257,184 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             const int whole = (first + 1) / PA_KEYS;       // key tiles that all rows see wholly
             float m = -INFINITY;
             f32x2 la = 0ull, lb = 0ull;
+            int buf = 0;
 #pragma unroll 1
-            for (int j = mine - 1; j >= 0; --j) {
-                kv_wait(s_full + 8u * x, tiles & 1u, dead);
-                ++tiles;
-                tc_fence_after();
+            for (int j = n - 1; j >= 0; --j) {
+                // the step's buffer; A has none on the last tile of keys where that is B's alone
+                const bool both = u.nb > 0 && j < u.na;
+                const int at_buf = BUFS == 2 ? x : both && x ? pa_next<BUFS>(buf, 1) : buf;
+                buf = pa_next<BUFS>(buf, both ? 2 : 1);
+                if (j >= mine)
+                    continue;
+                const uint32_t parity = (phases >> at_buf) & 1u;
+                phases ^= 1u << at_buf;
+                const uint32_t t_s = t_lane + TM_S + 128u * (uint32_t)at_buf;
                 const bool masked = j >= whole;
-                uint32_t ph[PA_KEYS / 2];
-                bool careful = masked || __any_sync(0xffffffffu, token >= 0 && m == -INFINITY);
-                if (!careful) {
-                    const f32x2 n2 = pack2(-m, -m);
-                    f32x2 ta = 0ull, tb = 0ull;
-                    uint32_t v[2][32];
-                    tmem_ld32_async(t_s, v[0]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c < 3)
-                            tmem_ld32_async(t_s + 32u * (c + 1), v[(c + 1) & 1]);
-                        const uint32_t (&w)[32] = v[c & 1];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            f32x2 a = fma2(pack2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), sl2, n2);
-                            f32x2 b = fma2(pack2(__uint_as_float(w[i + 2]), __uint_as_float(w[i + 3])), sl2, n2);
-                            float e[4];
-                            unpack2(a, e[0], e[1]);
-                            unpack2(b, e[2], e[3]);
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                e[y] = ex2(e[y]);
-                            ta = add2(ta, pack2(e[0], e[1]));
-                            tb = add2(tb, pack2(e[2], e[3]));
-                            ph[16 * c + i / 2] = bf16_pair(e[0], e[1]);
-                            ph[16 * c + i / 2 + 1] = bf16_pair(e[2], e[3]);
-                        }
-                        if (c < 3)
-                            tmem_wait_ld();
-                    }
-                    float sa, sb;
-                    unpack2(add2(ta, tb), sa, sb);
-                    careful = __any_sync(0xffffffffu, token >= 0 && !(sa + sb < PA_SUM_TOP));
-                    if (!careful) {
-                        la = add2(la, ta);
-                        lb = add2(lb, tb);
-                    }
-                }
-                const int seen = token - j * PA_KEYS;      // the row's last visible column
-                if (careful) {
-                    float want = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32_async(t_s + 32u * c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float s = __uint_as_float(v[i]) * sl;
-                            want = 32 * c + i <= seen ? fmaxf(want, s) : want;
-                        }
-                    }
-                    if (__any_sync(0xffffffffu, want > m)) {
-                        const float old = m;
-                        m = fmaxf(m, want);
-                        const float f = old == -INFINITY ? 0.f : ex2(old - m);
-                        const f32x2 f2 = pack2(f, f);
-                        la = mul2(la, f2);
-                        lb = mul2(lb, f2);
-                        if (j < mine - 1) {                // (the MMAs of the tile before are done: S came behind them)
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32_async(t_o + c, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st32(t_o + c, o);
-                            }
-                            tmem_wait_st();
-                        }
-                    }
-                    const float neg = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32_async(t_s + 32u * c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a = ex2(fmaf(__uint_as_float(v[i]), sl, neg)), b = ex2(fmaf(__uint_as_float(v[i + 1]), sl, neg));
-                            a = 32 * c + i <= seen ? a : 0.f;
-                            b = 32 * c + i + 1 <= seen ? b : 0.f;
-                            la = add2(la, pack2(a, b));
-                            ph[16 * c + i / 2] = bf16_pair(a, b);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < PA_KEYS / 2; c += 32)
-                    tmem_st32(t_s + c, reinterpret_cast<uint32_t(&)[32]>(ph[c]));
-                tmem_wait_st();
+                const int seen = token >= 0 ? token - j * PA_KEYS : PA_KEYS - 1;      // the row's last visible column
+                int hi = PA_KEYS - 1;
+                bool skip = false;
+                const uint32_t v_at = ring + 2u * (uint32_t)(n - 1 - j) + 1u;
+                const uint32_t v_tile = sm + L::RING + (v_at & (NS - 1)) * L::TILE;
+                kv_wait(s_full + 8u * (uint32_t)(x * BUFS + at_buf), parity, dead);
+                tc_fence_after();
                 if (masked) {
-                    // one row of v for each thread: is there anything that is not finite?
-                    const uint32_t at = ring + 2u * (uint32_t)(n - 1 - j) + 1u;
-                    const uint32_t v = sm + L::RING + (at & (NS - 1)) * L::TILE;
-                    kv_wait(kv_full + 8u * (at & (NS - 1)), (at / NS) & 1u, dead);
+                    hi = __reduce_max_sync(0xffffffffu, seen);
+                    // one row of v for each thread: is there anything that is not finite?  (Behind the wait for S: what the
+                    // ring's stage held before has been loaded by then, so that the phase is this one or the next.)
+                    kv_wait(kv_full + 8u * (v_at & (NS - 1)), (v_at / NS) & 1u, dead);
                     uint32_t bad = 0u;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
-                        const uint4 e = lds128(v + (uint32_t)(c >> 3) * 16384u + (uint32_t)row * 128u + 16u * ((uint32_t)(c ^ row) & 7u));
+                        const uint4 e = lds128(v_tile + (uint32_t)(c >> 3) * 16384u + (uint32_t)row * 128u + 16u * ((uint32_t)(c ^ row) & 7u));
                         bad |= ((e.x & 0x7f807f80u) + 0x00800080u) | ((e.y & 0x7f807f80u) + 0x00800080u) |
                                ((e.z & 0x7f807f80u) + 0x00800080u) | ((e.w & 0x7f807f80u) + 0x00800080u);
                     }
-                    const bool skip = bar_or(1 + x, 128, (bad & 0x80008000u) != 0u);
+                    skip = bar_or(1 + x, 128, (bad & 0x80008000u) != 0u);
+                }
+                if (row == 0)
+                    s_skip[at_buf] = skip;
+#pragma unroll 1
+                for (int half = 0; half < HALVES; ++half) {
+                    const int c0 = half * CH;
+                    uint32_t ph[CH / 2];
+                    bool careful = false;
+                    if (!masked && !__any_sync(0xffffffffu, token >= 0 && m == -INFINITY)) {
+                        uint32_t v[2][32];
+                        tmem_ld32_async(t_s + (uint32_t)c0, v[0]);
+                        tmem_wait_ld();
+                        const f32x2 n2 = pack2(-m, -m);
+                        f32x2 ta = 0ull, tb = 0ull;
+#pragma unroll
+                        for (int c = 0; c < CH / 32; ++c) {
+                            if (c + 1 < CH / 32)
+                                tmem_ld32_async(t_s + (uint32_t)(c0 + 32 * (c + 1)), v[(c + 1) & 1]);
+                            pa_exp<false>(v[c & 1], ph + 16 * c, sl2, n2, ta, tb, 0, 0);
+                            if (c + 1 < CH / 32)
+                                tmem_wait_ld();
+                        }
+                        float sa, sb;
+                        unpack2(add2(ta, tb), sa, sb);
+                        careful = __any_sync(0xffffffffu, token >= 0 && !(sa + sb < PA_SUM_TOP));
+                        if (!careful) {
+                            la = add2(la, ta);
+                            lb = add2(lb, tb);
+                        }
+                    } else if (c0 > hi) {
+#pragma unroll
+                        for (int i = 0; i < CH / 2; ++i)
+                            ph[i] = 0u;
+                    } else {
+                        f32x2 ta = 0ull, tb = 0ull;
+#pragma unroll
+                        for (int c = 0; c < CH / 32; ++c) {
+                            const int at = c0 + 32 * c;
+                            if (at > hi) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    ph[16 * c + i] = 0u;
+                                continue;
+                            }
+                            uint32_t v[32];
+                            tmem_ld32_async(t_s + (uint32_t)at, v);
+                            tmem_wait_ld();
+                            if (c == 0 && __any_sync(0xffffffffu, token >= 0 && m == -INFINITY)) {
+                                // the first reference: the largest of the first 32 scores that are seen
+                                float want = -INFINITY;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    want = at + i <= seen ? fmaxf(want, __uint_as_float(v[i]) * sl) : want;
+                                if (m == -INFINITY)
+                                    m = want;
+                                careful = __any_sync(0xffffffffu, token >= 0 && seen >= at && m == -INFINITY);
+                            }
+                            const float neg = m == -INFINITY ? 0.f : -m;
+                            pa_exp<true>(v, ph + 16 * c, sl2, pack2(neg, neg), ta, tb, at, seen);
+                        }
+                        float sa, sb;
+                        unpack2(add2(ta, tb), sa, sb);
+                        careful = careful || __any_sync(0xffffffffu, token >= 0 && !(sa + sb < PA_SUM_TOP));
+                        if (!careful) {
+                            la = add2(la, ta);
+                            lb = add2(lb, tb);
+                        }
+                    }
+                    const bool begun = j < mine - 1 || half > 0;       // O holds something
+                    if (careful) {
+                        // again, with the half's largest score as the reference
+                        float want = -INFINITY;
+#pragma unroll 1
+                        for (int c = c0; c < c0 + CH; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32_async(t_s + (uint32_t)c, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float s = __uint_as_float(v[i]) * sl;
+                                want = c + i <= seen ? fmaxf(want, s) : want;
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, want > m)) {
+                            const float old = m;
+                            m = fmaxf(m, want);
+                            const float f = old == -INFINITY ? 0.f : ex2(old - m);
+                            const f32x2 f2 = pack2(f, f);
+                            la = mul2(la, f2);
+                            lb = mul2(lb, f2);
+                            if (begun) {
+                                pv_wait(half);
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 32) {
+                                    uint32_t o[32];
+                                    tmem_ld32_async(t_o + c, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tmem_st32(t_o + c, o);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                        const float neg = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                        for (int c = 0; c < CH / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_ld32_async(t_s + (uint32_t)(c0 + 32 * c), v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float a = ex2(fmaf(__uint_as_float(v[i]), sl, neg)), b = ex2(fmaf(__uint_as_float(v[i + 1]), sl, neg));
+                                a = c0 + 32 * c + i <= seen ? a : 0.f;
+                                b = c0 + 32 * c + i + 1 <= seen ? b : 0.f;
+                                la = add2(la, pack2(a, b));
+                                ph[16 * c + i / 2] = bf16_pair(a, b);
+                            }
+                        }
+                    }
+                    const uint32_t t_p = t_s + (uint32_t)c0;
+#pragma unroll
+                    for (int c = 0; c < CH / 2; c += 32)
+                        tmem_st32(t_p + c, reinterpret_cast<uint32_t(&)[32]>(ph[c]));
+                    tmem_wait_st();
                     if (skip) {
                         // O += P V over the tokens that the row sees, 16 columns at a time
+                        if (begun)
+                            pv_wait(half);
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float o[16];
                             uint32_t w[16];
-                            if (j < mine - 1)
+                            if (begun)
                                 tmem_ld16(t_o + c, w);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                o[i] = j < mine - 1 ? __uint_as_float(w[i]) : 0.f;
+                                o[i] = begun ? __uint_as_float(w[i]) : 0.f;
 #pragma unroll 1
-                            for (int k = 0; k < PA_KEYS; ++k) {
+                            for (int k = c0; k < c0 + CH; ++k) {
                                 uint32_t pk;
-                                tmem_ld1(t_s + (k >> 1), pk);
+                                tmem_ld1(t_p + ((k - c0) >> 1), pk);
                                 const float pf = __uint_as_float((k & 1) ? pk & 0xffff0000u : pk << 16);
-                                const uint32_t r = v + (uint32_t)(c >> 6) * 16384u + (uint32_t)k * 128u;
+                                const uint32_t r = v_tile + (uint32_t)(c >> 6) * 16384u + (uint32_t)k * 128u;
                                 const uint32_t piece = (uint32_t)(c >> 3) & 7u;
                                 const uint4 e0 = lds128(r + 16u * (piece ^ ((uint32_t)k & 7u)));
                                 const uint4 e1 = lds128(r + 16u * ((piece + 1u) ^ ((uint32_t)k & 7u)));
@@ -307,22 +454,22 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                         }
                         tmem_wait_st();
                     }
-                    if (row == 0)
-                        s_skip[x] = skip;
-                } else if (row == 0) {
-                    s_skip[x] = 0;
+                    if (half == HALVES - 1)
+                        last_step();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(p_full + 8u * (uint32_t)(at_buf * HALVES + half));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(p_full + 8u * x);
+                if (BUFS == 3 || j == 0)
+                    ++pv_count;
+                ++steps;
             }
             ring += 2u * (uint32_t)n;
             if (mine == 0)
                 continue;
             // ---- the unit's results
-            kv_wait(o_full + 8u * x, units & 1u, dead);
-            ++units;
+            kv_wait(pv_last, (pv_count - 1u) & 1u, dead);
             tc_fence_after();
             float l0, l1;
             unpack2(add2(la, lb), l0, l1);
@@ -367,7 +514,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         uint32_t at = 0u;
         uint32_t loads[2] = {0u, 0u};
 #pragma unroll 1
-        for (int round = 0; walk.find(pa_number(round), u) && !gone_all(); ++round) {
+        for (int round = 0; unit(round) && !gone_all(); ++round) {
             const int n = u.nb > 0 ? u.nb : u.na;
 #pragma unroll 1
             for (int i = 0; i < 2 * n && !gone_all(); ++i, ++at) {
@@ -416,94 +563,174 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         }
     } else if (warp == PA_MMA) {
         // -------------------------------------------------------- MMAs
-        uint32_t at = 0u;                                  // copies before this unit
-        uint32_t qn[2] = {0u, 0u}, pn[2] = {0u, 0u};       // Q loads and P's before
+        // This warp is what the tensor cores wait for, so the two tiles are written out (x is known where it is
+        // compiled) and everything that an MMA takes is the warp's: such an MMA takes 30 (PV) and 52 cycles (S) to
+        // issue, of the 64 or 32 that it runs.
+        uint32_t at = 0u, qn = 0u, phases = 0u;            // copies before this unit; parities of Q loads and of P's
         const uint64_t qd = smem_desc_sw128(sm), kd = smem_desc_sw128(sm + L::RING);
         const uint64_t vd = (kd & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(D == 128 ? PA_KEYS * 128 >> 4 : 0) << 16);
         const uint32_t q_lo = (uint32_t)qd, q_hi = (uint32_t)(qd >> 32), k_lo = (uint32_t)kd, k_hi = (uint32_t)(kd >> 32),
                        v_lo = (uint32_t)vd, v_hi = (uint32_t)(vd >> 32);
-        auto scores = [&](uint32_t x, uint32_t stage) {    // S of tile x
-            if (elect_one()) {
-                const uint32_t a = q_lo + x * (L::TILE >> 4), b = k_lo + stage * (L::TILE >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t step = (uint32_t)(kk >> 2) * (16384u >> 4) + 2u * (kk & 3);
-                    mma_f16_2(tmem + TM_S + 128u * x, a + step, q_hi, b + step, k_hi, IDESC_S, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(s_full + 8u * x);
-            }
-            __syncwarp();
-        };
 #pragma unroll 1
-        for (int round = 0; walk.find(pa_number(round), u) && !gone_all(); ++round) {
-            const int nb = __shfl_sync(0xffffffffu, u.nb, 0), na = __shfl_sync(0xffffffffu, u.na, 0);
-            const int n = nb > 0 ? nb : na;
-            bool begun[2] = {false, false};                // O holds something
-            auto active = [&](int x, int t) { return x ? nb > 0 : t >= n - na; };
-            auto score_step = [&](int x, int t) {
-                if (!active(x, t))
-                    return;
-                if (t == (x ? 0 : n - na)) {
-                    kv_wait(q_full + 8u * x, qn[x] & 1u, dead);
-                    ++qn[x];
+        for (int round = 0; unit(round) && !gone_all(); ++round) {
+            const int nb = __shfl_sync(0xffffffffu, u.nb, 0), na = __shfl_sync(0xffffffffu, u.na, 0),
+                      begin = __shfl_sync(0xffffffffu, u.first, 0);
+            const bool pair = nb > 0;
+            const int n = pair ? nb : na, late = n - na;   // tiles of keys that A begins behind B
+            const int cut[2] = {n - (begin + 1) / PA_KEYS, n - (begin + p.tile_tokens + 1) / PA_KEYS};   // that the mask cuts
+            // S of tile x on the t-th tile of keys
+            auto score = [&](int x, int t, int buf) {
+                const uint32_t k = at + 2u * (uint32_t)t, stage = k & (NS - 1);
+                if (t == (x ? 0 : late)) {
+                    kv_wait(q_full + 8u * x, (qn >> x) & 1u, dead);
+                    qn ^= 1u << x;
                 }
+                if (x == 0 || t == 0)                      // (B's S comes behind A's, but for the first)
+                    kv_wait(kv_full + 8u * stage, (k / NS) & 1u, dead);
                 tc_fence_after();
-                scores((uint32_t)x, (at + 2u * t) & (NS - 1));
-            };
-            auto keys_wait = [&](int t) {
-                const uint32_t i = at + 2u * t;
-                kv_wait(kv_full + 8u * (i & (NS - 1)), (i / NS) & 1u, dead);
-            };
-            auto release = [&](uint32_t bar) {
-                if (elect_one())
-                    mma_commit(bar);
+                if (elect_one()) {
+                    const uint32_t a = q_lo + (uint32_t)x * (L::TILE >> 4), b = k_lo + stage * (L::TILE >> 4),
+                                   d = tmem + TM_S + 128u * (uint32_t)buf;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t step = (uint32_t)(kk >> 2) * (16384u >> 4) + 2u * (kk & 3);
+                        mma_f16_2(d, a + step, q_hi, b + step, k_hi, IDESC_S, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(s_full + 8u * (uint32_t)(x * BUFS + buf));
+                    if (x == 1 || !pair) {                 // the last with these keys
+                        mma_commit(kv_free + 8u * stage);
+                        if (t == n - 1)
+                            mma_commit(q_free);
+                    }
+                }
                 __syncwarp();
             };
-            keys_wait(0);
-            score_step(0, 0);
-            score_step(1, 0);
-            release(kv_free + 8u * (at & (NS - 1)));
-            if (n == 1)
-                release(q_free);
-#pragma unroll 1
-            for (int t = 0; t < n && !gone_all(); ++t) {
-                const uint32_t vi = at + 2u * t + 1u, vs = vi & (NS - 1);
-                kv_wait(kv_full + 8u * vs, (vi / NS) & 1u, dead);
+            // O of tile x += P V
+            auto add = [&](int x, int t, int buf) {
+                const uint32_t k = at + 2u * (uint32_t)t + 1u, stage = k & (NS - 1);
+                if (x == 0 || t < late)
+                    kv_wait(kv_full + 8u * stage, (k / NS) & 1u, dead);
+                const bool masked = t < cut[x], first = t == (x ? 0 : late);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (active(x, t)) {
-                        kv_wait(p_full + 8u * x, pn[x] & 1u, dead);
-                        ++pn[x];
-                        tc_fence_after();
-                        const bool skip = __shfl_sync(0xffffffffu, *(volatile int *)&s_skip[x], 0) != 0;
-                        if (elect_one()) {
-                            if (!skip) {
-                                const uint32_t b = v_lo + vs * (L::TILE >> 4);
+                for (int half = 0; half < HALVES; ++half) {
+                    kv_wait(p_full + 8u * (uint32_t)(buf * HALVES + half), (phases >> buf) & 1u, dead);
+                    tc_fence_after();
+                    const bool skip = masked && __shfl_sync(0xffffffffu, *(volatile int *)&s_skip[buf], 0) != 0;
+                    if (elect_one()) {
+                        if (!skip) {
+                            const uint32_t b = v_lo + stage * (L::TILE >> 4), o = tmem + TM_O + (uint32_t)(D * x),
+                                           pm = tmem + TM_S + 128u * (uint32_t)buf;
 #pragma unroll
-                                for (int kk = 0; kk < PA_KEYS / 16; ++kk)
-                                    mma_f16_tmem_a(tmem + TM_O + 128u * x, tmem + TM_S + 128u * x + 8u * kk,
-                                                   b + (uint32_t)kk * (2048 >> 4), v_hi, IDESC_O, kk > 0 || begun[x] ? 1u : 0u);
-                            }
-                            if (t == n - 1)
-                                mma_commit(o_full + 8u * x);
+                            for (int kk = 0; kk < CH / 16; ++kk)
+                                mma_f16_tmem_a(o, pm + (uint32_t)(half * CH) + 8u * kk,
+                                               b + (uint32_t)(half * (CH / 16) + kk) * (2048 >> 4), v_hi, IDESC_O,
+                                               kk > 0 || half > 0 || !first ? 1u : 0u);
                         }
-                        __syncwarp();
-                        begun[x] = true;
+                        if (BUFS == 3 || half < HALVES - 1 || t == n - 1)              // (the others are waited for by none)
+                            mma_commit(pv_done + 8u * (uint32_t)(x * HALVES + half));
+                        if (BUFS == 3 && half == HALVES - 1 && (x == 1 || !pair))
+                            mma_commit(kv_free + 8u * stage);
                     }
-                    if (t + 1 < n) {
-                        if (x == 0)
-                            keys_wait(t + 1);
-                        score_step(x, t + 1);
+                    __syncwarp();
+                }
+                phases ^= 1u << buf;
+            };
+            auto release = [&](uint32_t k) {
+                if (elect_one())
+                    mma_commit(kv_free + 8u * (k & (NS - 1)));
+                __syncwarp();
+            };
+            if constexpr (BUFS == 2) {
+                // A has the first buffer, B the second
+                score(0, late, 0);
+                if (pair)
+                    score(1, 0, 1);
+#pragma unroll 1
+                for (int t = 0; t < n && !gone_all(); ++t) {
+                    if (t >= late) {
+                        add(0, t, 0);
+                        if (t + 1 < n)
+                            score(0, t + 1, 0);
+                    }
+                    if (pair) {
+                        add(1, t, 1);
+                        if (t + 1 < n)
+                            score(1, t + 1, 1);
+                    }
+                    release(at + 2u * (uint32_t)t + 1u);
+                }
+            } else {
+                // the buffers go round
+                int sb = 0, pb = 0;
+                auto next = [&](int &buf) { const int now = buf; buf = pa_next<BUFS>(buf, 1); return now; };
+                if (pair) {
+                    if (late == 0)
+                        score(0, 0, next(sb));
+                    score(1, 0, next(sb));
+                    if (n > 1)
+                        score(0, 1, next(sb));
+                    if (late == 1)
+                        score(1, 1, next(sb));
+#pragma unroll 1
+                    for (int t = 0; t < n && !gone_all(); ++t) {
+                        if (t >= late) {
+                            add(0, t, next(pb));
+                            if (t + 1 < n)
+                                score(1, t + 1, next(sb));
+                        }
+                        add(1, t, next(pb));
+                        if (t + 2 < n)
+                            score(0, t + 2, next(sb));
+                    }
+                } else {
+                    for (int t = 0; t < BUFS && t < n; ++t)
+                        score(0, t, next(sb));
+#pragma unroll 1
+                    for (int t = 0; t < n && !gone_all(); ++t) {
+                        add(0, t, next(pb));
+                        if (t + BUFS < n)
+                            score(0, t + BUFS, next(sb));
                     }
                 }
-                release(kv_free + 8u * vs);
-                if (t + 1 < n)
-                    release(kv_free + 8u * ((at + 2u * t + 2u) & (NS - 1)));
-                if (t + 2 == n)
-                    release(q_free);
             }
             at += 2u * (uint32_t)n;
         }
+    } else if (warp == PA_NEXT) {
+        // ------------------------------------------------- units to come
+        // The grid has a CTA for each unit that there may be, and an SM room for one: a CTA takes over the units of those
+        // that have not begun, so that units of different lengths are dealt out as SMs come free.
+        bool more = true, wanted = true;
+        int asked = 0;
+#pragma unroll 1
+        for (int round = 1; more && !gone_all(); ++round) {
+            const int slot = (round - 1) % PA_QUEUE;
+            if (wanted && round > PA_QUEUE)
+                kv_wait(unit_free + 8u * slot, (uint32_t)((round - 1) / PA_QUEUE - 1) & 1u, dead);
+            if (gone_all())
+                break;
+            if (elect_one())
+                pa_ask(smem_u32(&s_answer), answered);
+            __syncwarp();
+            ++asked;
+            kv_wait(answered, (uint32_t)(asked - 1) & 1u, dead);
+            int number = pa_answer(smem_u32(&s_answer));
+            fence_proxy_async();                           // (the next answer comes to the same place)
+            more = number >= 0;
+            if (wanted) {
+                if (!more || !walk.find(number, u)) {
+                    // CTAs behind the last unit have nothing to do: they are taken over too, and that is all
+                    wanted = false;
+                    number = -1;
+                }
+                if (lane == 0) {
+                    *(volatile int *)&s_unit[slot] = number;
+                    mbar_arrive(unit_full + 8u * slot);
+                }
+            }
+            __syncwarp();
+        }
+        if (gone_all() && asked > 0)
+            mbar_wait(answered, (uint32_t)(asked - 1) & 1u, p.err);
     }
     pdl_launch_dependents();
     tc_fence_before();
@@ -518,7 +745,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
 }
 
 template <int D>
-static q4_status pa_launch(const DeviceInfo &dev, const PromptArgs &a, int64_t most_units, cudaStream_t st, bool pdl)
+static q4_status pa_launch(const PromptArgs &a, int64_t most_units, cudaStream_t st, bool pdl)
 {
     CUtensorMap q, k, v;
     const uint64_t n = (uint64_t)a.tokens;
@@ -534,7 +761,7 @@ static q4_status pa_launch(const DeviceInfo &dev, const PromptArgs &a, int64_t m
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaFuncSetAttribute(prompt_attention_kernel)");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(most_units < dev.sms ? most_units : dev.sms));
+    cfg.gridDim = dim3((unsigned)most_units);
     cfg.blockDim = dim3(PA_WARPS * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -547,14 +774,14 @@ static q4_status pa_launch(const DeviceInfo &dev, const PromptArgs &a, int64_t m
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of prompt_attention_kernel");
 }
 
-q4_status launch_prompt_attention(const DeviceInfo &dev, PromptArgs a, int head_dim, cudaStream_t st, bool pdl)
+q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, bool pdl)
 {
     a.group = a.q_heads / a.kv_heads;
     a.tile_tokens = PA_ROWS / a.group;
     a.err = device_error_flags();
     // at most one part-filled pair of tiles a sequence
     const int64_t units = ((int64_t)a.tokens / (2 * a.tile_tokens) + a.batch) * a.kv_heads;
-    return head_dim == 64 ? pa_launch<64>(dev, a, units, st, pdl) : pa_launch<128>(dev, a, units, st, pdl);
+    return head_dim == 64 ? pa_launch<64>(a, units, st, pdl) : pa_launch<128>(a, units, st, pdl);
 }
 
 }  // namespace q4

@@ -19,7 +19,7 @@ struct SegmentUnit {
     int unit;                    // unit of it, 0 ..
 };
 
-// Finds units in rising order of their number.  A warp takes the sequences 32 at a time, and asks
+// Finds units by their number, at little cost when it rises from one to the next.  A warp takes the sequences 32 at a time, and asks
 // for the next 32 offsets before it adds up those at hand.  Offsets that fall: a sequence that would begin before
 // the end of one in front of it is left out, so that no row is written twice and the work stays
 // bounded whatever the offsets are.
@@ -45,6 +45,11 @@ struct SegmentWalk {
     __device__ bool find(int number, SegmentUnit &u)
     {
         const int lane = threadIdx.x & 31;
+        if (number < base) {                   // back to the front
+            chunk = -32;
+            base = total = floor = 0;
+            ask(0);
+        }
         while (number >= base + total) {
             base += total;
             chunk += 32;

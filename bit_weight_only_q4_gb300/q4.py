@@ -650,13 +650,24 @@ def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengt
 # ------------------------------------------------- around a layer's projections
 # The checks of these calls are kept by shape and stride as those of the cache's are; types,
 # devices and contiguity are looked at in every call.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _here(device, **tensors):
-    """All tensors (or None) lie on one device, the current one, where the call is launched."""
+    """Why a call's tensors (or None) are not all on one device, the current one, where it is launched."""
     for name, t in tensors.items():
         if t is not None and (not t.is_cuda or t.get_device() != device):
             raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
     if device != torch.cuda.current_device():
         raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _empty_rows(like, stream):
+    """A contiguous result of the shape and type of `like`."""
+    if stream is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    with _on(stream):
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _vector(t, name, n, dtype):
@@ -695,22 +706,25 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     D]; weights bf16 [D], or None for no norm), then the rotation of their first 2 * len(inv_freq)
     columns by positions * inv_freq (int32 [batch * tokens], fp32; both None: no rotation), in adjacent
     pairs or halves.  k may be None.  q_out=q and k_out=k work in place."""
-    key = ("norm_rope", q.shape, q.stride(), None if k is None else (k.shape, k.stride()),
-           None if positions is None else (positions.shape, inv_freq.shape), q_weight is None or q_weight.shape,
-           k_weight is None or k_weight.shape)
+    bf16, dev = torch.bfloat16, q.get_device()
+    key = (q.shape, q.stride(), k is None or k.shape, k is None or k.stride(), positions is None or positions.shape,
+           inv_freq is None or inv_freq.shape, q_weight is None or q_weight.shape, k_weight is None or k_weight.shape)
     plan = _kv_plans.get(key)
-    bf16 = torch.bfloat16
-    if (plan is None or q.dtype is not bf16 or (k is not None and k.dtype is not bf16) or
-            (positions is not None and not (positions.dtype is torch.int32 and positions.is_contiguous() and
-                                            inv_freq.dtype is torch.float32 and inv_freq.is_contiguous())) or
-            (q_weight is not None and not (q_weight.dtype is bf16 and q_weight.is_contiguous())) or
-            (k_weight is not None and not (k_weight.dtype is bf16 and k_weight.is_contiguous()))):
+    if not (plan is not None and q.dtype is bf16 and (k is None or k.dtype is bf16) and
+            (positions is None or (positions.dtype is torch.int32 and positions.is_contiguous() and
+                                   inv_freq.dtype is torch.float32 and inv_freq.is_contiguous())) and
+            (q_weight is None or (q_weight.dtype is bf16 and q_weight.is_contiguous())) and
+            (k_weight is None or (k_weight.dtype is bf16 and k_weight.is_contiguous()))):
         plan = _norm_rope_plan(key, q, k, q_weight, k_weight, positions, inv_freq)
     tokens, Hq, H, D, qs, ks, qos, kos, rotary = plan
-    _here(q.get_device(), q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq,
-          q_out=q_out, k_out=k_out)
+    if not (dev == _device() and (k is None or k.get_device() == dev) and
+            (positions is None or (positions.get_device() == dev and inv_freq.get_device() == dev)) and
+            (q_weight is None or q_weight.get_device() == dev) and (k_weight is None or k_weight.get_device() == dev) and
+            (q_out is None or q_out.get_device() == dev) and (k_out is None or k_out.get_device() == dev)):
+        _here(dev, q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq, q_out=q_out,
+              k_out=k_out)
     if q_out is None:
-        q_out = _kv_empty(q.shape, q, stream)
+        q_out = _empty_rows(q, stream)
     elif q_out.shape != q.shape:
         raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
     else:
@@ -718,16 +732,19 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = _kv_empty(k.shape, k, stream)
+        k_out = _empty_rows(k, stream)
     elif k_out.shape != k.shape:
         raise ValueError(f"k_out must be {tuple(k.shape)}, got {tuple(k_out.shape)}")
     else:
         kos = _kv_rows(k_out, "k_out", k.shape)
     if tokens * (Hq + H) == 0:
         return q_out, k_out
-    status = (_lib or load()).q4_norm_rope(_ptr(q), qs, _ptr(q_weight), _ptr(q_out), qos, Hq, _ptr(k), ks, _ptr(k_weight),
-                                           _ptr(k_out), kos, H, _ptr(positions), _ptr(inv_freq), rotary,
-                                           1 if interleaved else 0, eps, tokens, D, _kv_stream(stream, q))
+    status = (_lib or load()).q4_norm_rope(
+        q.data_ptr(), qs, None if q_weight is None else q_weight.data_ptr(), q_out.data_ptr(), qos, Hq,
+        None if k is None else k.data_ptr(), ks, None if k_weight is None else k_weight.data_ptr(),
+        None if k is None else k_out.data_ptr(), kos, H, None if positions is None else positions.data_ptr(),
+        None if inv_freq is None else inv_freq.data_ptr(), rotary, 1 if interleaved else 0, eps, tokens, D,
+        _kv_stream(stream, q))
     if status:
         _check(status)
     return q_out, k_out
@@ -750,16 +767,18 @@ def q4_prompt_attention(q, k, v, offsets, scale=None, out=None, stream=None):
     """out [tokens, q_heads, D] (bf16) = causal attention within each of the packed sequences: the rows
     offsets[b] .. offsets[b + 1] - 1 (int32 [batch + 1]) of q (bf16 [tokens, q_heads, D]) and of k and v
     (bf16 [tokens, kv_heads, D]).  scale: D ** -0.5 if None.  Rows of no sequence are not written."""
-    key = "prompt", q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), offsets.shape
+    key = q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), offsets.shape
     plan = _kv_plans.get(key)
-    bf16 = torch.bfloat16
+    bf16, dev = torch.bfloat16, q.get_device()
     if (plan is None or q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or
             offsets.dtype is not torch.int32 or not offsets.is_contiguous()):
         plan = _prompt_plan(key, q, k, v, offsets)
     N, B, Hq, H, D, qs, ks, vs, s = plan
-    _here(q.get_device(), q=q, k=k, v=v, offsets=offsets, out=out)
+    if not (k.get_device() == v.get_device() == offsets.get_device() == dev == _device() and
+            (out is None or out.get_device() == dev)):
+        _here(dev, q=q, k=k, v=v, offsets=offsets, out=out)
     if out is None:
-        out = _kv_empty(q.shape, q, stream)
+        out = _empty_rows(q, stream)
     elif _cuda(out, "out", torch.bfloat16).shape != q.shape:
         raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
     if N == 0 or B == 0:
@@ -805,18 +824,20 @@ def q4_lora(x, a, b, scales, offsets, ids, base, out=None, stream=None):
     [tokens, K]; a bf16 [adapters, rank, K]; b bf16 [adapters, N, rank]; scales fp32 [adapters]; offsets int32
     [batch + 1]; ids int32 [batch]; base bf16 [tokens, N].  out=base works in place.  Rows of no request are not
     written."""
-    key = "lora", x.shape, x.stride(), a.shape, b.shape, scales.shape, offsets.shape, ids.shape, base.shape, base.stride()
+    key = x.shape, x.stride(), a.shape, b.shape, scales.shape, offsets.shape, ids.shape, base.shape, base.stride()
     plan = _kv_plans.get(key)
-    bf16, i32 = torch.bfloat16, torch.int32
+    bf16, i32, dev = torch.bfloat16, torch.int32, x.get_device()
     if (plan is None or x.dtype is not bf16 or a.dtype is not bf16 or b.dtype is not bf16 or base.dtype is not bf16 or
             offsets.dtype is not i32 or ids.dtype is not i32 or scales.dtype is not torch.float32 or not
             (a.is_contiguous() and b.is_contiguous() and offsets.is_contiguous() and ids.is_contiguous() and
              scales.is_contiguous())):
         plan = _lora_plan(key, x, a, b, scales, offsets, ids, base)
     M, B, n, r, N, K, xs, bs = plan
-    _here(x.get_device(), x=x, a=a, b=b, scales=scales, offsets=offsets, ids=ids, base=base, out=out)
+    if not (a.get_device() == b.get_device() == scales.get_device() == offsets.get_device() == ids.get_device() ==
+            base.get_device() == dev == _device() and (out is None or out.get_device() == dev)):
+        _here(dev, x=x, a=a, b=b, scales=scales, offsets=offsets, ids=ids, base=base, out=out)
     if out is None:
-        out, os_ = _kv_empty(base.shape, base, stream), N
+        out, os_ = _empty_rows(base, stream), N
     elif out.shape != base.shape:
         raise ValueError(f"out must be {tuple(base.shape)}, got {tuple(out.shape)}")
     else:

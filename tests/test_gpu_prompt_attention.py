@@ -95,6 +95,15 @@ def test_many_sequences():
     check(q4.q4_prompt_attention(q, k, v, offsets), q, k, v, spans_of(offsets))
 
 
+@pytest.mark.parametrize("Hq,H,D", [(16, 4, 128), (12, 12, 64), (6, 6, 128), (30, 10, 64)])
+def test_units_of_every_kind_in_turn(Hq, H, D):
+    """Several units for each CTA: pairs of tiles, tiles without a partner, one and many tiles of keys."""
+    gen = torch.Generator().manual_seed(5)
+    lens = [int(2 ** (11 * x)) for x in torch.rand(60, generator=gen).tolist()]
+    q, k, v, offsets = made(lens, Hq, H, D)
+    check(q4.q4_prompt_attention(q, k, v, offsets), q, k, v, spans_of(offsets))
+
+
 def test_rows_of_no_sequence_are_left_alone():
     q, k, v, offsets = made([70, 3, 200], 4, 2, 128, gap=37)
     out = torch.full_like(q, 7.0, memory_format=torch.contiguous_format)
