@@ -14,7 +14,7 @@
 // reference raised and what was summed scaled down.  So a tile that is seen whole costs one pass over its scores and no maximum.
 //
 // One CTA per SM, 12 warps: four with the softmax of A (one thread a row), four with that of
-// B, one that copies (TMA), one that issues the MMAs.  A step is one tile of rows on one tile of keys; A and
+// B, one that copies (TMA), one that issues the MMAs, one that fetches units.  A step is one tile of rows on one tile of keys; A and
 // B take turns.  Step n has its S in buffer n mod BUFS of tensor memory, and P takes the place of
 // its S.  MMAs run in the order
 //     .. P(n) V  S(n + BUFS)  P(n + 1) V  S(n + 1 + BUFS) ..
@@ -25,8 +25,8 @@
 // follows that of the rows' last one without a wait.
 //
 // A masked probability is 0, and 0 times a v that is not finite would be NaN: tiles cut by the
-// mask are looked through for such values, and a tile that has one is multiplied by the softmax
-// threads themselves, over the tokens that a row sees.
+// mask are looked through for such values (by a warp that does nothing else), and a tile that has one
+// is multiplied by the softmax threads themselves, over the tokens that a row sees.
 #include "layer_ops.h"
 #include "segments.cuh"
 #include "tc_device.cuh"
@@ -35,7 +35,7 @@
 namespace q4 {
 
 constexpr int PA_ROWS = 128, PA_KEYS = 128;
-constexpr int PA_COPY = 8, PA_MMA = 9, PA_NEXT = 10, PA_WARPS = 12;
+constexpr int PA_COPY = 8, PA_MMA = 9, PA_NEXT = 10, PA_WARPS = 12;          // (warp 11 looks through V)
 constexpr int PA_QUEUE = 2;                // units that a CTA has been given and not begun
 constexpr float PA_SUM_TOP = 0x1p20f;
 
@@ -44,17 +44,17 @@ struct PaSmem {
     static constexpr int BUFS = D == 128 ? 2 : 3, HALVES = D == 128 ? 2 : 1;
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t TILE = PA_KEYS * D * 2;
-    static constexpr uint32_t RING = 2 * TILE;                       // [Q of A, Q of B][ring][staging]
-    static constexpr uint32_t STAGE = RING + STAGES * TILE;
-    static constexpr uint32_t TOTAL = STAGE + 8 * 2048;
+    static constexpr uint32_t RING = 2 * TILE;                       // [Q of A, Q of B][ring]
+    static constexpr uint32_t TOTAL = RING + STAGES * TILE;
 };
 
 // What a unit is.
-struct PaUnit {
+struct __align__(16) PaUnit {
     int start, len;              // the sequence's first row and tokens
     int first;                   // first token of tile A
     int head;                    // key head
-    int na, nb;                  // key tiles of A and of B (0: B has no token)
+    int na, nb;                  // key tiles of A and of B (0: B has no token; na = 0: no unit)
+    int pad[2];
 };
 
 // A warp's units.  Units are numbered by sequence, then from the last pair of tiles to the first, then
@@ -151,11 +151,11 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     constexpr uint32_t IDESC_S = (1u << 4) | BF16 | ((uint32_t)(PA_KEYS >> 3) << 17) | (8u << 24);
     constexpr uint32_t IDESC_O = (1u << 4) | BF16 | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 4 + 2 * HALVES + BUFS * (2 + HALVES) + 2 * PA_QUEUE + 1];
+    __shared__ uint64_t s_bar[2 * NS + 4 + 2 * HALVES + BUFS * (2 + HALVES) + 2 * PA_QUEUE + 1 + NS];
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) uint4 s_answer;
-    __shared__ int s_unit[PA_QUEUE];
-    __shared__ int s_dead, s_skip[BUFS];
+    __shared__ PaUnit s_unit[PA_QUEUE];
+    __shared__ int s_dead, s_bad[NS];
     const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                    s_full = pv_done + 16u * HALVES,            // by tile and buffer: each phase has one waiter, who misses none
                    p_full = s_full + 16u * BUFS,               // by buffer and half
                    unit_full = p_full + 8u * BUFS * HALVES, unit_free = unit_full + 8u * PA_QUEUE,
-                   answered = unit_free + 8u * PA_QUEUE;
+                   answered = unit_free + 8u * PA_QUEUE, v_raw = answered + 8;        // by stage: V that is to be looked through
     pdl_wait();
     PaWalk walk(p);
     PaUnit u;
@@ -175,13 +175,14 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             for (int i = 0; i < NS; ++i) {
                 mbar_init(kv_full + 8u * i, 1);
                 mbar_init(kv_free + 8u * i, 1);
+                mbar_init(v_raw + 8u * i, 1);
             }
             mbar_init(q_free, 1);
             mbar_init(drained, 1);
             mbar_init(answered, 1);
             for (int i = 0; i < PA_QUEUE; ++i) {
                 mbar_init(unit_full + 8u * i, 1);
-                mbar_init(unit_free + 8u * i, 10);
+                mbar_init(unit_free + 8u * i, 11);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(q_full + 8u * i, 1);
@@ -212,11 +213,12 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             return true;
         const int slot = (round - 1) % PA_QUEUE;
         kv_wait(unit_full + 8u * slot, (uint32_t)((round - 1) / PA_QUEUE) & 1u, dead);
-        const int number = *(volatile int *)&s_unit[slot];
+        const uint4 e = lds128(smem_u32(&s_unit[slot])), f = lds128(smem_u32(&s_unit[slot]) + 16u);
+        u.start = (int)e.x, u.len = (int)e.y, u.first = (int)e.z, u.head = (int)e.w, u.na = (int)f.x, u.nb = (int)f.y;
         __syncwarp();
         if (lane == 0)
             mbar_arrive(unit_free + 8u * slot);
-        return number >= 0 && walk.find(number, u);
+        return u.na > 0;
     };
 
     if (warp < 8) {
@@ -272,27 +274,12 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 const bool masked = j >= whole;
                 const int seen = token >= 0 ? token - j * PA_KEYS : PA_KEYS - 1;      // the row's last visible column
                 int hi = PA_KEYS - 1;
-                bool skip = false;
-                const uint32_t v_at = ring + 2u * (uint32_t)(n - 1 - j) + 1u;
-                const uint32_t v_tile = sm + L::RING + (v_at & (NS - 1)) * L::TILE;
+                const uint32_t v_at = ring + 2u * (uint32_t)(n - 1 - j) + 1u, v_stage = v_at & (NS - 1);
+                const uint32_t v_tile = sm + L::RING + v_stage * L::TILE;
                 kv_wait(s_full + 8u * (uint32_t)(x * BUFS + at_buf), parity, dead);
                 tc_fence_after();
-                if (masked) {
+                if (masked)
                     hi = __reduce_max_sync(0xffffffffu, seen);
-                    // one row of v for each thread: is there anything that is not finite?  (Behind the wait for S: what the
-                    // ring's stage held before has been loaded by then, so that the phase is this one or the next.)
-                    kv_wait(kv_full + 8u * (v_at & (NS - 1)), (v_at / NS) & 1u, dead);
-                    uint32_t bad = 0u;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 e = lds128(v_tile + (uint32_t)(c >> 3) * 16384u + (uint32_t)row * 128u + 16u * ((uint32_t)(c ^ row) & 7u));
-                        bad |= ((e.x & 0x7f807f80u) + 0x00800080u) | ((e.y & 0x7f807f80u) + 0x00800080u) |
-                               ((e.z & 0x7f807f80u) + 0x00800080u) | ((e.w & 0x7f807f80u) + 0x00800080u);
-                    }
-                    skip = bar_or(1 + x, 128, (bad & 0x80008000u) != 0u);
-                }
-                if (row == 0)
-                    s_skip[at_buf] = skip;
 #pragma unroll 1
                 for (int half = 0; half < HALVES; ++half) {
                     const int c0 = half * CH;
@@ -416,6 +403,13 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                     for (int c = 0; c < CH / 2; c += 32)
                         tmem_st32(t_p + c, reinterpret_cast<uint32_t(&)[32]>(ph[c]));
                     tmem_wait_st();
+                    bool skip = false;
+                    if (masked) {
+                        // (behind the wait for S: what the ring's stage held before has been loaded by then, so that the
+                        // phase is this one or the next)
+                        kv_wait(kv_full + 8u * v_stage, (v_at / NS) & 1u, dead);
+                        skip = __shfl_sync(0xffffffffu, *(volatile int *)&s_bad[v_stage], 0) != 0;
+                    }
                     if (skip) {
                         // O += P V over the tokens that the row sees, 16 columns at a time
                         if (begun)
@@ -474,48 +468,43 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             float l0, l1;
             unpack2(add2(la, lb), l0, l1);
             const float inv = l0 + l1 == 0.f ? 0.f : 1.f / (l0 + l1);
-            // 32 columns at a time through the warp's 2 KB of shared memory: written by row, read four
-            // lanes to a row, so that a store fills whole sectors.  Piece c of row r lies at c ^ (r / 2 & 3).
-            const uint32_t st = sm + L::STAGE + (uint32_t)warp * 2048u;
-            const uint32_t st_row = st + (uint32_t)lane * 64u, key = (uint32_t)(lane >> 1) & 3u;
-            const int at_row = token < 0 ? -1 : (u.start + token) * p.q_heads + u.head * p.group + row_head;
-            int to[4];
+            const bool gone = gone_all(), store = token >= 0 && !gone;         // (the vote is the whole warp's)
+            uint16_t *to = p.out + ((int64_t)(u.start + token) * p.q_heads + u.head * p.group + row_head) * D;
+            uint32_t o[2][32];
+            tmem_ld32_async(t_o, o[0]);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                to[i] = __shfl_sync(0xffffffffu, at_row, (lane >> 2) + 8 * i);
-            const bool store = !gone_all();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32_async(t_o + c, o);
-                tmem_wait_ld();
+            for (int c = 0; c < D / 32; ++c) {
+                if (c + 1 < D / 32)
+                    tmem_ld32_async(t_o + 32u * (c + 1), o[(c + 1) & 1]);
+                uint32_t e[16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t e[4];
+                for (int i = 0; i < 16; ++i)
+                    e[i] = bf16_pair(__uint_as_float(o[c & 1][2 * i]) * inv, __uint_as_float(o[c & 1][2 * i + 1]) * inv);
+                if (store) {
+                    // a row's 32 columns are two whole sectors, each one store where `out` begins at one
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        e[y] = bf16_pair(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
-                    sts128(st_row + (((uint32_t)i ^ key) << 4), e[0], e[1], e[2], e[3]);
+                    for (int i = 0; i < 16; i += 8) {
+                        if (p.sectors) {
+                            st_global_32(to + 32 * c + 2 * i, e + i);
+                        } else {
+                            *reinterpret_cast<uint4 *>(to + 32 * c + 2 * i) = make_uint4(e[i], e[i + 1], e[i + 2], e[i + 3]);
+                            *reinterpret_cast<uint4 *>(to + 32 * c + 2 * i + 8) = make_uint4(e[i + 4], e[i + 5], e[i + 6], e[i + 7]);
+                        }
+                    }
                 }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t r = (uint32_t)(lane >> 2) + 8u * i, piece = (uint32_t)lane & 3u;
-                    const uint4 e = lds128(st + r * 64u + ((piece ^ ((r >> 1) & 3u)) << 4));
-                    if (to[i] >= 0 && store)
-                        *reinterpret_cast<uint4 *>(p.out + (int64_t)to[i] * D + c + 8 * piece) = e;
-                }
-                __syncwarp();
+                if (c + 1 < D / 32)
+                    tmem_wait_ld();
             }
             tc_fence_before();                             // (the next P of this tile lets its O be written again)
         }
     } else if (warp == PA_COPY) {
         // ------------------------------------------------------- copies
         uint32_t at = 0u;
-        uint32_t loads[2] = {0u, 0u};
+        uint32_t loads[2] = {0u, 0u}, raw = 0u, raw_uses = 0u;           // stages that v_raw counts now; its parities
 #pragma unroll 1
         for (int round = 0; unit(round) && !gone_all(); ++round) {
-            const int n = u.nb > 0 ? u.nb : u.na;
+            const int n = u.nb > 0 ? u.nb : u.na, cut = n - (u.first + 1) / PA_KEYS;       // V is looked through
 #pragma unroll 1
             for (int i = 0; i < 2 * n && !gone_all(); ++i, ++at) {
                 const uint32_t s = at & (NS - 1);
@@ -523,9 +512,12 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                     kv_wait(kv_free + 8u * s, (at / NS - 1u) & 1u, dead);
                 if (gone_all())
                     break;
+                const bool look = (i & 1) && i / 2 < cut;
+                raw = look ? raw | 1u << s : raw & ~(1u << s);
+                raw_uses ^= (uint32_t)look << s;
                 if (elect_one()) {
                     const CUtensorMap *map = (i & 1) ? &v_map : &k_map;
-                    const uint32_t dst = sm + L::RING + s * L::TILE, bar = kv_full + 8u * s;
+                    const uint32_t dst = sm + L::RING + s * L::TILE, bar = (look ? v_raw : kv_full) + 8u * s;
                     mbar_arrive_expect_tx(bar, L::TILE);
 #pragma unroll
                     for (int c = 0; c < D; c += 64)
@@ -555,8 +547,13 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         }
         if (gone_all()) {
             // copies in flight land before the CTA ends
-            for (uint32_t i = at > NS ? at - NS : 0u; i < at; ++i)
-                mbar_wait(kv_full + 8u * (i & (NS - 1)), (i / NS) & 1u, p.err);
+            for (uint32_t i = at > NS ? at - NS : 0u; i < at; ++i) {
+                const uint32_t s = i & (NS - 1);
+                if ((raw >> s) & 1u)
+                    mbar_wait(v_raw + 8u * s, ~(raw_uses >> s) & 1u, p.err);
+                else
+                    mbar_wait(kv_full + 8u * s, (i / NS) & 1u, p.err);
+            }
             for (int x = 0; x < 2; ++x)
                 if (loads[x] > 0)
                     mbar_wait(q_full + 8u * x, (loads[x] - 1u) & 1u, p.err);
@@ -615,7 +612,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 for (int half = 0; half < HALVES; ++half) {
                     kv_wait(p_full + 8u * (uint32_t)(buf * HALVES + half), (phases >> buf) & 1u, dead);
                     tc_fence_after();
-                    const bool skip = masked && __shfl_sync(0xffffffffu, *(volatile int *)&s_skip[buf], 0) != 0;
+                    const bool skip = masked && __shfl_sync(0xffffffffu, *(volatile int *)&s_bad[stage], 0) != 0;
                     if (elect_one()) {
                         if (!skip) {
                             const uint32_t b = v_lo + stage * (L::TILE >> 4), o = tmem + TM_O + (uint32_t)(D * x),
@@ -713,17 +710,19 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             __syncwarp();
             ++asked;
             kv_wait(answered, (uint32_t)(asked - 1) & 1u, dead);
-            int number = pa_answer(smem_u32(&s_answer));
+            const int number = pa_answer(smem_u32(&s_answer));
             fence_proxy_async();                           // (the next answer comes to the same place)
             more = number >= 0;
             if (wanted) {
                 if (!more || !walk.find(number, u)) {
                     // CTAs behind the last unit have nothing to do: they are taken over too, and that is all
                     wanted = false;
-                    number = -1;
+                    u.na = 0;
                 }
                 if (lane == 0) {
-                    *(volatile int *)&s_unit[slot] = number;
+                    const uint32_t to = smem_u32(&s_unit[slot]);
+                    sts128(to, (uint32_t)u.start, (uint32_t)u.len, (uint32_t)u.first, (uint32_t)u.head);
+                    sts128(to + 16u, (uint32_t)u.na, (uint32_t)u.nb, 0u, 0u);
                     mbar_arrive(unit_full + 8u * slot);
                 }
             }
@@ -731,6 +730,33 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         }
         if (gone_all() && asked > 0)
             mbar_wait(answered, (uint32_t)(asked - 1) & 1u, p.err);
+    } else {
+        // ------------ values that are not finite in tiles of V that the mask cuts
+        uint32_t at = 0u, uses = 0u;                       // copies before this unit, parities of v_raw
+#pragma unroll 1
+        for (int round = 0; unit(round) && !gone_all(); ++round) {
+            const int n = u.nb > 0 ? u.nb : u.na, cut = n - (u.first + 1) / PA_KEYS;
+#pragma unroll 1
+            for (int t = 0; t < cut && !gone_all(); ++t) {
+                const uint32_t stage = (at + 2u * (uint32_t)t + 1u) & (NS - 1), v = sm + L::RING + stage * L::TILE;
+                kv_wait(v_raw + 8u * stage, (uses >> stage) & 1u, dead);
+                uses ^= 1u << stage;
+                uint32_t bad = 0u;
+#pragma unroll 8
+                for (uint32_t c = (uint32_t)lane * 16u; c < L::TILE; c += 512u) {
+                    const uint4 e = lds128(v + c);
+                    bad |= ((e.x & 0x7f807f80u) + 0x00800080u) | ((e.y & 0x7f807f80u) + 0x00800080u) |
+                           ((e.z & 0x7f807f80u) + 0x00800080u) | ((e.w & 0x7f807f80u) + 0x00800080u);
+                }
+                const bool any = __any_sync(0xffffffffu, (bad & 0x80008000u) != 0u);
+                if (lane == 0) {
+                    *(volatile int *)&s_bad[stage] = any;
+                    mbar_arrive(kv_full + 8u * stage);
+                }
+                __syncwarp();
+            }
+            at += 2u * (uint32_t)n;
+        }
     }
     pdl_launch_dependents();
     tc_fence_before();
@@ -779,6 +805,7 @@ q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, b
     a.group = a.q_heads / a.kv_heads;
     a.tile_tokens = PA_ROWS / a.group;
     a.err = device_error_flags();
+    a.sectors = (uintptr_t)a.out % 32 == 0;
     // at most one part-filled pair of tiles a sequence
     const int64_t units = ((int64_t)a.tokens / (2 * a.tile_tokens) + a.batch) * a.kv_heads;
     return head_dim == 64 ? pa_launch<64>(a, units, st, pdl) : pa_launch<128>(a, units, st, pdl);
