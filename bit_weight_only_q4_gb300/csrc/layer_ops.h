@@ -29,7 +29,7 @@ struct PromptArgs {
     const int32_t *offsets;                                    // [batch + 1]
     int batch, tokens, q_heads, kv_heads;
     float scale_log2;                                          // scale * log2(e)
-    int group, tile_tokens, sectors;                           // (by the launch) query heads per key head, tokens of a tile; out is 32-byte aligned
+    int group, tile_tokens, box_tokens;                        // (by the launch) query heads per key head, tokens of a tile, of 32 rows
     unsigned *err;
 };
 q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, bool pdl);

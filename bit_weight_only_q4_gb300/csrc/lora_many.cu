@@ -31,13 +31,6 @@ struct LmSmem {
     static constexpr uint32_t BARS = T + (WIDE ? 32768 : 16384), TOTAL = BARS + 512;
 };
 
-__device__ __forceinline__ void lm_store_2d(const CUtensorMap *map, int c0, int c1, uint32_t src)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(src)
-                 : "memory");
-}
-
 template <bool WIDE>
 __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 32, 2)
     lora_many_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap a_map,
@@ -198,7 +191,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
                 __syncwarp();
                 if (lane == 0) {
                     if (ok) {
-                        lm_store_2d(&out_map, (n0 + q) * LM_COLS, tile.row + quad * 32, sm + s * L::SLOT + (uint32_t)quad * 4096u);
+                        tma_store_2d(&out_map, (n0 + q) * LM_COLS, tile.row + quad * 32, sm + s * L::SLOT + (uint32_t)quad * 4096u);
                         asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
                     mbar_arrive(base_free + 8u * s);

@@ -44,8 +44,9 @@ struct PaSmem {
     static constexpr int BUFS = D == 128 ? 2 : 3, HALVES = D == 128 ? 2 : 1;
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t TILE = PA_KEYS * D * 2;
-    static constexpr uint32_t RING = 2 * TILE;                       // [Q of A, Q of B][ring]
-    static constexpr uint32_t TOTAL = RING + STAGES * TILE;
+    static constexpr uint32_t RING = 2 * TILE;                       // [Q of A, Q of B][ring][results, 4 KB a warp]
+    static constexpr uint32_t STAGE = RING + STAGES * TILE;
+    static constexpr uint32_t TOTAL = STAGE + 8 * 4096;
 };
 
 // What a unit is.
@@ -140,7 +141,8 @@ __device__ __forceinline__ int pa_next(int buf, int steps)
 template <int D>
 __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                            const __grid_constant__ CUtensorMap v_map, const PromptArgs p)
+                            const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap out_map,
+                            const PromptArgs p)
 {
     using L = PaSmem<D>;
     constexpr int NS = L::STAGES;
@@ -468,36 +470,56 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             float l0, l1;
             unpack2(add2(la, lb), l0, l1);
             const float inv = l0 + l1 == 0.f ? 0.f : 1.f / (l0 + l1);
-            const bool gone = gone_all(), store = token >= 0 && !gone;         // (the vote is the whole warp's)
-            uint16_t *to = p.out + ((int64_t)(u.start + token) * p.q_heads + u.head * p.group + row_head) * D;
-            uint32_t o[2][32];
-            tmem_ld32_async(t_o, o[0]);
-            tmem_wait_ld();
+            const bool gone = gone_all(), full = p.box_tokens > 0 && __all_sync(0xffffffffu, token >= 0);
+            if (full) {
+                // All of the warp's rows are results: by way of its 4 KB of shared memory, 64 columns at a time, and from
+                // there by TMA (whose rows of 128 bytes have piece c at c ^ (row & 7)).
+                const uint32_t st = sm + L::STAGE + (uint32_t)warp * 4096u, st_row = st + (uint32_t)lane * 128u;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                if (c + 1 < D / 32)
-                    tmem_ld32_async(t_o + 32u * (c + 1), o[(c + 1) & 1]);
-                uint32_t e[16];
+                for (int c = 0; c < D; c += 64) {
+                    uint32_t o[2][32];
+                    tmem_ld32_async(t_o + c, o[0]);
+                    tmem_ld32_async(t_o + c + 32, o[1]);
+                    tmem_wait_ld();
+                    uint32_t e[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    e[i] = bf16_pair(__uint_as_float(o[c & 1][2 * i]) * inv, __uint_as_float(o[c & 1][2 * i + 1]) * inv);
-                if (store) {
-                    // a row's 32 columns are two whole sectors, each one store where `out` begins at one
+                    for (int i = 0; i < 32; ++i)
+                        e[i] = bf16_pair(__uint_as_float(o[i / 16][2 * i % 32]) * inv, __uint_as_float(o[i / 16][2 * i % 32 + 1]) * inv);
+                    if (lane == 0)                         // (the last store has read them)
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 8) {
-                        if (p.sectors) {
-                            st_global_32(to + 32 * c + 2 * i, e + i);
-                        } else {
-                            *reinterpret_cast<uint4 *>(to + 32 * c + 2 * i) = make_uint4(e[i], e[i + 1], e[i + 2], e[i + 3]);
-                            *reinterpret_cast<uint4 *>(to + 32 * c + 2 * i + 8) = make_uint4(e[i + 4], e[i + 5], e[i + 6], e[i + 7]);
-                        }
+                    for (int i = 0; i < 8; ++i)
+                        sts128(st_row + (((uint32_t)i ^ ((uint32_t)lane & 7u)) << 4), e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0 && !gone) {
+                        tma_store_3d(&out_map, c, u.head * p.group, u.start + token, st);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 }
-                if (c + 1 < D / 32)
+            } else {
+                uint16_t *to = p.out + ((int64_t)(u.start + token) * p.q_heads + u.head * p.group + row_head) * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32_async(t_o + c, o);
                     tmem_wait_ld();
+                    uint32_t e[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        e[i] = bf16_pair(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                    if (token >= 0 && !gone) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<uint4 *>(to + c + 2 * i) = make_uint4(e[i], e[i + 1], e[i + 2], e[i + 3]);
+                    }
+                }
             }
             tc_fence_before();                             // (the next P of this tile lets its O be written again)
         }
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (warp == PA_COPY) {
         // ------------------------------------------------------- copies
         uint32_t at = 0u;
@@ -773,13 +795,16 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
 template <int D>
 static q4_status pa_launch(const PromptArgs &a, int64_t most_units, cudaStream_t st, bool pdl)
 {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
     const uint64_t n = (uint64_t)a.tokens;
     q4_status s = tma_heads(q, a.q, D, a.q_heads, n, a.q_stride, a.group, a.tile_tokens);
     if (s == Q4_OK)
         s = tma_heads(k, a.k, D, a.kv_heads, n, a.k_stride, 1, PA_KEYS);
     if (s == Q4_OK)
         s = tma_heads(v, a.v, D, a.kv_heads, n, a.v_stride, 1, PA_KEYS);
+    // (without boxes of whole tokens in 32 rows there are no stores through this map)
+    if (s == Q4_OK)
+        s = tma_heads(out, a.out, D, a.q_heads, n, (int64_t)a.q_heads * D, a.box_tokens ? a.group : 1, a.box_tokens ? a.box_tokens : 1);
     if (s != Q4_OK)
         return s;
     const size_t smem = PaSmem<D>::TOTAL + 1024;
@@ -796,7 +821,7 @@ static q4_status pa_launch(const PromptArgs &a, int64_t most_units, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = pdl ? attr : nullptr;
     cfg.numAttrs = pdl ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D>, q, k, v, a);
+    e = cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D>, q, k, v, out, a);
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of prompt_attention_kernel");
 }
 
@@ -805,7 +830,7 @@ q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, b
     a.group = a.q_heads / a.kv_heads;
     a.tile_tokens = PA_ROWS / a.group;
     a.err = device_error_flags();
-    a.sectors = (uintptr_t)a.out % 32 == 0;
+    a.box_tokens = 32 % a.group == 0 ? 32 / a.group : 0;
     // at most one part-filled pair of tiles a sequence
     const int64_t units = ((int64_t)a.tokens / (2 * a.tile_tokens) + a.batch) * a.kv_heads;
     return head_dim == 64 ? pa_launch<64>(a, units, st, pdl) : pa_launch<128>(a, units, st, pdl);

@@ -279,14 +279,6 @@ __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &v)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(v) : "r"(taddr));
 }
 
-// 32 bytes, a whole sector, in one store (32-byte aligned).
-__device__ __forceinline__ void st_global_32(void *p, const uint32_t *v)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 // (lo, hi) rounded to bf16.
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
