@@ -145,7 +145,7 @@ q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b,
     p.err = device_error_flags();
     // Requests are judged by their mean length, for the lengths are on the device.
     return tokens <= 8 * (int64_t)batch ? launch_lora_few(p, static_cast<cudaStream_t>(stream), pdl_on())
-                                        : launch_lora_many(p, static_cast<cudaStream_t>(stream), pdl_on());
+                                        : launch_lora_many(dev, p, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
 }  // extern "C"

@@ -45,6 +45,6 @@ struct LoraArgs {
     unsigned *err;
 };
 q4_status launch_lora_few(const LoraArgs &a, cudaStream_t st, bool pdl);
-q4_status launch_lora_many(const LoraArgs &a, cudaStream_t st, bool pdl);
+q4_status launch_lora_many(const DeviceInfo &dev, const LoraArgs &a, cudaStream_t st, bool pdl);
 
 }  // namespace q4

@@ -2,9 +2,9 @@
 //
 // For token m of a request with adapter a
 //     t = x_m A_a^T  (rank values),   out_m = base_m + scale_a (t B_a^T).
-// A cluster of eight CTAs takes a tile of a request's tokens through both products in one launch: each
-// CTA sums t over an eighth of K, the eight add their sums up through each other's shared memory, and
-// each then has an eighth of the output columns.  Sums are fp32; t meets B as bf16, as wide as x and B are.
+// A cluster of up to eight CTAs takes a tile of a request's tokens through both products in one launch:
+// each CTA sums t over its share of K, they add their sums up through each other's shared memory, and
+// each then has its share of the output columns.  Sums are fp32; t meets B as bf16, as wide as x and B are.
 #pragma once
 
 #include "layer_ops.h"
@@ -13,12 +13,19 @@
 
 namespace q4 {
 
-constexpr int LR_CLUSTER = 8;
+constexpr int LR_CLUSTER = 8;              // at most
 
 __device__ __forceinline__ uint32_t lr_rank_in_cluster()
 {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lr_cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
 
@@ -40,8 +47,8 @@ __device__ __forceinline__ float4 lr_load(uint32_t cluster_address)
     return v;
 }
 
-// Part `rank` of n things shared out evenly.
-__device__ __forceinline__ int lr_share(int n, uint32_t rank) { return (int)((int64_t)n * rank / LR_CLUSTER); }
+// First of n things that CTA `rank` of `size` has, when they are shared out evenly.
+__device__ __forceinline__ int lr_share(int n, uint32_t rank, uint32_t size) { return (int)((int64_t)n * rank / size); }
 
 // The tile of tokens that a cluster works on; false: none.
 struct LoraTile {
@@ -50,6 +57,8 @@ struct LoraTile {
 
 __device__ __forceinline__ bool lr_tile(const LoraArgs &p, int number, int span, LoraTile &t)
 {
+    // (the first ids are asked for with the first offsets)
+    const int lane = (int)(threadIdx.x & 31), id = lane < p.batch ? __ldg(p.ids + lane) : -1;
     SegmentWalk walk(Segments{p.offsets, p.batch, p.tokens, span, 1, p.err});
     SegmentUnit u;
     if (!walk.find(number, u))
@@ -57,7 +66,9 @@ __device__ __forceinline__ bool lr_tile(const LoraArgs &p, int number, int span,
     const int first = u.unit * span;
     t.row = u.start + first;
     t.rows = u.len - first < span ? u.len - first : span;
-    t.adapter = __ldg(p.ids + u.sequence);
+    t.adapter = __shfl_sync(0xffffffffu, id, u.sequence & 31);
+    if (u.sequence >= 32)
+        t.adapter = __ldg(p.ids + u.sequence);
     if (t.adapter >= p.adapters) {
         if (p.err && (threadIdx.x & 31) == 0)
             atomicOr(p.err, kErrIndex);
@@ -67,11 +78,11 @@ __device__ __forceinline__ bool lr_tile(const LoraArgs &p, int number, int span,
 }
 
 // A tile without an adapter: this CTA's columns of base, where out is not base itself.
-__device__ __forceinline__ void lr_copy(const LoraArgs &p, const LoraTile &t, uint32_t rank)
+__device__ __forceinline__ void lr_copy(const LoraArgs &p, const LoraTile &t, uint32_t rank, uint32_t size)
 {
     if (p.out == p.base)
         return;
-    const int c0 = lr_share(p.N / 8, rank), n = lr_share(p.N / 8, rank + 1) - c0;
+    const int c0 = lr_share(p.N / 8, rank, size), n = lr_share(p.N / 8, rank + 1, size) - c0;
     for (int i = (int)threadIdx.x; i < t.rows * n; i += (int)blockDim.x) {
         const int r = i / n, c = 8 * (c0 + i - r * n);
         *reinterpret_cast<uint4 *>(p.out + (int64_t)(t.row + r) * p.out_stride + c) =

@@ -38,7 +38,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
     if (!lr_tile(p, (int)(blockIdx.x / LR_CLUSTER), LF_TOKENS, tile))
         return;                                             // (the whole cluster)
     if (tile.adapter < 0) {
-        lr_copy(p, tile, rank);
+        lr_copy(p, tile, rank, LR_CLUSTER);
         return;
     }
     const float scale = __ldg(p.scales + tile.adapter);
@@ -46,7 +46,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
     // ---- t over this CTA's columns of K
     {
         // 32 columns at a time for each warp: all rank values against one load of x
-        const int k0 = lr_share((p.K + 31) / 32, rank), k1 = lr_share((p.K + 31) / 32, rank + 1);
+        const int k0 = lr_share((p.K + 31) / 32, rank, LR_CLUSTER), k1 = lr_share((p.K + 31) / 32, rank + 1, LR_CLUSTER);
         const uint16_t *a = p.a + ((int64_t)tile.adapter * r + g) * p.K + 8 * t;
         const uint16_t *x = p.x + (int64_t)(tile.row + g) * p.x_stride + 8 * t;
         const bool token = g < tile.rows;
@@ -79,7 +79,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
         }
     }
     // ---- the first of the B rows and base values that this warp needs are on their way during the exchange
-    const int n0 = lr_share((p.N + 15) / 16, rank), n1 = lr_share((p.N + 15) / 16, rank + 1);
+    const int n0 = lr_share((p.N + 15) / 16, rank, LR_CLUSTER), n1 = lr_share((p.N + 15) / 16, rank + 1, LR_CLUSTER);
     struct Group {
         uint2 b[2][STEPS];
         uint32_t base[2];

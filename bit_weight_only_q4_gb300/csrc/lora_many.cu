@@ -2,9 +2,9 @@
 //
 //     t [128 x rank] = x [128 x K] A^T,     out [128 x 64] = base + scale (t [128 x rank] B [64 x rank]^T)
 // with tokens as the MMA's M.  Ten warps: eight with the exchange of t and the results, one that copies
-// (TMA), one that issues the MMAs.  A CTA's eighth of K comes first, through a ring of x and A tiles of 64
-// columns.  The sums go from tensor memory to shared memory; CTA c of the cluster adds up rows 16 c .. 16 c + 15
-// of all eight and writes them, as bf16, into the second product's operand of all eight.  Then come the
+// (TMA), one that issues the MMAs.  A CTA's share of K comes first, through a ring of x and A tiles of 64
+// columns.  The sums go from tensor memory to shared memory; each CTA of the cluster adds up its share of
+// the rows of all and writes them, as bf16, into the second product's operand of all.  Then come the
 // CTA's output columns, 64 at a time: base and B through rings, base + product in place, and out by TMA from there,
 // or, where a warp's 32 rows are not all the tile's, with plain stores (the next rows are
 // another request's).  The two groups of four warps take the pieces of 64 columns in turn.
@@ -16,23 +16,25 @@
 
 namespace q4 {
 
-constexpr int LM_ROWS = 128, LM_COPY = 8, LM_MMA = 9, LM_WARPS = 10, LM_COLS = 64, LM_D = 4;
+constexpr int LM_ROWS = 128, LM_COPY = 8, LM_MMA = 9, LM_B = 10, LM_WARPS = 11, LM_COLS = 64, LM_D = 4;
 
 // WIDE: ranks above 64.  Shared memory, in KB:
 //          base ring     weights (A or B)    t             while t is being made: x, A, and its sums
-//   narrow 0: 5 x 16     80: 2 x 8           96: 16        0: 4 x 16, 64: 4 x 8, 48: 32
-//   wide   0: 3 x 16     48: 2 x 16          80: 32        0: 3 x 16, 48: 3 x 16, 0: 64
+//   narrow 0: 4 x 16     64: 4 x 8           96: 16        0: 4 x 16, 64: 4 x 8, 32: 32
+//   wide   0: 4 x 16     64: 1 x 16          80: 32        0: 3 x 16, 48: 3 x 16, 0: 64
 template <bool WIDE>
 struct LmSmem {
-    static constexpr int BASES = WIDE ? 3 : 5, WEIGHTS = 2, STAGES = WIDE ? 3 : 4;
+    static constexpr int BASES = 4, WEIGHTS = WIDE ? 1 : 4, STAGES = WIDE ? 3 : 4;
+    // (an even number: a slot's phases are those of one group of warps, which waits for each of them)
+    static_assert(BASES % 2 == 0 && LM_D % 2 == 0, "each slot and each D is one group's");
     static constexpr uint32_t SLOT = 16384, W_SLOT = WIDE ? 16384 : 8192;
-    static constexpr uint32_t W = BASES * SLOT, T = W + WEIGHTS * W_SLOT, A = STAGES * SLOT, SUMS = WIDE ? 0 : 3 * SLOT;
-    static constexpr int BASES_EARLY = WIDE ? 0 : 3;       // slots beside the sums
+    static constexpr uint32_t W = BASES * SLOT, T = W + WEIGHTS * W_SLOT, A = STAGES * SLOT, SUMS = WIDE ? 0 : 2 * SLOT;
+    static constexpr int BASES_EARLY = WIDE ? 0 : 2, WEIGHTS_EARLY = WIDE ? 1 : 4;       // slots beside the sums
     static constexpr uint32_t BARS = T + (WIDE ? 32768 : 16384), TOTAL = BARS + 512;
 };
 
 template <bool WIDE>
-__global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 32, 2)
+__global__ void __launch_bounds__(LM_WARPS * 32, 2)
     lora_many_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap a_map,
                      const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap base_map,
                      const __grid_constant__ CUtensorMap out_map, const LoraArgs p)
@@ -44,19 +46,26 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
     const uint32_t sm = smem_u32(smem);
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const uint32_t rank = lr_rank_in_cluster();
-    const uint32_t x_full = sm + L::BARS, x_free = x_full + 32, base_full = x_free + 32, base_free = base_full + 40,
-                   w_full = base_free + 40, w_free = w_full + 16, d_full = w_free + 16, d_free = d_full + 32,
+    const uint32_t rank = lr_rank_in_cluster(), size = lr_cluster_size();
+    const uint32_t x_full = sm + L::BARS, x_free = x_full + 32, base_full = x_free + 32, base_free = base_full + 32,
+                   w_full = base_free + 32, w_free = w_full + 32, d_full = w_free + 32, d_free = d_full + 32,
                    t_full = d_free + 32, drained = t_full + 8;
     volatile int *dead_flag = reinterpret_cast<volatile int *>(smem + L::BARS + 384);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + L::BARS + 388);
 
+    if (warp == LM_COPY && lane == 0) {
+        tma_prefetch_map(&x_map);
+        tma_prefetch_map(&a_map);
+        tma_prefetch_map(&base_map);
+        tma_prefetch_map(&b_map);
+        tma_prefetch_map(&out_map);
+    }
     pdl_wait();
     LoraTile tile;
-    if (!lr_tile(p, (int)(blockIdx.x / LR_CLUSTER), LM_ROWS, tile))
+    if (!lr_tile(p, (int)(blockIdx.x / size), LM_ROWS, tile))
         return;                                            // (the whole cluster)
     if (tile.adapter < 0) {
-        lr_copy(p, tile, rank);
+        lr_copy(p, tile, rank, size);
         return;
     }
     if ((sm & 1023u) != 0u) {                              // (there is no static shared memory in front of it)
@@ -99,8 +108,8 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
     const KvDead dead = {p.err, dead_flag, smem_u32(const_cast<int *>(dead_flag))};
     auto gone_all = [&]() { return __any_sync(0xffffffffu, *dead.flag != 0); };
     const int ranks = (p.rank + 15) / 16 * 16;
-    const int k0 = lr_share((p.K + 63) / 64, rank), nk = lr_share((p.K + 63) / 64, rank + 1) - k0;
-    const int n0 = lr_share((p.N + 63) / 64, rank), nn = lr_share((p.N + 63) / 64, rank + 1) - n0;
+    const int k0 = lr_share((p.K + 63) / 64, rank, size), nk = lr_share((p.K + 63) / 64, rank + 1, size) - k0;
+    const int n0 = lr_share((p.N + 63) / 64, rank, size), nn = lr_share((p.N + 63) / 64, rank + 1, size) - n0;
     const int groups = (tile.rows + 31) / 32;              // of 32 rows
 
     if (warp < 8) {
@@ -108,47 +117,67 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
         const int quad = warp & 3, side = warp >> 2;
         const int row = quad * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t key = ranks % 32 == 0 ? (uint32_t)row & 7u : (uint32_t)(row >> 1) & 3u;
+        // place of columns j .. j + 3 (7) of row r in t
+        auto t_place = [&](int r, int j) {
+            return sm + L::T + (uint32_t)(j >> 6) * 16384u + (uint32_t)r * 128u +
+                   ((((uint32_t)(j >> 3) & 7u) ^ ((uint32_t)r & 7u)) << 4) + ((uint32_t)j & 7u) * 2u;
+        };
         if (nk > 0) {
             kv_wait(t_full, 0u, dead);
             tc_fence_after();
         }
+        if (size == 1) {
 #pragma unroll 1
-        for (int c = side * (ranks / 2); c < (side + 1) * (ranks / 2); c += 8) {
-            uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            if (nk > 0)
+            for (int c = side * (ranks / 2); c < (side + 1) * (ranks / 2); c += 8) {
+                uint32_t v[8], e[4];
                 tmem_ld8(t_lane + c, v);
-            const uint32_t at = sm + L::SUMS + (uint32_t)(row * ranks * 4);
-            sts128(at + ((((uint32_t)c >> 2) ^ key) << 4), v[0], v[1], v[2], v[3]);
-            sts128(at + ((((uint32_t)(c >> 2) + 1u) ^ key) << 4), v[4], v[5], v[6], v[7]);
-        }
-        tc_fence_before();
-        lr_cluster_arrive();
-        lr_cluster_wait();
-        const int pieces = ranks / 4;
-        for (int i = tid; i < 16 * pieces; i += 256) {
-            const int rr = i / pieces, c = i - rr * pieces, r = 16 * (int)rank + rr;
-            if (r >= tile.rows)
-                break;
-            const uint32_t k = ranks % 32 == 0 ? (uint32_t)r & 7u : (uint32_t)(r >> 1) & 3u;
-            const uint32_t at = sm + L::SUMS + (uint32_t)(r * ranks * 4) + (((uint32_t)c ^ k) << 4);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                // (columns behind the rank meet zeros of B, and are to be some)
 #pragma unroll
-            for (uint32_t j = 0; j < LR_CLUSTER; ++j) {
-                const float4 w = lr_load(lr_map(at, j));
-                v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                for (int i = 0; i < 4; ++i)
+                    e[i] = c < p.rank ? bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])) : 0u;
+                sts128(t_place(row, c), e[0], e[1], e[2], e[3]);
             }
-            // (columns behind the rank meet zeros of B, and are to be some)
-            const int j = 4 * c;
-            const uint32_t lo = bf16_pair(j < p.rank ? v.x : 0.f, j < p.rank ? v.y : 0.f),
-                           hi = bf16_pair(j < p.rank ? v.z : 0.f, j < p.rank ? v.w : 0.f);
-            const uint32_t to = sm + L::T + (uint32_t)(j >> 6) * 16384u + (uint32_t)r * 128u +
-                                ((((uint32_t)(j >> 3) & 7u) ^ ((uint32_t)r & 7u)) << 4) + ((uint32_t)j & 7u) * 2u;
+            tc_fence_before();
+        } else {
+            const uint32_t key = ranks % 32 == 0 ? (uint32_t)row & 7u : (uint32_t)(row >> 1) & 3u;
+#pragma unroll 1
+            for (int c = side * (ranks / 2); c < (side + 1) * (ranks / 2); c += 8) {
+                uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                if (nk > 0)
+                    tmem_ld8(t_lane + c, v);
+                const uint32_t at = sm + L::SUMS + (uint32_t)(row * ranks * 4);
+                sts128(at + ((((uint32_t)c >> 2) ^ key) << 4), v[0], v[1], v[2], v[3]);
+                sts128(at + ((((uint32_t)(c >> 2) + 1u) ^ key) << 4), v[4], v[5], v[6], v[7]);
+            }
+            tc_fence_before();
+            lr_cluster_arrive();
+            lr_cluster_wait();
+            const int pieces = ranks / 4, part = LM_ROWS / (int)size;
+            for (int i = tid; i < part * pieces; i += 256) {
+                const int rr = i / pieces, c = i - rr * pieces, r = part * (int)rank + rr;
+                if (r >= tile.rows)
+                    break;
+                const uint32_t k = ranks % 32 == 0 ? (uint32_t)r & 7u : (uint32_t)(r >> 1) & 3u;
+                const uint32_t at = sm + L::SUMS + (uint32_t)(r * ranks * 4) + (((uint32_t)c ^ k) << 4);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (uint32_t y = 0; y < LR_CLUSTER; ++y)
-                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(lr_map(to, y)), "r"(lo), "r"(hi) : "memory");
+                for (uint32_t j = 0; j < LR_CLUSTER; ++j) {
+                    if (j < size) {
+                        const float4 w = lr_load(lr_map(at, j));
+                        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                    }
+                }
+                const int j = 4 * c;
+                const uint32_t lo = j < p.rank ? bf16_pair(v.x, v.y) : 0u, hi = j < p.rank ? bf16_pair(v.z, v.w) : 0u;
+                const uint32_t to = t_place(r, j);
+#pragma unroll
+                for (uint32_t y = 0; y < LR_CLUSTER; ++y)
+                    if (y < size)
+                        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(lr_map(to, y)), "r"(lo), "r"(hi) : "memory");
+            }
         }
         asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
         lr_cluster_arrive();
         lr_cluster_wait();
         const float scale = __ldg(p.scales + tile.adapter);
@@ -218,7 +247,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (warp == LM_COPY) {
         // ------------------------------------------------------- copies
-        int xs = 0, bs = 0, ws = 0;                        // issued
+        int xs = 0, bs = 0;                                // issued
 #pragma unroll 1
         for (int i = 0; i < nk && !gone_all(); ++i) {
             const uint32_t s = (uint32_t)i % L::STAGES;
@@ -249,8 +278,10 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
             kv_wait(t_full, 0u, dead);                     // (x and A have been read)
         for (int i = 0; i < L::BASES_EARLY && i < nn && !gone_all(); ++i)
             ask_base();
-        lr_cluster_arrive();
-        lr_cluster_wait();
+        if (size > 1) {                                    // (every thread passes the same barriers)
+            lr_cluster_arrive();
+            lr_cluster_wait();
+        }
         lr_cluster_arrive();
         lr_cluster_wait();
 #pragma unroll 1
@@ -262,20 +293,6 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
                     break;
                 ask_base();
             }
-            const uint32_t s = (uint32_t)q % L::WEIGHTS;
-            if (q >= L::WEIGHTS)
-                kv_wait(w_free + 8u * s, ((uint32_t)q / L::WEIGHTS - 1u) & 1u, dead);
-            if (gone_all())
-                break;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(w_full + 8u * s, L::W_SLOT);
-#pragma unroll
-                for (int h = 0; h < (WIDE ? 2 : 1); ++h)
-                    tma_load_3d(sm + L::W + s * L::W_SLOT + 8192u * h, &b_map, 64 * h, (n0 + q) * LM_COLS, tile.adapter,
-                                w_full + 8u * s);
-            }
-            __syncwarp();
-            ++ws;
         }
         if (gone_all()) {
             // copies in flight land before the CTA ends
@@ -283,9 +300,43 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
                 mbar_wait(x_full + 8u * ((uint32_t)i % L::STAGES), ((uint32_t)i / L::STAGES) & 1u, p.err);
             for (int i = bs > L::BASES ? bs - L::BASES : 0; i < bs; ++i)
                 mbar_wait(base_full + 8u * ((uint32_t)i % L::BASES), ((uint32_t)i / L::BASES) & 1u, p.err);
+        }
+    } else if (warp == LM_B) {
+        // ------------------------------------------- B, beside the copies of base
+        int ws = 0;
+        auto ask = [&]() {
+            const uint32_t s = (uint32_t)ws % L::WEIGHTS;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(w_full + 8u * s, L::W_SLOT);
+#pragma unroll
+                for (int h = 0; h < (WIDE ? 2 : 1); ++h)
+                    tma_load_3d(sm + L::W + s * L::W_SLOT + 8192u * h, &b_map, 64 * h, (n0 + ws) * LM_COLS, tile.adapter,
+                                w_full + 8u * s);
+            }
+            __syncwarp();
+            ++ws;
+        };
+        if (nk > 0)
+            kv_wait(t_full, 0u, dead);                     // (x and A have been read)
+        for (int i = 0; i < L::WEIGHTS_EARLY && i < nn && !gone_all(); ++i)
+            ask();
+        if (size > 1) {
+            lr_cluster_arrive();
+            lr_cluster_wait();
+        }
+        lr_cluster_arrive();
+        lr_cluster_wait();
+#pragma unroll 1
+        while (ws < nn && !gone_all()) {
+            if (ws >= L::WEIGHTS)
+                kv_wait(w_free + 8u * ((uint32_t)ws % L::WEIGHTS), ((uint32_t)ws / L::WEIGHTS - 1u) & 1u, dead);
+            if (gone_all())
+                break;
+            ask();
+        }
+        if (gone_all())
             for (int i = ws > L::WEIGHTS ? ws - L::WEIGHTS : 0; i < ws; ++i)
                 mbar_wait(w_full + 8u * ((uint32_t)i % L::WEIGHTS), ((uint32_t)i / L::WEIGHTS) & 1u, p.err);
-        }
     } else {
         // --------------------------------------------------------- MMAs
         const uint64_t d0 = smem_desc_sw128(sm);
@@ -306,8 +357,10 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
             }
             __syncwarp();
         }
-        lr_cluster_arrive();
-        lr_cluster_wait();
+        if (size > 1) {                                    // (every thread passes the same barriers)
+            lr_cluster_arrive();
+            lr_cluster_wait();
+        }
         lr_cluster_arrive();
         lr_cluster_wait();
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -343,7 +396,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LM_WARPS * 
 }
 
 template <bool WIDE>
-static q4_status lm_launch(const LoraArgs &a, cudaStream_t st, bool pdl)
+static q4_status lm_launch(const DeviceInfo &dev, const LoraArgs &a, cudaStream_t st, bool pdl)
 {
     CUtensorMap x, wa, wb, base, out;
     const int ranks = (a.rank + 15) / 16 * 16;
@@ -362,25 +415,33 @@ static q4_status lm_launch(const LoraArgs &a, cudaStream_t st, bool pdl)
     cudaError_t e = cudaFuncSetAttribute(lora_many_kernel<WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaFuncSetAttribute(lora_many_kernel)");
-    // at most one part-filled tile a request
-    const int64_t tiles = (int64_t)a.tokens / LM_ROWS + a.batch;
+    // At most one part-filled tile a request.  Clusters are as small as leaves two CTAs for every SM: what comes before the
+    // columns takes a CTA some 15,000 cycles, whether they are many or few.
+    int64_t tiles = (int64_t)a.tokens / LM_ROWS + a.batch;
+    tiles = tiles < a.tokens ? tiles : a.tokens;
+    int size = 1;
+    while (size < LR_CLUSTER && tiles * size < 2 * (int64_t)dev.sms)
+        size *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((tiles < a.tokens ? tiles : a.tokens) * LR_CLUSTER));
+    cfg.gridDim = dim3((unsigned)(tiles * size));
     cfg.blockDim = dim3(LM_WARPS * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = pdl ? attr : nullptr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, lora_many_kernel<WIDE>, x, wa, wb, base, out, a);
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of lora_many_kernel");
 }
 
-q4_status launch_lora_many(const LoraArgs &a, cudaStream_t st, bool pdl)
+q4_status launch_lora_many(const DeviceInfo &dev, const LoraArgs &a, cudaStream_t st, bool pdl)
 {
-    return a.rank <= 64 ? lm_launch<false>(a, st, pdl) : lm_launch<true>(a, st, pdl);
+    return a.rank <= 64 ? lm_launch<false>(dev, a, st, pdl) : lm_launch<true>(dev, a, st, pdl);
 }
 
 }  // namespace q4
