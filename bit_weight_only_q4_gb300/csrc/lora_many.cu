@@ -16,20 +16,21 @@
 
 namespace q4 {
 
-constexpr int LM_ROWS = 128, LM_COPY = 8, LM_MMA = 9, LM_B = 10, LM_WARPS = 11, LM_COLS = 64, LM_D = 4;
+constexpr int LM_ROWS = 128, LM_COPY = 8, LM_MMA = 9, LM_B = 10, LM_WARPS = 11, LM_COLS = 64;
 
-// WIDE: ranks above 64.  Shared memory, in KB:
+// WIDE: ranks above 64.  There t goes on into tensor memory, as the second product's A operand, and leaves its
+// place to B.  Shared memory, in KB:
 //          base ring     weights (A or B)    t             while t is being made: x, A, and its sums
 //   narrow 0: 4 x 16     64: 4 x 8           96: 16        0: 4 x 16, 64: 4 x 8, 32: 32
-//   wide   0: 4 x 16     64: 1 x 16          80: 32        0: 3 x 16, 48: 3 x 16, 0: 64
+//   wide   0: 4 x 16     64: 3 x 16          80: 32        0: 3 x 16, 48: 3 x 16, 0: 64
 template <bool WIDE>
 struct LmSmem {
-    static constexpr int BASES = 4, WEIGHTS = WIDE ? 1 : 4, STAGES = WIDE ? 3 : 4;
+    static constexpr int BASES = 4, WEIGHTS = WIDE ? 3 : 4, STAGES = WIDE ? 3 : 4, DS = WIDE ? 2 : 4;       // DS: D in tensor memory
     // (an even number: a slot's phases are those of one group of warps, which waits for each of them)
-    static_assert(BASES % 2 == 0 && LM_D % 2 == 0, "each slot and each D is one group's");
+    static_assert(BASES % 2 == 0 && DS % 2 == 0, "each slot and each D is one group's");
     static constexpr uint32_t SLOT = 16384, W_SLOT = WIDE ? 16384 : 8192;
-    static constexpr uint32_t W = BASES * SLOT, T = W + WEIGHTS * W_SLOT, A = STAGES * SLOT, SUMS = WIDE ? 0 : 2 * SLOT;
-    static constexpr int BASES_EARLY = WIDE ? 0 : 2, WEIGHTS_EARLY = WIDE ? 1 : 4;       // slots beside the sums
+    static constexpr uint32_t W = BASES * SLOT, T = W + (WIDE ? 1 : 4) * W_SLOT, A = STAGES * SLOT, SUMS = WIDE ? 0 : 2 * SLOT;
+    static constexpr int BASES_EARLY = WIDE ? 0 : 2, WEIGHTS_EARLY = WIDE ? 1 : 4;       // slots beside the sums and t
     static constexpr uint32_t BARS = T + (WIDE ? 32768 : 16384), TOTAL = BARS + 512;
 };
 
@@ -40,7 +41,8 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
                      const __grid_constant__ CUtensorMap out_map, const LoraArgs p)
 {
     using L = LmSmem<WIDE>;
-    constexpr uint32_t TM_COLS = LM_D * LM_COLS;
+    constexpr uint32_t TM_COLS = 256, TM_T = 128;           // D from column 0 on, t as an operand
+    constexpr int LM_D = L::DS;
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);    // bf16, fp32 sums, M = 128
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sm = smem_u32(smem);
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
     const uint32_t rank = lr_rank_in_cluster(), size = lr_cluster_size();
     const uint32_t x_full = sm + L::BARS, x_free = x_full + 32, base_full = x_free + 32, base_free = base_full + 32,
                    w_full = base_free + 32, w_free = w_full + 32, d_full = w_free + 32, d_free = d_full + 32,
-                   t_full = d_free + 32, drained = t_full + 8;
+                   t_full = d_free + 32, drained = t_full + 8, t_ready = drained + 8;
     volatile int *dead_flag = reinterpret_cast<volatile int *>(smem + L::BARS + 384);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(smem + L::BARS + 388);
 
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
             }
             mbar_init(t_full, 1);
             mbar_init(drained, 1);
+            mbar_init(t_ready, 4);
             *dead_flag = 0;
         }
         mbar_init_fence();
@@ -180,6 +183,24 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
         __syncwarp();
         lr_cluster_arrive();
         lr_cluster_wait();
+        if (WIDE && side == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 e = lds128(t_place(row, 64 * h + 8 * c));
+                    w[4 * c] = e.x, w[4 * c + 1] = e.y, w[4 * c + 2] = e.z, w[4 * c + 3] = e.w;
+                }
+                tmem_st32(t_lane + TM_T + 32u * h, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async();                           // (B comes to where they were)
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(t_ready);
+        }
         const float scale = __ldg(p.scales + tile.adapter);
         const int last = tile.rows - quad * 32;            // the warp's rows, if below 32
 #pragma unroll 1
@@ -326,6 +347,8 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
         }
         lr_cluster_arrive();
         lr_cluster_wait();
+        if (WIDE)
+            kv_wait(t_ready, 0u, dead);
 #pragma unroll 1
         while (ws < nn && !gone_all()) {
             if (ws >= L::WEIGHTS)
@@ -364,6 +387,8 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
         lr_cluster_arrive();
         lr_cluster_wait();
         asm volatile("fence.proxy.async;" ::: "memory");
+        if (WIDE)
+            kv_wait(t_ready, 0u, dead);
         tc_fence_after();
 #pragma unroll 1
         for (int q = 0; q < nn && !gone_all(); ++q) {
@@ -373,10 +398,14 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
                 kv_wait(d_free + 8u * d, ((uint32_t)q / LM_D - 1u) & 1u, dead);
             tc_fence_after();
             if (elect_one()) {
-                for (int kk = 0; kk < ranks / 16; ++kk)
-                    mma_f16_2(tmem + LM_COLS * d, lo + ((L::T + (uint32_t)(kk >> 2) * 16384u) >> 4) + 2u * (kk & 3), hi,
-                              lo + ((L::W + s * L::W_SLOT + (uint32_t)(kk >> 2) * 8192u) >> 4) + 2u * (kk & 3), hi,
-                              IDESC | ((uint32_t)(LM_COLS >> 3) << 17), kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < ranks / 16; ++kk) {
+                    const uint32_t b = lo + ((L::W + s * L::W_SLOT + (uint32_t)(kk >> 2) * 8192u) >> 4) + 2u * (kk & 3),
+                                   idesc = IDESC | ((uint32_t)(LM_COLS >> 3) << 17);
+                    if (WIDE)
+                        mma_f16_tmem_a(tmem + LM_COLS * d, tmem + TM_T + 8u * kk, b, hi, idesc, kk > 0 ? 1u : 0u);
+                    else
+                        mma_f16_2(tmem + LM_COLS * d, lo + (L::T >> 4) + 2u * kk, hi, b, hi, idesc, kk > 0 ? 1u : 0u);
+                }
                 mma_commit(d_full + 8u * d);
                 mma_commit(w_free + 8u * s);
             }
