@@ -143,9 +143,16 @@ q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b,
     p.offsets = offsets, p.ids = ids;
     p.batch = batch, p.tokens = tokens, p.adapters = adapters, p.rank = rank, p.N = N, p.K = K;
     p.err = device_error_flags();
-    // Requests are judged by their mean length, for the lengths are on the device.
-    return tokens <= 8 * (int64_t)batch ? launch_lora_few(p, static_cast<cudaStream_t>(stream), pdl_on())
-                                        : launch_lora_many(dev, p, static_cast<cudaStream_t>(stream), pdl_on());
+    // Which kernel, for the lengths are on the device: the one of eight-token tiles where requests have
+    // eight tokens in the mean, or where its CTAs are all on the GPU at once and what their tiles read of the
+    // adapters, each anew, stays below 32 MB.  Measured (eight-token tiles, 128-token tiles): 64 requests of 5, rank 64, 14.9
+    // against 28 us; 16 of 32, rank 16, 6.4 against 10.8; 16 of 64, rank 64, 18.6 against 12.2; 60 of 50, rank 16, 33
+    // against 18.
+    const int64_t tiles = tokens / 8 + batch / 2;
+    const bool few = tokens <= 8 * (int64_t)batch ||
+                     (tiles <= dev.sms / 2 && tiles * 2 * rank * ((int64_t)N + K) <= 32 << 20);
+    return few ? launch_lora_few(p, static_cast<cudaStream_t>(stream), pdl_on())
+               : launch_lora_many(dev, p, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
 }  // extern "C"

@@ -7,7 +7,8 @@
 // long as both operands agree: a lane takes eight adjacent ones (16 bytes), which serve two MMAs.
 // Output columns lie two to a lane, so that eight lanes store 32 bytes.
 //
-// What bounds it: the chain of offsets, x and A, the exchange, B, not the bytes.
+// What bounds it: the chain of offsets, x and A, the exchange, B (48 single tokens, rank 16: 5.4 us), and where tiles
+// share adapters, L2, from which each tile reads its own.
 #include "lora.cuh"
 
 namespace q4 {
@@ -21,9 +22,10 @@ __device__ __forceinline__ void lf_mma(float (&c)[4], uint32_t a0, uint32_t a1, 
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// STEPS: 16s of rank values, rounded up to a power of two.
+// STEPS: 16s of rank values, rounded up to a power of two.  Four CTAs an SM up to rank 64 (64 registers): 64 requests of
+// 5 tokens, 512 CTAs, are one wave then (14.9 us; with 76 registers 20.3).
 template <int STEPS>
-__global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 32) lora_few_kernel(const LoraArgs p)
+__global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 32, STEPS <= 4 ? 4 : 2) lora_few_kernel(const LoraArgs p)
 {
     constexpr int RANKS = 16 * STEPS;
     constexpr int PITCH = RANKS + 8;

@@ -19,14 +19,16 @@
 //     y_j = r (x_j (w_j cos_j) + x_p (+-w_p sin_j)),    p the partner,
 // and the bracket's factors are worked out once for a token's queries and once for its keys.
 //
-// What bounds it: HBM, 4 bytes a value.
+// What bounds it: HBM, 4 bytes a value (65,000 tokens, 32 and 8 heads of 128: 235 us, 5.7 TB/s), with
+// instruction issue close behind (some 130 for 512 bytes); for a few thousand tokens the issue (8,162 tokens, 36 heads
+// of 64: 23 us) and for a step its launch and the chain of loads, fp64 and sincospif (3.3 us).
 #include "layer_ops.h"
 #include "tc_device.cuh"
 
 namespace q4 {
 
-constexpr int NR_WARPS = 8;
-constexpr int NR_BATCH = 4;                // passes over the warp whose loads are in flight together
+constexpr int NR_WARPS = 4;
+constexpr int NR_BATCH = 2;                // passes over the warp whose loads are in flight together
 
 // u of frequency f (see above).
 __device__ __forceinline__ uint64_t nr_turn(float f)
@@ -47,7 +49,7 @@ __device__ __forceinline__ uint32_t nr_narrow(f32x2 v)
 {
     float a, b;
     unpack2(v, a, b);
-    return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+    return bf16_pair(a, b);
 }
 
 template <int LANES>
@@ -95,7 +97,7 @@ __device__ __forceinline__ void nr_factors(NrFactors &f, const uint16_t *weight,
 
 // PAIRS: adjacent columns are turned together (interleaved).
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(NR_WARPS * 32, 3) norm_rope_kernel(const NormRopeArgs a)
+__global__ void __launch_bounds__(NR_WARPS * 32, 6) norm_rope_kernel(const NormRopeArgs a)
 {
     constexpr int LANES = D / 8;           // of a head
     constexpr int PER = 32 / LANES;        // heads of a pass
@@ -151,15 +153,23 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 3) norm_rope_kernel(const NormR
             uint16_t *out = (kind ? a.k_out + token * a.k_out_stride : a.q_out + token * a.q_out_stride) + 8 * lane;
             NrFactors f;
             nr_factors<PAIRS>(f, weight, l, partner % LANES, turned, front ? -1.f : 1.f, &s_angle[warp][first]);
+            uint4 next[NR_BATCH];
+            auto ask = [&](int base) {
+#pragma unroll
+                for (int i = 0; i < NR_BATCH; ++i) {
+                    next[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (base + i * PER + sub < end)
+                        next[i] = *reinterpret_cast<const uint4 *>(in + (int64_t)(base + i * PER) * D);
+                }
+            };
+            ask(begin);
 #pragma unroll 1
             for (int base = begin; base < end; base += NR_BATCH * PER) {
                 uint4 x[NR_BATCH];
 #pragma unroll
-                for (int i = 0; i < NR_BATCH; ++i) {
-                    x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (base + i * PER + sub < end)
-                        x[i] = *reinterpret_cast<const uint4 *>(in + (int64_t)(base + i * PER) * D);
-                }
+                for (int i = 0; i < NR_BATCH; ++i)
+                    x[i] = next[i];
+                ask(base + NR_BATCH * PER);
 #pragma unroll
                 for (int i = 0; i < NR_BATCH; ++i) {
                     if (base + i * PER >= end)
@@ -224,12 +234,13 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 3) norm_rope_kernel(const NormR
 q4_status launch_norm_rope(const DeviceInfo &dev, NormRopeArgs a, int head_dim, cudaStream_t st, bool pdl)
 {
     // A warp takes all heads of a token, or, where that would leave SMs without work, as many as
-    // one batch of loads brings.
+    // one batch of loads brings.  Measured: 8,162 tokens of 36 heads of 64, whole 25.1, in batches 29.8 us (the angles are
+    // worked out for each); 48 tokens of 32 heads of 128 in CTAs of 4 warps 3.3, of 8 warps 4.2 us.
     const int heads = a.q_heads + a.kv_heads, batch = NR_BATCH * (256 / head_dim);
-    a.part_heads = (int64_t)a.tokens >= (int64_t)dev.sms * NR_WARPS * 2 ? heads : batch;
+    a.part_heads = (int64_t)a.tokens >= (int64_t)dev.sms * NR_WARPS * 4 ? heads : batch;
     a.parts = (heads + a.part_heads - 1) / a.part_heads;
     const int64_t ctas = ((int64_t)a.tokens * a.parts + NR_WARPS - 1) / NR_WARPS;
-    const int64_t most = (int64_t)dev.sms * 3;
+    const int64_t most = (int64_t)dev.sms * 6;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most));
     cfg.blockDim = dim3(NR_WARPS * 32);
