@@ -330,7 +330,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 // of hanging.
 constexpr uint32_t kMbarSpinLimit = 1u << 26;
 constexpr unsigned kErrBarrierTimeout = 1u;
-constexpr unsigned kErrIndex = 4u;         // Q4_DEVERR_INDEX
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned *err)
 {

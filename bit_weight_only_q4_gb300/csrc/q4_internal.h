@@ -90,6 +90,8 @@ q4_status tc_launch(int kind, const void *x, const uint8_t *codes, const void *s
                     const void *minv, const float *gscale, void *y, int M, int N, int K,
                     void *ws, size_t ws_bytes, cudaStream_t stream, bool pdl);
 
+constexpr unsigned kErrIndex = 4u;         // Q4_DEVERR_INDEX
+
 // Device address of the library's error-flag word in the current context
 // (looked up once per device and context; nullptr if the lookup fails).
 unsigned *device_error_flags();

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "q4_device.cuh"
+#include "q4_internal.h"
 
 namespace q4 {
 
