@@ -14,15 +14,14 @@
 // reference raised and what was summed scaled down.  So a tile that is seen whole costs one pass over its scores and no maximum.
 //
 // One CTA per SM, 12 warps: four with the softmax of A (one thread a row), four with that of
-// B, one that copies (TMA), one that issues the MMAs, one that fetches units.  A step is one tile of rows on one tile of keys; A and
-// B take turns.  Step n has its S in buffer n mod BUFS of tensor memory, and P takes the place of
-// its S.  MMAs run in the order
-//     .. P(n) V  S(n + BUFS)  P(n + 1) V  S(n + 1 + BUFS) ..
-// so that the tensor cores work on one tile of rows while the other is in its softmax, and an S is
-// overwritten by an MMA that comes behind the one that reads P in its place.  With heads of 128, two S
-// and two O fill the tensor memory, and P is handed over in two halves, so that less of a step's
-// softmax lies between two MMAs of its rows; with heads of 64 there is room for a third S, and the softmax of a step
-// follows that of the rows' last one without a wait.
+// B, one that copies (TMA), one that issues the MMAs, one that fetches units.  A step is one tile of
+// rows on one tile of keys; A and B take turns, so that the tensor cores work on one while the
+// other is in its softmax.
+//   Heads of 128: two S and two O fill the tensor memory, and P takes the place of its S, whose MMA for the next step
+//   comes behind the one that reads P.  P is handed over in two halves, so that less of a step's softmax lies between two MMAs of
+//   its rows.
+//   Heads of 64: P has a place of its own, and S is free for the next step as soon as it has been read: a step's softmax
+//   follows that of the rows' last one without a wait.
 //
 // A masked probability is 0, and 0 times a v that is not finite would be NaN: tiles cut by the
 // mask are looked through for such values (by a warp that does nothing else), and a tile that has one
@@ -41,7 +40,8 @@ constexpr float PA_SUM_TOP = 0x1p20f;
 
 template <int D>
 struct PaSmem {
-    static constexpr int BUFS = D == 128 ? 2 : 3, HALVES = D == 128 ? 2 : 1;
+    static constexpr bool APART = D == 64;                           // P is not in the place of S
+    static constexpr int HALVES = APART ? 1 : 2;
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t TILE = PA_KEYS * D * 2;
     static constexpr uint32_t RING = 2 * TILE;                       // [Q of A, Q of B][ring][results, 4 KB a warp]
@@ -131,13 +131,6 @@ __device__ __forceinline__ int pa_answer(uint32_t at)
     return r;
 }
 
-template <int BUFS>
-__device__ __forceinline__ int pa_next(int buf, int steps)
-{
-    buf += steps;
-    return buf >= BUFS ? buf - BUFS : buf;
-}
-
 template <int D>
 __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -146,14 +139,17 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
 {
     using L = PaSmem<D>;
     constexpr int NS = L::STAGES;
-    constexpr int BUFS = L::BUFS, HALVES = L::HALVES, CH = PA_KEYS / HALVES;
-    constexpr uint32_t TM_S = 0, TM_O = 128 * BUFS, TM_COLS = 512;   // buffers of S, O of A and of B
+    constexpr bool APART = L::APART;
+    constexpr int HALVES = L::HALVES, CH = PA_KEYS / HALVES;
+    // tensor memory: S of A and of B, P (where it is apart), O
+    constexpr uint32_t TM_S = 0, TM_P = APART ? 256 : TM_S, TM_P_STEP = APART ? 64 : 128, TM_P_HALF = APART ? CH / 2 : CH,
+                       TM_O = APART ? 384 : 256, TM_COLS = 512;
     static_assert(TM_O + 2 * D <= TM_COLS, "tensor memory");
     constexpr uint32_t BF16 = (1u << 7) | (1u << 10);
     constexpr uint32_t IDESC_S = (1u << 4) | BF16 | ((uint32_t)(PA_KEYS >> 3) << 17) | (8u << 24);
     constexpr uint32_t IDESC_O = (1u << 4) | BF16 | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 4 + 2 * HALVES + BUFS * (2 + HALVES) + 2 * PA_QUEUE + 1 + NS];
+    __shared__ uint64_t s_bar[2 * NS + 8 + 4 * HALVES + 2 * PA_QUEUE + 1 + NS];
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) uint4 s_answer;
     __shared__ PaUnit s_unit[PA_QUEUE];
@@ -163,9 +159,8 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
     const uint32_t kv_full = smem_u32(s_bar), kv_free = kv_full + 8u * NS, q_full = kv_free + 8u * NS,   // q_full: A, B
                    q_free = q_full + 16, drained = q_full + 24, pv_done = q_full + 32,      // pv_done: by tile and half
-                   s_full = pv_done + 16u * HALVES,            // by tile and buffer: each phase has one waiter, who misses none
-                   p_full = s_full + 16u * BUFS,               // by buffer and half
-                   unit_full = p_full + 8u * BUFS * HALVES, unit_free = unit_full + 8u * PA_QUEUE,
+                   s_full = pv_done + 16u * HALVES, s_free = s_full + 16, p_full = s_free + 16,        // by tile (and half)
+                   unit_full = p_full + 16u * HALVES, unit_free = unit_full + 8u * PA_QUEUE,
                    answered = unit_free + 8u * PA_QUEUE, v_raw = answered + 8;        // by stage: V that is to be looked through
     pdl_wait();
     PaWalk walk(p);
@@ -191,9 +186,11 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 for (int half = 0; half < HALVES; ++half)
                     mbar_init(pv_done + 8u * (i * HALVES + half), 1);
             }
-            for (int i = 0; i < 2 * BUFS; ++i)
+            for (int i = 0; i < 2; ++i) {
                 mbar_init(s_full + 8u * i, 1);
-            for (int i = 0; i < BUFS * HALVES; ++i)
+                mbar_init(s_free + 8u * i, 4);
+            }
+            for (int i = 0; i < 2 * HALVES; ++i)
                 mbar_init(p_full + 8u * i, 4);
             s_dead = 0;
         }
@@ -233,14 +230,16 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         const uint32_t t_o = t_lane + TM_O + (uint32_t)(D * x);
         const float sl = p.scale_log2;
         const f32x2 sl2 = pack2(sl, sl);
-        uint32_t ring = 0u, steps = 0u, pv_count = 0u, phases = 0u;       // copies and this tile's steps before; parity of its S in each buffer
+        const uint32_t t_s = t_lane + TM_S + 128u * x, t_ps = t_lane + TM_P + TM_P_STEP * x;
+        uint32_t ring = 0u, steps = 0u, pv_count = 0u;     // copies, this tile's steps and waited-for MMAs before
         const uint32_t pv_first = pv_done + 8u * (uint32_t)(x * HALVES), pv_last = pv_first + 8u * (HALVES - 1);
-        // The step before is through its MMAs.  With two buffers its S is overwritten by this step's, which came behind
-        // them; with three, each step waits for the one before it, so that no barrier is ever two phases from the one
-        // that is waited for.
+        // The step before is through its MMAs.  Where P is in the place of S, this step's S came behind them; where it
+        // is apart, each step waits for the one before it, so that no barrier is ever two phases from the one that is waited for.
         auto last_step = [&]() {
-            if (BUFS == 3 && pv_count > 0)
+            if (APART && pv_count > 0) {
                 kv_wait(pv_last, (pv_count - 1u) & 1u, dead);
+                tc_fence_after();
+            }
         };
         // And so are the halves of this step before half `half`.
         auto pv_wait = [&](int half) {
@@ -261,24 +260,14 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             const int whole = (first + 1) / PA_KEYS;       // key tiles that all rows see wholly
             float m = -INFINITY;
             f32x2 la = 0ull, lb = 0ull;
-            int buf = 0;
 #pragma unroll 1
-            for (int j = n - 1; j >= 0; --j) {
-                // the step's buffer; A has none on the last tile of keys where that is B's alone
-                const bool both = u.nb > 0 && j < u.na;
-                const int at_buf = BUFS == 2 ? x : both && x ? pa_next<BUFS>(buf, 1) : buf;
-                buf = pa_next<BUFS>(buf, both ? 2 : 1);
-                if (j >= mine)
-                    continue;
-                const uint32_t parity = (phases >> at_buf) & 1u;
-                phases ^= 1u << at_buf;
-                const uint32_t t_s = t_lane + TM_S + 128u * (uint32_t)at_buf;
+            for (int j = mine - 1; j >= 0; --j) {
                 const bool masked = j >= whole;
                 const int seen = token >= 0 ? token - j * PA_KEYS : PA_KEYS - 1;      // the row's last visible column
                 int hi = PA_KEYS - 1;
                 const uint32_t v_at = ring + 2u * (uint32_t)(n - 1 - j) + 1u, v_stage = v_at & (NS - 1);
                 const uint32_t v_tile = sm + L::RING + v_stage * L::TILE;
-                kv_wait(s_full + 8u * (uint32_t)(x * BUFS + at_buf), parity, dead);
+                kv_wait(s_full + 8u * x, steps & 1u, dead);
                 tc_fence_after();
                 if (masked)
                     hi = __reduce_max_sync(0xffffffffu, seen);
@@ -400,7 +389,14 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                             }
                         }
                     }
-                    const uint32_t t_p = t_s + (uint32_t)c0;
+                    if (APART) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(s_free + 8u * x);
+                        last_step();                       // (its P has been read)
+                    }
+                    const uint32_t t_p = t_ps + TM_P_HALF * (uint32_t)half;
 #pragma unroll
                     for (int c = 0; c < CH / 2; c += 32)
                         tmem_st32(t_p + c, reinterpret_cast<uint32_t(&)[32]>(ph[c]));
@@ -450,14 +446,12 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                         }
                         tmem_wait_st();
                     }
-                    if (half == HALVES - 1)
-                        last_step();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(p_full + 8u * (uint32_t)(at_buf * HALVES + half));
+                        mbar_arrive(p_full + 8u * (uint32_t)(x * HALVES + half));
                 }
-                if (BUFS == 3 || j == 0)
+                if (APART || j == 0)
                     ++pv_count;
                 ++steps;
             }
@@ -585,7 +579,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         // This warp is what the tensor cores wait for, so the two tiles are written out (x is known where it is
         // compiled) and everything that an MMA takes is the warp's: such an MMA takes 30 (PV) and 52 cycles (S) to
         // issue, of the 64 or 32 that it runs.
-        uint32_t at = 0u, qn = 0u, phases = 0u;            // copies before this unit; parities of Q loads and of P's
+        uint32_t at = 0u, qn = 0u, sn[2] = {0u, 0u}, pn = 0u;          // copies before this unit; parities of Q loads, S's, parities of P's
         const uint64_t qd = smem_desc_sw128(sm), kd = smem_desc_sw128(sm + L::RING);
         const uint64_t vd = (kd & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(D == 128 ? PA_KEYS * 128 >> 4 : 0) << 16);
         const uint32_t q_lo = (uint32_t)qd, q_hi = (uint32_t)(qd >> 32), k_lo = (uint32_t)kd, k_hi = (uint32_t)(kd >> 32),
@@ -598,7 +592,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             const int n = pair ? nb : na, late = n - na;   // tiles of keys that A begins behind B
             const int cut[2] = {n - (begin + 1) / PA_KEYS, n - (begin + p.tile_tokens + 1) / PA_KEYS};   // that the mask cuts
             // S of tile x on the t-th tile of keys
-            auto score = [&](int x, int t, int buf) {
+            auto score = [&](int x, int t) {
                 const uint32_t k = at + 2u * (uint32_t)t, stage = k & (NS - 1);
                 if (t == (x ? 0 : late)) {
                     kv_wait(q_full + 8u * x, (qn >> x) & 1u, dead);
@@ -606,16 +600,19 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 }
                 if (x == 0 || t == 0)                      // (B's S comes behind A's, but for the first)
                     kv_wait(kv_full + 8u * stage, (k / NS) & 1u, dead);
+                if (APART && sn[x] > 0)
+                    kv_wait(s_free + 8u * x, (sn[x] - 1u) & 1u, dead);
+                ++sn[x];
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t a = q_lo + (uint32_t)x * (L::TILE >> 4), b = k_lo + stage * (L::TILE >> 4),
-                                   d = tmem + TM_S + 128u * (uint32_t)buf;
+                                   d = tmem + TM_S + 128u * (uint32_t)x;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t step = (uint32_t)(kk >> 2) * (16384u >> 4) + 2u * (kk & 3);
                         mma_f16_2(d, a + step, q_hi, b + step, k_hi, IDESC_S, kk > 0 ? 1u : 0u);
                     }
-                    mma_commit(s_full + 8u * (uint32_t)(x * BUFS + buf));
+                    mma_commit(s_full + 8u * (uint32_t)x);
                     if (x == 1 || !pair) {                 // the last with these keys
                         mma_commit(kv_free + 8u * stage);
                         if (t == n - 1)
@@ -625,92 +622,58 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 __syncwarp();
             };
             // O of tile x += P V
-            auto add = [&](int x, int t, int buf) {
+            auto add = [&](int x, int t) {
                 const uint32_t k = at + 2u * (uint32_t)t + 1u, stage = k & (NS - 1);
                 if (x == 0 || t < late)
                     kv_wait(kv_full + 8u * stage, (k / NS) & 1u, dead);
                 const bool masked = t < cut[x], first = t == (x ? 0 : late);
 #pragma unroll
                 for (int half = 0; half < HALVES; ++half) {
-                    kv_wait(p_full + 8u * (uint32_t)(buf * HALVES + half), (phases >> buf) & 1u, dead);
+                    kv_wait(p_full + 8u * (uint32_t)(x * HALVES + half), (pn >> x) & 1u, dead);
                     tc_fence_after();
                     const bool skip = masked && __shfl_sync(0xffffffffu, *(volatile int *)&s_bad[stage], 0) != 0;
                     if (elect_one()) {
                         if (!skip) {
                             const uint32_t b = v_lo + stage * (L::TILE >> 4), o = tmem + TM_O + (uint32_t)(D * x),
-                                           pm = tmem + TM_S + 128u * (uint32_t)buf;
+                                           pm = tmem + TM_P + TM_P_STEP * (uint32_t)x + TM_P_HALF * (uint32_t)half;
 #pragma unroll
                             for (int kk = 0; kk < CH / 16; ++kk)
-                                mma_f16_tmem_a(o, pm + (uint32_t)(half * CH) + 8u * kk,
+                                mma_f16_tmem_a(o, pm + 8u * kk,
                                                b + (uint32_t)(half * (CH / 16) + kk) * (2048 >> 4), v_hi, IDESC_O,
                                                kk > 0 || half > 0 || !first ? 1u : 0u);
                         }
-                        if (BUFS == 3 || half < HALVES - 1 || t == n - 1)              // (the others are waited for by none)
+                        if (APART || half < HALVES - 1 || t == n - 1)          // (the others are waited for by none)
                             mma_commit(pv_done + 8u * (uint32_t)(x * HALVES + half));
-                        if (BUFS == 3 && half == HALVES - 1 && (x == 1 || !pair))
+                        if (APART && half == HALVES - 1 && (x == 1 || !pair))
                             mma_commit(kv_free + 8u * stage);
                     }
                     __syncwarp();
                 }
-                phases ^= 1u << buf;
+                pn ^= 1u << x;
             };
             auto release = [&](uint32_t k) {
                 if (elect_one())
                     mma_commit(kv_free + 8u * (k & (NS - 1)));
                 __syncwarp();
             };
-            if constexpr (BUFS == 2) {
-                // A has the first buffer, B the second
-                score(0, late, 0);
-                if (pair)
-                    score(1, 0, 1);
+            score(0, late);
+            if (pair)
+                score(1, 0);
 #pragma unroll 1
-                for (int t = 0; t < n && !gone_all(); ++t) {
-                    if (t >= late) {
-                        add(0, t, 0);
-                        if (t + 1 < n)
-                            score(0, t + 1, 0);
-                    }
-                    if (pair) {
-                        add(1, t, 1);
-                        if (t + 1 < n)
-                            score(1, t + 1, 1);
-                    }
+            for (int t = 0; t < n && !gone_all(); ++t) {
+                // where P is apart, the next S may come first
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x ? !pair : t < late)
+                        continue;
+                    if (APART && t + 1 < n)
+                        score(x, t + 1);
+                    add(x, t);
+                    if (!APART && t + 1 < n)
+                        score(x, t + 1);
+                }
+                if (!APART)                                // V: behind B's next S (measured: before it, grouped prompts 5% slower)
                     release(at + 2u * (uint32_t)t + 1u);
-                }
-            } else {
-                // the buffers go round
-                int sb = 0, pb = 0;
-                auto next = [&](int &buf) { const int now = buf; buf = pa_next<BUFS>(buf, 1); return now; };
-                if (pair) {
-                    if (late == 0)
-                        score(0, 0, next(sb));
-                    score(1, 0, next(sb));
-                    if (n > 1)
-                        score(0, 1, next(sb));
-                    if (late == 1)
-                        score(1, 1, next(sb));
-#pragma unroll 1
-                    for (int t = 0; t < n && !gone_all(); ++t) {
-                        if (t >= late) {
-                            add(0, t, next(pb));
-                            if (t + 1 < n)
-                                score(1, t + 1, next(sb));
-                        }
-                        add(1, t, next(pb));
-                        if (t + 2 < n)
-                            score(0, t + 2, next(sb));
-                    }
-                } else {
-                    for (int t = 0; t < BUFS && t < n; ++t)
-                        score(0, t, next(sb));
-#pragma unroll 1
-                    for (int t = 0; t < n && !gone_all(); ++t) {
-                        add(0, t, next(pb));
-                        if (t + BUFS < n)
-                            score(0, t + BUFS, next(sb));
-                    }
-                }
             }
             at += 2u * (uint32_t)n;
         }
