@@ -24,7 +24,7 @@
 //   follows that of the rows' last one without a wait.
 //
 // A masked probability is 0, and 0 times a v that is not finite would be NaN: tiles cut by the
-// mask are looked through for such values (by a warp that does nothing else), and a tile that has one
+// mask are looked through for such values (by the warp that fetches units), and a tile that has one
 // is multiplied by the softmax threads themselves, over the tokens that a row sees.
 #include "layer_ops.h"
 #include "segments.cuh"
@@ -34,7 +34,7 @@
 namespace q4 {
 
 constexpr int PA_ROWS = 128, PA_KEYS = 128;
-constexpr int PA_COPY = 8, PA_MMA = 9, PA_NEXT = 10, PA_WARPS = 12;          // (warp 11 looks through V)
+constexpr int PA_COPY = 8, PA_MMA = 9, PA_NEXT = 10, PA_ADD = 11, PA_WARPS = 12;
 constexpr int PA_QUEUE = 2;                // units that a CTA has been given and not begun
 constexpr float PA_SUM_TOP = 0x1p20f;
 
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     constexpr uint32_t IDESC_S = (1u << 4) | BF16 | ((uint32_t)(PA_KEYS >> 3) << 17) | (8u << 24);
     constexpr uint32_t IDESC_O = (1u << 4) | BF16 | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 8 + 4 * HALVES + 2 * PA_QUEUE + 1 + NS];
+    __shared__ uint64_t s_bar[2 * NS + 9 + 4 * HALVES + 2 * PA_QUEUE + 1 + NS];
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) uint4 s_answer;
     __shared__ PaUnit s_unit[PA_QUEUE];
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
     const uint32_t kv_full = smem_u32(s_bar), kv_free = kv_full + 8u * NS, q_full = kv_free + 8u * NS,   // q_full: A, B
-                   q_free = q_full + 16, drained = q_full + 24, pv_done = q_full + 32,      // pv_done: by tile and half
+                   q_free = q_full + 16, drained = q_full + 24, pv_done = q_full + 40,      // pv_done: by tile and half
                    s_full = pv_done + 16u * HALVES, s_free = s_full + 16, p_full = s_free + 16,        // by tile (and half)
                    unit_full = p_full + 16u * HALVES, unit_free = unit_full + 8u * PA_QUEUE,
                    answered = unit_free + 8u * PA_QUEUE, v_raw = answered + 8;        // by stage: V that is to be looked through
@@ -176,10 +176,11 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             }
             mbar_init(q_free, 1);
             mbar_init(drained, 1);
+            mbar_init(drained + 8, 1);
             mbar_init(answered, 1);
             for (int i = 0; i < PA_QUEUE; ++i) {
                 mbar_init(unit_full + 8u * i, 1);
-                mbar_init(unit_free + 8u * i, 11);
+                mbar_init(unit_free + 8u * i, APART ? 11 : 10);        // softmax, copies, MMAs
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(q_full + 8u * i, 1);
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 if (loads[x] > 0)
                     mbar_wait(q_full + 8u * x, (loads[x] - 1u) & 1u, p.err);
         }
-    } else if (warp == PA_MMA) {
+    } else if (warp == PA_MMA || (APART && warp == PA_ADD)) {
         // -------------------------------------------------------- MMAs
         // This warp is what the tensor cores wait for, so the two tiles are written out (x is known where it is
         // compiled) and everything that an MMA takes is the warp's: such an MMA takes 30 (PV) and 52 cycles (S) to
@@ -656,98 +657,115 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                     mma_commit(kv_free + 8u * (k & (NS - 1)));
                 __syncwarp();
             };
-            score(0, late);
-            if (pair)
-                score(1, 0);
+            if constexpr (APART) {
+                // S and PV wait for different things: a warp each
+                const bool adds = warp == PA_ADD;
 #pragma unroll 1
-            for (int t = 0; t < n && !gone_all(); ++t) {
-                // where P is apart, the next S may come first
+                for (int t = 0; t < n && !gone_all(); ++t) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (x ? !pair : t < late)
-                        continue;
-                    if (APART && t + 1 < n)
-                        score(x, t + 1);
-                    add(x, t);
-                    if (!APART && t + 1 < n)
-                        score(x, t + 1);
+                    for (int x = 0; x < 2; ++x) {
+                        if (x ? !pair : t < late)
+                            continue;
+                        if (adds)
+                            add(x, t);
+                        else
+                            score(x, t);
+                    }
                 }
-                if (!APART)                                // V: behind B's next S (measured: before it, grouped prompts 5% slower)
-                    release(at + 2u * (uint32_t)t + 1u);
+            } else {
+                score(0, late);
+                if (pair)
+                    score(1, 0);
+#pragma unroll 1
+                for (int t = 0; t < n && !gone_all(); ++t) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (x ? !pair : t < late)
+                            continue;
+                        add(x, t);
+                        if (t + 1 < n)
+                            score(x, t + 1);
+                    }
+                    release(at + 2u * (uint32_t)t + 1u);   // V: behind B's next S (measured: before it, grouped prompts 5% slower)
+                }
             }
             at += 2u * (uint32_t)n;
         }
     } else if (warp == PA_NEXT) {
         // ------------------------------------------------- units to come
         // The grid has a CTA for each unit that there may be, and an SM room for one: a CTA takes over the units of those
-        // that have not begun, so that units of different lengths are dealt out as SMs come free.
+        // that have not begun, so that units of different lengths are dealt out as SMs come free.  The next unit is
+        // fetched before this one's V is looked through.
         bool more = true, wanted = true;
         int asked = 0;
-#pragma unroll 1
-        for (int round = 1; more && !gone_all(); ++round) {
-            const int slot = (round - 1) % PA_QUEUE;
-            if (wanted && round > PA_QUEUE)
-                kv_wait(unit_free + 8u * slot, (uint32_t)((round - 1) / PA_QUEUE - 1) & 1u, dead);
-            if (gone_all())
-                break;
-            if (elect_one())
-                pa_ask(smem_u32(&s_answer), answered);
-            __syncwarp();
-            ++asked;
-            kv_wait(answered, (uint32_t)(asked - 1) & 1u, dead);
-            const int number = pa_answer(smem_u32(&s_answer));
-            fence_proxy_async();                           // (the next answer comes to the same place)
-            more = number >= 0;
-            if (wanted) {
-                if (!more || !walk.find(number, u)) {
-                    // CTAs behind the last unit have nothing to do: they are taken over too, and that is all
-                    wanted = false;
-                    u.na = 0;
-                }
-                if (lane == 0) {
-                    const uint32_t to = smem_u32(&s_unit[slot]);
-                    sts128(to, (uint32_t)u.start, (uint32_t)u.len, (uint32_t)u.first, (uint32_t)u.head);
-                    sts128(to + 16u, (uint32_t)u.na, (uint32_t)u.nb, 0u, 0u);
-                    mbar_arrive(unit_full + 8u * slot);
-                }
-            }
-            __syncwarp();
-        }
-        if (gone_all() && asked > 0)
-            mbar_wait(answered, (uint32_t)(asked - 1) & 1u, p.err);
-    } else {
-        // ------------ values that are not finite in tiles of V that the mask cuts
         uint32_t at = 0u, uses = 0u;                       // copies before this unit, parities of v_raw
+        PaUnit now = u;
 #pragma unroll 1
-        for (int round = 0; unit(round) && !gone_all(); ++round) {
-            const int n = u.nb > 0 ? u.nb : u.na, cut = n - (u.first + 1) / PA_KEYS;
-#pragma unroll 1
-            for (int t = 0; t < cut && !gone_all(); ++t) {
-                const uint32_t stage = (at + 2u * (uint32_t)t + 1u) & (NS - 1), v = sm + L::RING + stage * L::TILE;
-                kv_wait(v_raw + 8u * stage, (uses >> stage) & 1u, dead);
-                uses ^= 1u << stage;
-                uint32_t bad = 0u;
-#pragma unroll 8
-                for (uint32_t c = (uint32_t)lane * 16u; c < L::TILE; c += 512u) {
-                    const uint4 e = lds128(v + c);
-                    bad |= ((e.x & 0x7f807f80u) + 0x00800080u) | ((e.y & 0x7f807f80u) + 0x00800080u) |
-                           ((e.z & 0x7f807f80u) + 0x00800080u) | ((e.w & 0x7f807f80u) + 0x00800080u);
-                }
-                const bool any = __any_sync(0xffffffffu, (bad & 0x80008000u) != 0u);
-                if (lane == 0) {
-                    *(volatile int *)&s_bad[stage] = any;
-                    mbar_arrive(kv_full + 8u * stage);
+        for (int round = 1; (more || now.na > 0) && !gone_all(); ++round) {
+            u.na = 0;
+            if (more) {
+                const int slot = (round - 1) % PA_QUEUE;
+                if (wanted && round > PA_QUEUE)
+                    kv_wait(unit_free + 8u * slot, (uint32_t)((round - 1) / PA_QUEUE - 1) & 1u, dead);
+                if (gone_all())
+                    break;
+                if (elect_one())
+                    pa_ask(smem_u32(&s_answer), answered);
+                __syncwarp();
+                ++asked;
+                kv_wait(answered, (uint32_t)(asked - 1) & 1u, dead);
+                const int number = pa_answer(smem_u32(&s_answer));
+                fence_proxy_async();                       // (the next answer comes to the same place)
+                more = number >= 0;
+                if (wanted) {
+                    if (!more || !walk.find(number, u)) {
+                        // CTAs behind the last unit have nothing to do: they are taken over too, and that is all
+                        wanted = false;
+                        u.na = 0;
+                    }
+                    if (lane == 0) {
+                        const uint32_t to = smem_u32(&s_unit[slot]);
+                        sts128(to, (uint32_t)u.start, (uint32_t)u.len, (uint32_t)u.first, (uint32_t)u.head);
+                        sts128(to + 16u, (uint32_t)u.na, (uint32_t)u.nb, 0u, 0u);
+                        mbar_arrive(unit_full + 8u * slot);
+                    }
                 }
                 __syncwarp();
             }
-            at += 2u * (uint32_t)n;
+            if (now.na > 0) {
+                // values that are not finite in tiles of V that the mask cuts
+                const int n = now.nb > 0 ? now.nb : now.na, cut = n - (now.first + 1) / PA_KEYS;
+#pragma unroll 1
+                for (int t = 0; t < cut && !gone_all(); ++t) {
+                    const uint32_t stage = (at + 2u * (uint32_t)t + 1u) & (NS - 1), v = sm + L::RING + stage * L::TILE;
+                    kv_wait(v_raw + 8u * stage, (uses >> stage) & 1u, dead);
+                    uses ^= 1u << stage;
+                    uint32_t bad = 0u;
+#pragma unroll 8
+                    for (uint32_t c = (uint32_t)lane * 16u; c < L::TILE; c += 512u) {
+                        const uint4 e = lds128(v + c);
+                        bad |= ((e.x & 0x7f807f80u) + 0x00800080u) | ((e.y & 0x7f807f80u) + 0x00800080u) |
+                               ((e.z & 0x7f807f80u) + 0x00800080u) | ((e.w & 0x7f807f80u) + 0x00800080u);
+                    }
+                    const bool any = __any_sync(0xffffffffu, (bad & 0x80008000u) != 0u);
+                    if (lane == 0) {
+                        *(volatile int *)&s_bad[stage] = any;
+                        mbar_arrive(kv_full + 8u * stage);
+                    }
+                    __syncwarp();
+                }
+                at += 2u * (uint32_t)n;
+            }
+            now = u;
         }
+        if (gone_all() && asked > 0)
+            mbar_wait(answered, (uint32_t)(asked - 1) & 1u, p.err);
     }
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (*dead.flag != 0 && warp == PA_MMA)
-        kv_mma_drain(drained, dead);
+    if (*dead.flag != 0 && (warp == PA_MMA || (APART && warp == PA_ADD)))
+        kv_mma_drain(drained + (warp == PA_ADD ? 8u : 0u), dead);
     __syncthreads();
     if (warp == PA_MMA) {
         tc_fence_after();
