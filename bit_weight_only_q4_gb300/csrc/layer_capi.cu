@@ -1,6 +1,6 @@
 // C ABI of the operators around a layer's projections (include/q4.h): host-side validation,
-// then the launches of norm_rope.cu, prompt_attention.cu, lora_few.cu and
-// lora_many.cu.
+// then the launches of norm_rope.cu, prompt_attention.cu, lora_few.cu,
+// lora_shared.cu and lora_many.cu.
 #include "layer_ops.h"
 
 namespace q4 {
@@ -151,6 +151,8 @@ q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b,
     const int64_t tiles = tokens / 8 + batch / 2;
     const bool few = tokens <= 8 * (int64_t)batch ||
                      (tiles <= dev.sms / 2 && tiles * 2 * rank * ((int64_t)N + K) <= 32 << 20);
+    if (few && lora_shared_eligible(p))
+        return launch_lora_shared(p, static_cast<cudaStream_t>(stream), pdl_on());
     return few ? launch_lora_few(p, static_cast<cudaStream_t>(stream), pdl_on())
                : launch_lora_many(dev, p, static_cast<cudaStream_t>(stream), pdl_on());
 }

@@ -34,7 +34,7 @@ struct PromptArgs {
 };
 q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, bool pdl);
 
-// ---- lora_few.cu, lora_many.cu
+// ---- lora_few.cu, lora_shared.cu, lora_many.cu
 struct LoraArgs {
     const uint16_t *x, *a, *b, *base;
     uint16_t *out;
@@ -45,6 +45,8 @@ struct LoraArgs {
     unsigned *err;
 };
 q4_status launch_lora_few(const LoraArgs &a, cudaStream_t st, bool pdl);
+bool lora_shared_eligible(const LoraArgs &a);
+q4_status launch_lora_shared(const LoraArgs &a, cudaStream_t st, bool pdl);
 q4_status launch_lora_many(const DeviceInfo &dev, const LoraArgs &a, cudaStream_t st, bool pdl);
 
 }  // namespace q4

@@ -50,6 +50,14 @@ __device__ __forceinline__ float4 lr_load(uint32_t cluster_address)
 // First of n things that CTA `rank` of `size` has, when they are shared out evenly.
 __device__ __forceinline__ int lr_share(int n, uint32_t rank, uint32_t size) { return (int)((int64_t)n * rank / size); }
 
+// One warp's MMA, for tiles of a few tokens (see lora_few.cu).
+__device__ __forceinline__ void lr_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // The tile of tokens that a cluster works on; false: none.
 struct LoraTile {
     int row, rows, adapter;                // adapter < 0: base as it is

@@ -15,13 +15,6 @@ namespace q4 {
 
 constexpr int LF_TOKENS = 8, LF_WARPS = 8;
 
-__device__ __forceinline__ void lf_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // STEPS: 16s of rank values, rounded up to a power of two.  Four CTAs an SM up to rank 64 (64 registers): 64 requests of
 // 5 tokens, 512 CTAs, are one wave then (14.9 us; with 76 registers 20.3).
 template <int STEPS>
@@ -70,8 +63,8 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
             }
 #pragma unroll
             for (int m = 0; m < STEPS; ++m) {
-                lf_mma(c[m], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, b.x, b.y);
-                lf_mma(c[m], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, b.z, b.w);
+                lr_mma(c[m], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, b.x, b.y);
+                lr_mma(c[m], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, b.z, b.w);
             }
         }
 #pragma unroll
@@ -145,7 +138,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
         float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
-            lf_mma(c, now.b[0][s].x, now.b[1][s].x, now.b[0][s].y, now.b[1][s].y, tt[s].x, tt[s].y);
+            lr_mma(c, now.b[0][s].x, now.b[1][s].x, now.b[0][s].y, now.b[1][s].y, tt[s].x, tt[s].y);
         const int n = 16 * group + 2 * g;
 #pragma unroll
         for (int i = 0; i < 2; ++i)

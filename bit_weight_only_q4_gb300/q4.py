@@ -651,6 +651,7 @@ def q4_kv_attention_shared(q, cache, prefix_pages, prefix_len, page_table, lengt
 # The checks of these calls are kept by shape and stride as those of the cache's are; types,
 # devices and contiguity are looked at in every call.
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_BF16, _F32, _I32, _CONTIGUOUS = torch.bfloat16, torch.float32, torch.int32, torch.contiguous_format
 
 
 def _here(device, **tensors):
@@ -665,9 +666,9 @@ def _here(device, **tensors):
 def _empty_rows(like, stream):
     """A contiguous result of the shape and type of `like`."""
     if stream is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return torch.empty_like(like, memory_format=_CONTIGUOUS)
     with _on(stream):
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return torch.empty_like(like, memory_format=_CONTIGUOUS)
 
 
 def _vector(t, name, n, dtype):
@@ -706,15 +707,15 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     D]; weights bf16 [D], or None for no norm), then the rotation of their first 2 * len(inv_freq)
     columns by positions * inv_freq (int32 [batch * tokens], fp32; both None: no rotation), in adjacent
     pairs or halves.  k may be None.  q_out=q and k_out=k work in place."""
-    bf16, dev = torch.bfloat16, q.get_device()
+    dev = q.get_device()
     key = (q.shape, q.stride(), k is None or k.shape, k is None or k.stride(), positions is None or positions.shape,
            inv_freq is None or inv_freq.shape, q_weight is None or q_weight.shape, k_weight is None or k_weight.shape)
     plan = _kv_plans.get(key)
-    if not (plan is not None and q.dtype is bf16 and (k is None or k.dtype is bf16) and
-            (positions is None or (positions.dtype is torch.int32 and positions.is_contiguous() and
-                                   inv_freq.dtype is torch.float32 and inv_freq.is_contiguous())) and
-            (q_weight is None or (q_weight.dtype is bf16 and q_weight.is_contiguous())) and
-            (k_weight is None or (k_weight.dtype is bf16 and k_weight.is_contiguous()))):
+    if not (plan is not None and q.dtype is _BF16 and (k is None or k.dtype is _BF16) and
+            (positions is None or (positions.dtype is _I32 and positions.is_contiguous() and
+                                   inv_freq.dtype is _F32 and inv_freq.is_contiguous())) and
+            (q_weight is None or (q_weight.dtype is _BF16 and q_weight.is_contiguous())) and
+            (k_weight is None or (k_weight.dtype is _BF16 and k_weight.is_contiguous()))):
         plan = _norm_rope_plan(key, q, k, q_weight, k_weight, positions, inv_freq)
     tokens, Hq, H, D, qs, ks, qos, kos, rotary = plan
     if not (dev == _device() and (k is None or k.get_device() == dev) and
@@ -724,7 +725,7 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
         _here(dev, q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq, q_out=q_out,
               k_out=k_out)
     if q_out is None:
-        q_out = _empty_rows(q, stream)
+        q_out = torch.empty_like(q, memory_format=_CONTIGUOUS) if stream is None else _empty_rows(q, stream)
     elif q_out.shape != q.shape:
         raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
     else:
@@ -732,7 +733,7 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = _empty_rows(k, stream)
+        k_out = torch.empty_like(k, memory_format=_CONTIGUOUS) if stream is None else _empty_rows(k, stream)
     elif k_out.shape != k.shape:
         raise ValueError(f"k_out must be {tuple(k.shape)}, got {tuple(k_out.shape)}")
     else:
@@ -744,7 +745,7 @@ def q4_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
         None if k is None else k.data_ptr(), ks, None if k_weight is None else k_weight.data_ptr(),
         None if k is None else k_out.data_ptr(), kos, H, None if positions is None else positions.data_ptr(),
         None if inv_freq is None else inv_freq.data_ptr(), rotary, 1 if interleaved else 0, eps, tokens, D,
-        _kv_stream(stream, q))
+        _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     if status:
         _check(status)
     return q_out, k_out
@@ -769,9 +770,9 @@ def q4_prompt_attention(q, k, v, offsets, scale=None, out=None, stream=None):
     (bf16 [tokens, kv_heads, D]).  scale: D ** -0.5 if None.  Rows of no sequence are not written."""
     key = q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), offsets.shape
     plan = _kv_plans.get(key)
-    bf16, dev = torch.bfloat16, q.get_device()
-    if (plan is None or q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or
-            offsets.dtype is not torch.int32 or not offsets.is_contiguous()):
+    dev = q.get_device()
+    if (plan is None or q.dtype is not _BF16 or k.dtype is not _BF16 or v.dtype is not _BF16 or
+            offsets.dtype is not _I32 or not offsets.is_contiguous()):
         plan = _prompt_plan(key, q, k, v, offsets)
     N, B, Hq, H, D, qs, ks, vs, s = plan
     if not (k.get_device() == v.get_device() == offsets.get_device() == dev == _device() and
@@ -786,7 +787,7 @@ def q4_prompt_attention(q, k, v, offsets, scale=None, out=None, stream=None):
     if scale is not None:
         s = float(scale)
     status = (_lib or load()).q4_prompt_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, offsets.data_ptr(),
-                                                  B, N, Hq, H, D, s, out.data_ptr(), _kv_stream(stream, q))
+                                                  B, N, Hq, H, D, s, out.data_ptr(), _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     if status:
         _check(status)
     return out
@@ -826,9 +827,9 @@ def q4_lora(x, a, b, scales, offsets, ids, base, out=None, stream=None):
     written."""
     key = x.shape, x.stride(), a.shape, b.shape, scales.shape, offsets.shape, ids.shape, base.shape, base.stride()
     plan = _kv_plans.get(key)
-    bf16, i32, dev = torch.bfloat16, torch.int32, x.get_device()
-    if (plan is None or x.dtype is not bf16 or a.dtype is not bf16 or b.dtype is not bf16 or base.dtype is not bf16 or
-            offsets.dtype is not i32 or ids.dtype is not i32 or scales.dtype is not torch.float32 or not
+    dev = x.get_device()
+    if (plan is None or x.dtype is not _BF16 or a.dtype is not _BF16 or b.dtype is not _BF16 or base.dtype is not _BF16 or
+            offsets.dtype is not _I32 or ids.dtype is not _I32 or scales.dtype is not _F32 or not
             (a.is_contiguous() and b.is_contiguous() and offsets.is_contiguous() and ids.is_contiguous() and
              scales.is_contiguous())):
         plan = _lora_plan(key, x, a, b, scales, offsets, ids, base)
@@ -846,7 +847,7 @@ def q4_lora(x, a, b, scales, offsets, ids, base, out=None, stream=None):
         return out
     status = (_lib or load()).q4_lora(x.data_ptr(), xs, a.data_ptr(), b.data_ptr(), scales.data_ptr(), n, r,
                                       offsets.data_ptr(), ids.data_ptr(), B, base.data_ptr(), bs, out.data_ptr(), os_, M, N,
-                                      K, _kv_stream(stream, x))
+                                      K, _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     if status:
         _check(status)
     return out

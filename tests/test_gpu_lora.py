@@ -67,6 +67,55 @@ def test_requests_and_ranks(lens, ids, rank):
     case.check(case())
 
 
+@pytest.mark.parametrize("rank", [8, 16, 40, 64, 72, 128])
+@pytest.mark.parametrize("spare", [0, 200])
+def test_requests_that_share_adapters_and_adapters_to_spare(spare, rank):
+    """Few tokens each: tiles by adapter where requests share them, and by request where there are as many adapters."""
+    gen = torch.Generator().manual_seed(7)
+    lens = torch.randint(0, 9, (200,), generator=gen).tolist()
+    ids = torch.randint(-1, 6, (200,), generator=gen).tolist()
+    case = Case(lens, ids, 264, 392, rank, adapters=6 + spare, gap=5)
+    out = torch.full_like(case.base, 5.0)
+    case.check(case(out=out))
+    assert (out[:5] == 5).all() and (out[-5:] == 5).all()
+    got = case(base=(base := case.base.clone()), out=base)
+    assert torch.equal(got[5:-5], out[5:-5]) and torch.equal(got[:5], case.base[:5]) and torch.equal(got[-5:], case.base[-5:])
+    # one adapter for all, and none for any
+    for ids in ([3] * 200, [-1] * 200):
+        case.id_list = ids
+        case.check(case(ids=torch.tensor(ids, dtype=torch.int32, device="cuda")))
+
+
+@pytest.mark.parametrize("adapters", [2, 200])
+def test_few_tokens_with_offsets_and_ids_that_are_none(adapters):
+    q4.device_error_flags()
+    case = Case([3] * 40, [b % 2 for b in range(40)], 128, 256, 16, adapters=adapters)
+    o = case.offsets.clone()
+    o[10], o[20], o[40] = 5, 1000, 118                      # 10 falls back, 20 is past the end, 40 ends early
+    ids = case.ids.clone()
+    ids[3] = adapters
+    out = torch.full_like(case.base, 5.0)
+    case(offsets=o, ids=ids, out=out)
+    assert q4.device_error_flags() == 4
+    # request 9 ends before it begins; 10 begins before 9 in front of it does not end ... what is left is in order
+    spans = []
+    floor, at = 0, o.tolist()
+    for b, (lo, hi) in enumerate(zip(at, at[1:])):
+        lo, hi = min(max(lo, 0), 120), min(max(hi, 0), 120)
+        if hi >= lo and lo >= floor:
+            spans.append((lo, hi, -1 if b == 3 else b % 2))
+        floor = max(floor, hi)
+    case.at, case.id_list = [0], []
+    ref, tol = case.base.double().clone(), torch.full(case.base.shape, 0.0, dtype=torch.float64, device="cuda")
+    seen = torch.zeros(120, dtype=torch.bool, device="cuda")
+    for lo, hi, i in spans:
+        case.at, case.id_list = [lo, hi], [i]
+        a, b = case.want()
+        ref[lo:hi], tol[lo:hi] = a[lo:hi], b[lo:hi]
+        seen[lo:hi] = True
+    assert ((out[seen].double() - ref[seen]).abs() <= tol[seen]).all() and (out[~seen] == 5).all()
+
+
 @pytest.mark.parametrize("K,N", [(8, 8), (16, 520), (72, 8), (136, 264), (1000, 72), (2048, 2048), (8192, 1048), (776, 2584)])
 @pytest.mark.parametrize("lens,ids", [FEW[3], MANY[3]], ids=str)
 def test_sizes(lens, ids, K, N):
