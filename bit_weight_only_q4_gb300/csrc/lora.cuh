@@ -58,6 +58,9 @@ __device__ __forceinline__ void lr_mma(float (&c)[4], uint32_t a0, uint32_t a1, 
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// How many of n things dealt round `size` CTAs fall to CTA `rank`.
+__device__ __forceinline__ int lr_round(int n, uint32_t rank, uint32_t size) { return (n - (int)rank + (int)size - 1) / (int)size; }
+
 // The tile of tokens that a cluster works on; false: none.
 struct LoraTile {
     int row, rows, adapter;                // adapter < 0: base as it is

@@ -111,8 +111,9 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
     const KvDead dead = {p.err, dead_flag, smem_u32(const_cast<int *>(dead_flag))};
     auto gone_all = [&]() { return __any_sync(0xffffffffu, *dead.flag != 0); };
     const int ranks = (p.rank + 15) / 16 * 16;
-    const int k0 = lr_share((p.K + 63) / 64, rank, size), nk = lr_share((p.K + 63) / 64, rank + 1, size) - k0;
-    const int n0 = lr_share((p.N + 63) / 64, rank, size), nn = lr_share((p.N + 63) / 64, rank + 1, size) - n0;
+    // Pieces of 64 columns go round the cluster, so that its CTAs are in the same DRAM pages at a time.
+    const int nk = lr_round((p.K + 63) / 64, rank, size), nn = lr_round((p.N + 63) / 64, rank, size);
+    auto slice = [&](int i) { return (int)rank + i * (int)size; };
     const int groups = (tile.rows + 31) / 32;              // of 32 rows
 
     if (warp < 8) {
@@ -241,13 +242,13 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
                 __syncwarp();
                 if (lane == 0) {
                     if (ok) {
-                        tma_store_2d(&out_map, (n0 + q) * LM_COLS, tile.row + quad * 32, sm + s * L::SLOT + (uint32_t)quad * 4096u);
+                        tma_store_2d(&out_map, slice(q) * LM_COLS, tile.row + quad * 32, sm + s * L::SLOT + (uint32_t)quad * 4096u);
                         asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
                     mbar_arrive(base_free + 8u * s);
                 }
             } else {
-                const int piece = lane & 7, n = (n0 + q) * LM_COLS + 8 * piece;
+                const int piece = lane & 7, n = slice(q) * LM_COLS + 8 * piece;
                 if (ok && n < p.N) {
 #pragma unroll 1
                     for (int r = lane >> 3; r < last; r += 4) {
@@ -279,8 +280,8 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
             if (elect_one()) {
                 mbar_arrive_expect_tx(x_full + 8u * s, (uint32_t)(groups * 4096 + ranks * 128));
                 for (int g = 0; g < groups; ++g)
-                    tma_load_2d(sm + s * L::SLOT + 4096u * g, &x_map, 64 * (k0 + i), tile.row + 32 * g, x_full + 8u * s);
-                tma_load_3d(sm + L::A + s * L::W_SLOT, &a_map, 64 * (k0 + i), 0, tile.adapter, x_full + 8u * s);
+                    tma_load_2d(sm + s * L::SLOT + 4096u * g, &x_map, 64 * slice(i), tile.row + 32 * g, x_full + 8u * s);
+                tma_load_3d(sm + L::A + s * L::W_SLOT, &a_map, 64 * slice(i), 0, tile.adapter, x_full + 8u * s);
             }
             __syncwarp();
             ++xs;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
             if (elect_one()) {
                 mbar_arrive_expect_tx(base_full + 8u * s, (uint32_t)groups * 4096u);
                 for (int g = 0; g < groups; ++g)
-                    tma_load_2d(sm + s * L::SLOT + 4096u * g, &base_map, (n0 + bs) * LM_COLS, tile.row + 32 * g, base_full + 8u * s);
+                    tma_load_2d(sm + s * L::SLOT + 4096u * g, &base_map, slice(bs) * LM_COLS, tile.row + 32 * g, base_full + 8u * s);
             }
             __syncwarp();
             ++bs;
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
                 mbar_arrive_expect_tx(w_full + 8u * s, L::W_SLOT);
 #pragma unroll
                 for (int h = 0; h < (WIDE ? 2 : 1); ++h)
-                    tma_load_3d(sm + L::W + s * L::W_SLOT + 8192u * h, &b_map, 64 * h, (n0 + ws) * LM_COLS, tile.adapter,
+                    tma_load_3d(sm + L::W + s * L::W_SLOT + 8192u * h, &b_map, 64 * h, slice(ws) * LM_COLS, tile.adapter,
                                 w_full + 8u * s);
             }
             __syncwarp();
