@@ -1,16 +1,18 @@
 // Adapters for requests of many tokens (see lora.cuh): tiles of up to 128 tokens on tcgen05.
 //
 //     t [128 x rank] = x [128 x K] A^T,     out [128 x 64] = base + scale (t [128 x rank] B [64 x rank]^T)
-// with tokens as the MMA's M.  Ten warps: eight with the exchange of t and the results, one that copies
-// (TMA), one that issues the MMAs.  A CTA's share of K comes first, through a ring of x and A tiles of 64
-// columns.  The sums go from tensor memory to shared memory; each CTA of the cluster adds up its share of
+// with tokens as the MMA's M.  Eleven warps: eight with the exchange of t and the results, one that copies x, A and base
+// (TMA), one that copies B and one that issues the MMAs.  A CTA's share of K comes first, through a ring of x and A
+// tiles of 64 columns.  The sums go from tensor memory to shared memory; each CTA of the cluster adds up its share of
 // the rows of all and writes them, as bf16, into the second product's operand of all.  Then come the
 // CTA's output columns, 64 at a time: base and B through rings, base + product in place, and out by TMA from there,
 // or, where a warp's 32 rows are not all the tile's, with plain stores (the next rows are
 // another request's).  The two groups of four warps take the pieces of 64 columns in turn.
 //
 // What bounds it: HBM, 2 bytes of x, and 4 of base and out, a value.  Two CTAs share an SM (112 KB each), so that the
-// beginning of one runs beside the columns of another.
+// beginning of one runs beside the columns of another.  Measured: 31,500 tokens, 8192 -> 2048, rank 128, 198 us, 5.7 TB/s
+// (84% of a copy's rate; the exchange of t and the last wave are the rest); 8,000 tokens in 79 tiles, 2048 -> 8192,
+// rank 32, 63 us, 5.6 TB/s, one wave, whose first 10 us store nothing.
 #include "lora.cuh"
 #include "tma.h"
 
@@ -130,55 +132,41 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
             kv_wait(t_full, 0u, dead);
             tc_fence_after();
         }
-        if (size == 1) {
+        const uint32_t key = ranks % 32 == 0 ? (uint32_t)row & 7u : (uint32_t)(row >> 1) & 3u;
 #pragma unroll 1
-            for (int c = side * (ranks / 2); c < (side + 1) * (ranks / 2); c += 8) {
-                uint32_t v[8], e[4];
+        for (int c = side * (ranks / 2); c < (side + 1) * (ranks / 2); c += 8) {
+            uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            if (nk > 0)
                 tmem_ld8(t_lane + c, v);
-                // (columns behind the rank meet zeros of B, and are to be some)
+            const uint32_t at = sm + L::SUMS + (uint32_t)(row * ranks * 4);
+            sts128(at + ((((uint32_t)c >> 2) ^ key) << 4), v[0], v[1], v[2], v[3]);
+            sts128(at + ((((uint32_t)(c >> 2) + 1u) ^ key) << 4), v[4], v[5], v[6], v[7]);
+        }
+        tc_fence_before();
+        lr_cluster_arrive();
+        lr_cluster_wait();
+        const int pieces = ranks / 4, part = (LM_ROWS + (int)size - 1) / (int)size;
+        for (int i = tid; i < part * pieces; i += 256) {
+            const int rr = i / pieces, c = i - rr * pieces, r = part * (int)rank + rr;
+            if (r >= tile.rows)                        // (and below 128)
+                break;
+            const uint32_t k = ranks % 32 == 0 ? (uint32_t)r & 7u : (uint32_t)(r >> 1) & 3u;
+            const uint32_t at = sm + L::SUMS + (uint32_t)(r * ranks * 4) + (((uint32_t)c ^ k) << 4);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    e[i] = c < p.rank ? bf16_pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])) : 0u;
-                sts128(t_place(row, c), e[0], e[1], e[2], e[3]);
-            }
-            tc_fence_before();
-        } else {
-            const uint32_t key = ranks % 32 == 0 ? (uint32_t)row & 7u : (uint32_t)(row >> 1) & 3u;
-#pragma unroll 1
-            for (int c = side * (ranks / 2); c < (side + 1) * (ranks / 2); c += 8) {
-                uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                if (nk > 0)
-                    tmem_ld8(t_lane + c, v);
-                const uint32_t at = sm + L::SUMS + (uint32_t)(row * ranks * 4);
-                sts128(at + ((((uint32_t)c >> 2) ^ key) << 4), v[0], v[1], v[2], v[3]);
-                sts128(at + ((((uint32_t)(c >> 2) + 1u) ^ key) << 4), v[4], v[5], v[6], v[7]);
-            }
-            tc_fence_before();
-            lr_cluster_arrive();
-            lr_cluster_wait();
-            const int pieces = ranks / 4, part = LM_ROWS / (int)size;
-            for (int i = tid; i < part * pieces; i += 256) {
-                const int rr = i / pieces, c = i - rr * pieces, r = part * (int)rank + rr;
-                if (r >= tile.rows)
-                    break;
-                const uint32_t k = ranks % 32 == 0 ? (uint32_t)r & 7u : (uint32_t)(r >> 1) & 3u;
-                const uint32_t at = sm + L::SUMS + (uint32_t)(r * ranks * 4) + (((uint32_t)c ^ k) << 4);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (uint32_t j = 0; j < LR_CLUSTER; ++j) {
-                    if (j < size) {
-                        const float4 w = lr_load(lr_map(at, j));
-                        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-                    }
+            for (uint32_t j = 0; j < LR_CLUSTER; ++j) {
+                if (j < size) {
+                    const float4 w = lr_load(lr_map(at, j));
+                    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
                 }
-                const int j = 4 * c;
-                const uint32_t lo = j < p.rank ? bf16_pair(v.x, v.y) : 0u, hi = j < p.rank ? bf16_pair(v.z, v.w) : 0u;
-                const uint32_t to = t_place(r, j);
-#pragma unroll
-                for (uint32_t y = 0; y < LR_CLUSTER; ++y)
-                    if (y < size)
-                        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(lr_map(to, y)), "r"(lo), "r"(hi) : "memory");
             }
+            const int j = 4 * c;
+            const uint32_t lo = j < p.rank ? bf16_pair(v.x, v.y) : 0u, hi = j < p.rank ? bf16_pair(v.z, v.w) : 0u;
+            const uint32_t to = t_place(r, j);
+#pragma unroll
+            for (uint32_t y = 0; y < LR_CLUSTER; ++y)
+                if (y < size)
+                    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(lr_map(to, y)), "r"(lo), "r"(hi) : "memory");
         }
         asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
@@ -300,10 +288,8 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
             kv_wait(t_full, 0u, dead);                     // (x and A have been read)
         for (int i = 0; i < L::BASES_EARLY && i < nn && !gone_all(); ++i)
             ask_base();
-        if (size > 1) {                                    // (every thread passes the same barriers)
-            lr_cluster_arrive();
-            lr_cluster_wait();
-        }
+        lr_cluster_arrive();                               // (every thread passes the same barriers)
+        lr_cluster_wait();
         lr_cluster_arrive();
         lr_cluster_wait();
 #pragma unroll 1
@@ -342,10 +328,8 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
             kv_wait(t_full, 0u, dead);                     // (x and A have been read)
         for (int i = 0; i < L::WEIGHTS_EARLY && i < nn && !gone_all(); ++i)
             ask();
-        if (size > 1) {
-            lr_cluster_arrive();
-            lr_cluster_wait();
-        }
+        lr_cluster_arrive();
+        lr_cluster_wait();
         lr_cluster_arrive();
         lr_cluster_wait();
         if (WIDE)
@@ -381,10 +365,8 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
             }
             __syncwarp();
         }
-        if (size > 1) {                                    // (every thread passes the same barriers)
-            lr_cluster_arrive();
-            lr_cluster_wait();
-        }
+        lr_cluster_arrive();                               // (every thread passes the same barriers)
+        lr_cluster_wait();
         lr_cluster_arrive();
         lr_cluster_wait();
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -445,13 +427,15 @@ static q4_status lm_launch(const DeviceInfo &dev, const LoraArgs &a, cudaStream_
     cudaError_t e = cudaFuncSetAttribute(lora_many_kernel<WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return cuda_fail(e, "cudaFuncSetAttribute(lora_many_kernel)");
-    // At most one part-filled tile a request.  Clusters are as small as leaves two CTAs for every SM: what comes before the
-    // columns takes a CTA some 15,000 cycles, whether they are many or few.
+    // At most one part-filled tile a request.  The cluster is the largest whose CTAs all run at once, two an SM: a CTA
+    // that has to wait for a place costs a second wave.  Measured, 79 tiles, 2048 -> 8192, rank 32: sizes 2 .. 8 take 76.6,
+    // 62.7, 77.8, 74.5, 68.0, 75.2, 75.6 us (3: 237 CTAs of 304); 13 tiles, rank 64: 48, 36, 29, 26, 24, 22.7, 21.4 us.
+    // With more tiles than that two: 248 tiles, rank 128, 199, 213, 205, 227, 227, 243, 241 us, and 282 without clusters.
     int64_t tiles = (int64_t)a.tokens / LM_ROWS + a.batch;
     tiles = tiles < a.tokens ? tiles : a.tokens;
-    int size = 1;
-    while (size < LR_CLUSTER && tiles * size < 2 * (int64_t)dev.sms)
-        size *= 2;
+    int size = 2;
+    while (size < LR_CLUSTER && tiles * (size + 1) <= 2 * (int64_t)dev.sms)
+        ++size;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * size));
     cfg.blockDim = dim3(LM_WARPS * 32);

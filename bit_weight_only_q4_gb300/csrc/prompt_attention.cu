@@ -14,7 +14,7 @@
 // reference raised and what was summed scaled down.  So a tile that is seen whole costs one pass over its scores and no maximum.
 //
 // One CTA per SM, 12 warps: four with the softmax of A (one thread a row), four with that of
-// B, one that copies (TMA), one that issues the MMAs, one that fetches units.  A step is one tile of
+// B, one that copies (TMA), one or two that issue the MMAs, one that fetches units.  A step is one tile of
 // rows on one tile of keys; A and B take turns, so that the tensor cores work on one while the
 // other is in its softmax.
 //   Heads of 128: two S and two O fill the tensor memory, and P takes the place of its S, whose MMA for the next step
@@ -26,6 +26,13 @@
 // A masked probability is 0, and 0 times a v that is not finite would be NaN: tiles cut by the
 // mask are looked through for such values (by the warp that fetches units), and a tile that has one
 // is multiplied by the softmax threads themselves, over the tokens that a row sees.
+//
+// What bounds it.  Heads of 128, 32 on 8: the tensor cores, whose pipe is busy for 76% of the SMs' time: 7 prompts of 333
+// to 8,191 tokens 1,050 us, 1,730 TFLOP/s of what the mask leaves (89% of a large library product's rate); one of 32,768
+// 5,200 us, 1,700 TFLOP/s under the power limit.  The rest is tiles that the mask cuts, and a unit's beginning and end, some
+// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 182 us, 870 TFLOP/s.
+// Heads of 64: half the products for as many exponentials, so 2^x (4 cycles a warp and scheduler) and what is about it: 3
+// prompts of 5,000 to 16,383 tokens, 28 on 4 heads, 1,330 us, 1,140 TFLOP/s.  5 of at most 77 tokens: 6 us, latency.
 #include "layer_ops.h"
 #include "segments.cuh"
 #include "tc_device.cuh"

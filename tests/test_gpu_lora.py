@@ -67,6 +67,15 @@ def test_requests_and_ranks(lens, ids, rank):
     case.check(case())
 
 
+@pytest.mark.parametrize("rank", [16, 72])
+@pytest.mark.parametrize("tiles", [1, 41, 48, 58, 70, 90, 120, 160])
+def test_clusters_of_every_size(tiles, rank):
+    """From eight CTAs for a tile to two, as tiles become more; pieces of K and N that do not share out evenly."""
+    lens = [128 * (tiles // 2) + 100, 0, 128 * (tiles - tiles // 2) - 128 + 61]
+    case = Case(lens, [1, 0, 0], 328, 840, rank)
+    case.check(case())
+
+
 @pytest.mark.parametrize("rank", [8, 16, 40, 64, 72, 128])
 @pytest.mark.parametrize("spare", [0, 200])
 def test_requests_that_share_adapters_and_adapters_to_spare(spare, rank):

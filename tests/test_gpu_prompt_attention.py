@@ -95,7 +95,7 @@ def test_many_sequences():
     check(q4.q4_prompt_attention(q, k, v, offsets), q, k, v, spans_of(offsets))
 
 
-@pytest.mark.parametrize("Hq,H,D", [(16, 4, 128), (12, 12, 64), (6, 6, 128), (30, 10, 64)])
+@pytest.mark.parametrize("Hq,H,D", [(20, 4, 128), (12, 12, 64), (6, 6, 128), (30, 10, 64)])
 def test_units_of_every_kind_in_turn(Hq, H, D):
     """Several units for each CTA: pairs of tiles, tiles without a partner, one and many tiles of keys."""
     gen = torch.Generator().manual_seed(5)
