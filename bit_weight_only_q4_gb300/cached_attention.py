@@ -29,7 +29,7 @@ class CachedAttention:
 
     turn: norms and rotation of q and k, as q4_norm_rope takes them: (q_weight, k_weight, inv_freq),
     weights None for no norm.  adapters: (of qkv, of out), each (a, b, scales) as q4_lora takes them, or
-    None; calls then name their requests as (offsets, ids)."""
+    None; calls then name their requests as (offsets, ids), and one that names none has the projections alone."""
 
     def __init__(self, qkv, out, q_heads: int, cache: torch.Tensor, fmt: int, head_dim: int, turn=None, adapters=None,
                  eps=1e-6, interleaved=False):

@@ -46,6 +46,8 @@ q4_status q4_norm_rope(const void *q, int64_t q_stride, const void *q_weight, vo
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(q_out, 16) || !aligned_to(k_out, 16) ||
         !aligned_to(q_weight, 16) || !aligned_to(k_weight, 16) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 4))
         return fail(Q4_ERR_ALIGN, "q, k, their outputs and weights must be 16-byte, positions and inv_freq 4-byte aligned");
+    if (q_heads > 0 && kv_heads > 0 && (q_out == k_out || q_out == k || k_out == q))
+        return fail(Q4_ERR_ARG, "q_out and k_out must be apart from each other and from the other's input");
     DeviceInfo dev;
     const q4_status s = current_device(dev);
     if (s != Q4_OK)
@@ -89,6 +91,8 @@ q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, in
         return fail(Q4_ERR_ARG, "scale must be finite");
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 16) || !aligned_to(offsets, 4))
         return fail(Q4_ERR_ALIGN, "q, k, v and out must be 16-byte, offsets 4-byte aligned");
+    if (out == q || out == k || out == v)
+        return fail(Q4_ERR_ARG, "out must be apart from q, k and v");
     DeviceInfo dev;
     const q4_status s = current_device(dev);
     if (s != Q4_OK)
@@ -128,6 +132,8 @@ q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b,
     if (!aligned_to(x, 16) || !aligned_to(a, 16) || !aligned_to(b, 16) || !aligned_to(base, 16) || !aligned_to(out, 16) ||
         !aligned_to(scales, 4) || !aligned_to(offsets, 4) || !aligned_to(ids, 4))
         return fail(Q4_ERR_ALIGN, "x, a, b, base and out must be 16-byte, scales, offsets and ids 4-byte aligned");
+    if (out == x || out == a || out == b)
+        return fail(Q4_ERR_ARG, "out must be apart from x, a and b");
     DeviceInfo dev;
     const q4_status s = current_device(dev);
     if (s != Q4_OK)

@@ -1,4 +1,4 @@
-// What the two adapter kernels share: the request that a cluster works on, and clusters.
+// What the adapter kernels share: the tile that a cluster works on, and clusters.
 //
 // For token m of a request with adapter a
 //     t = x_m A_a^T  (rank values),   out_m = base_m + scale_a (t B_a^T).

@@ -107,6 +107,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
         }
         reinterpret_cast<float4 *>(s_sum)[i] = v;
     }
+    __syncwarp();
     lr_cluster_arrive();
     lr_cluster_wait();
     for (int i = tid; i < RANKS * LF_TOKENS / 4; i += LF_WARPS * 32) {
@@ -148,6 +149,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
                               fmaf(scale, c[2 + i], __uint_as_float(now.base[i] & 0xffff0000u)));
         now = next;
     }
+    __syncwarp();
     lr_cluster_wait();
 }
 

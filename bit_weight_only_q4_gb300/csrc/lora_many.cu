@@ -245,11 +245,10 @@ __global__ void __launch_bounds__(LM_WARPS * 32, 2)
                         *reinterpret_cast<uint4 *>(p.out + (int64_t)(tile.row + quad * 32 + r) * p.out_stride + n) = v;
                     }
                 }
+                fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) {
-                    fence_proxy_async();
+                if (lane == 0)
                     mbar_arrive(base_free + 8u * s);
-                }
             }
             __syncwarp();
         }

@@ -86,3 +86,114 @@ def test_a_layer_without_any_of_them_is_what_it_was():
     q, k, v = layer.project(x.unsqueeze(0))
     a = q4.q4_prompt_attention(q[0], k, v, offsets)
     assert torch.equal(y, q4.q4_linear_int4g128(a.view(n, -1), *layer.out))
+
+
+def pieces(tokens, seed, far=None):
+    """x, base, q | k | v rows and adapters for `tokens`; far: elements from token to token."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+
+    def rows(n):
+        t = torch.randn(tokens, n, device="cuda", generator=gen).bfloat16()
+        if far is None:
+            return t
+        wide = torch.empty(tokens * far, device="cuda", dtype=torch.bfloat16).view(tokens, far)[:, :n]
+        return wide.copy_(t)
+
+    rand = lambda *shape: torch.randn(*shape, device="cuda", generator=gen)
+    return dict(x=rows(256), base=rows(320), qkv=rows(6 * 128).unflatten(1, (6, 128)),
+                a=(rand(3, 24, 256) / 16).bfloat16(), b=(rand(3, 320, 24) / 5).bfloat16(), scales=1 + 0.1 * rand(3).abs(),
+                w=(1 + 0.1 * rand(128)).bfloat16(), f=10000.0 ** (-torch.arange(64, device="cuda") / 64.0),
+                pos=torch.arange(tokens, device="cuda", dtype=torch.int32))
+
+
+def all_three(p, offsets, ids, in_place=False, stream=None):
+    q, k, v = p["qkv"][:, :4], p["qkv"][:, 4:5], p["qkv"][:, 5:]
+    to = dict(q_out=q, k_out=k) if in_place else {}
+    q, k = q4.q4_norm_rope(q, k, p["w"], p["w"], p["pos"], p["f"], stream=stream, **to)
+    return (q, k, q4.q4_prompt_attention(q, k, v, offsets, stream=stream),
+            q4.q4_lora(p["x"], p["a"], p["b"], p["scales"], offsets, ids, p["base"], out=p["base"] if in_place else None,
+                       stream=stream))
+
+
+def ints(*a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+# requests of many tokens, of a few, of a few that share adapters
+LENS = [([300, 0, 1, 260], [1, -1, 0, 2]), ([7, 9, 8], [0, 1, 2]), ([3] * 12, [0, 1, 2, -1] * 3)]
+
+
+@pytest.mark.parametrize("lens,ids", LENS, ids=str)
+def test_rows_far_apart(lens, ids):
+    """Offsets of more than 2^32 bytes (and, at the first lengths, elements) from the tensors' beginnings."""
+    n = sum(lens)
+    near, far = pieces(n, 5), pieces(n, 5, far=8 * (2**32 // 8 // n + 64) if n > 500 else 8 * (2**31 // 8 // n + 64))
+    offsets = ints(*[sum(lens[:i]) for i in range(len(lens) + 1)])
+    for in_place in (False, True):
+        want, got = all_three(near, offsets, ints(*ids), in_place), all_three(far, offsets, ints(*ids), in_place)
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("lens,ids", LENS, ids=str)
+def test_streams_at_once_and_chained_launches(lens, ids):
+    n = sum(lens)
+    offsets, ids = ints(*[sum(lens[:i]) for i in range(len(lens) + 1)]), ints(*ids)
+    made = [pieces(n, seed) for seed in range(4)]
+    want = [all_three(p, offsets, ids) for p in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(5):
+        got = [all_three(p, offsets, ids, stream=s) for p, s in zip(made, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for a, b in zip(got, want) for g, w in zip(a, b))
+    # launches that begin before the one in front has ended, each reading what that one writes; eager and as a graph
+    p = made[0]
+    fresh = {k: v.clone() for k, v in p.items()}
+
+    def chain():
+        p["base"].copy_(fresh["base"])
+        for _ in range(3):
+            p["qkv"].copy_(fresh["qkv"])
+            out = all_three(p, offsets, ids, in_place=True)
+        return out[2], q4.q4_lora(p["x"], p["a"], p["b"], p["scales"], offsets, ids, p["base"])
+
+    plain = [t.clone() for t in chain()]
+    q4.set_launch_flags(q4.FLAG_PDL)
+    try:
+        early = [t.clone() for t in chain()]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = chain()
+    finally:
+        q4.set_launch_flags(0)
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(early, plain, out))
+
+
+def test_threads():
+    """Calls of several host threads, each on a stream of its own."""
+    from concurrent.futures import ThreadPoolExecutor
+    made = [(pieces(sum(lens), 20 + i), ints(*[sum(lens[:j]) for j in range(len(lens) + 1)]), ints(*ids))
+            for i, (lens, ids) in enumerate(LENS)]
+    want = [all_three(*m) for m in made]
+    torch.cuda.synchronize()
+
+    def work(i):
+        s = torch.cuda.Stream()
+        got = [all_three(*made[i % 3], stream=s) for _ in range(20)][-1]
+        s.synchronize()
+        return all(torch.equal(g, w) for g, w in zip(got, want[i % 3]))
+
+    with ThreadPoolExecutor(6) as pool:
+        assert all(pool.map(work, range(6)))
+
+
+def test_nothing_but_empty_requests():
+    p = pieces(5, 9)
+    for offsets, ids in ((ints(0, 0, 0), ints(0, 1)), (ints(5, 5), ints(2)), (ints(*[3] * 41), ints(*[0, 1] * 20))):
+        out, to = torch.full((5, 4, 128), 3.0, device="cuda").bfloat16(), torch.full((5, 320), 3.0, device="cuda").bfloat16()
+        q4.q4_prompt_attention(p["qkv"][:, :4], p["qkv"][:, 4:5], p["qkv"][:, 5:], offsets, out=out)
+        q4.q4_lora(p["x"], p["a"], p["b"], p["scales"], offsets, ids, p["base"], out=to)
+        assert (out == 3).all() and (to == 3).all()
+    assert q4.device_error_flags() == 0

@@ -80,6 +80,16 @@ def test_lora(lib):
     assert lora(lib, out=FAKE, outs=136) == 5
 
 
+def test_results_over_other_inputs(lib):
+    assert rope(lib, k=2 * FAKE, ko=2 * FAKE, q=FAKE, qo=2 * FAKE) == 5
+    assert rope(lib, k=2 * FAKE, ko=FAKE, q=FAKE, qo=3 * FAKE) == 5
+    assert rope(lib, k=2 * FAKE, ko=3 * FAKE, q=FAKE, qo=3 * FAKE) == 5
+    for name in ("q", "k", "v"):
+        assert prompt(lib, **dict(dict(q=2 * FAKE, k=2 * FAKE, v=2 * FAKE), **{name: FAKE})) == 5
+    for name in ("x", "a", "b"):
+        assert lora(lib, **{name: FAKE + 4096}) == 5
+
+
 def test_host_tensors_are_refused():
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     i32 = lambda n: torch.zeros(n, dtype=torch.int32)      # noqa: E731
