@@ -30,7 +30,7 @@
 // What bounds it.  Heads of 128, 32 on 8: the tensor cores, whose pipe is busy for 76% of the SMs' time: 7 prompts of 333
 // to 8,191 tokens 1,050 us, 1,730 TFLOP/s of what the mask leaves (89% of a large library product's rate); one of 32,768
 // 5,200 us, 1,700 TFLOP/s under the power limit.  The rest is tiles that the mask cuts, and a unit's beginning and end, some
-// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 182 us, 870 TFLOP/s.
+// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 180 us, 880 TFLOP/s.
 // Heads of 64: half the products for as many exponentials, so 2^x (4 cycles a warp and scheduler) and what is about it: 3
 // prompts of 5,000 to 16,383 tokens, 28 on 4 heads, 1,330 us, 1,140 TFLOP/s.  5 of at most 77 tokens: 6 us, latency.
 #include "layer_ops.h"
@@ -115,6 +115,14 @@ __device__ __forceinline__ void pa_exp(const uint32_t (&s)[32], uint32_t *p, f32
         p[i / 2] = bf16_pair(e[0], e[1]);
         p[i / 2 + 1] = bf16_pair(e[2], e[3]);
     }
+}
+
+// 0 v + acc for a pair of bf16: NaN if v is not finite or acc is NaN already, else a zero.
+__device__ __forceinline__ uint32_t pa_fma_bf16(uint32_t v, uint32_t acc)
+{
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0u), "r"(acc));
+    return r;
 }
 
 // Asks for a CTA of the grid that has not begun, to have its work instead: 16 bytes at `to`, counted on `bar`.
@@ -747,14 +755,16 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                     const uint32_t stage = (at + 2u * (uint32_t)t + 1u) & (NS - 1), v = sm + L::RING + stage * L::TILE;
                     kv_wait(v_raw + 8u * stage, (uses >> stage) & 1u, dead);
                     uses ^= 1u << stage;
-                    uint32_t bad = 0u;
+                    uint32_t zero[2] = {0u, 0u};
 #pragma unroll 8
                     for (uint32_t c = (uint32_t)lane * 16u; c < L::TILE; c += 512u) {
                         const uint4 e = lds128(v + c);
-                        bad |= ((e.x & 0x7f807f80u) + 0x00800080u) | ((e.y & 0x7f807f80u) + 0x00800080u) |
-                               ((e.z & 0x7f807f80u) + 0x00800080u) | ((e.w & 0x7f807f80u) + 0x00800080u);
+                        zero[0] = pa_fma_bf16(e.x, zero[0]);
+                        zero[1] = pa_fma_bf16(e.y, zero[1]);
+                        zero[0] = pa_fma_bf16(e.z, zero[0]);
+                        zero[1] = pa_fma_bf16(e.w, zero[1]);
                     }
-                    const bool any = __any_sync(0xffffffffu, (bad & 0x80008000u) != 0u);
+                    const bool any = __any_sync(0xffffffffu, ((zero[0] | zero[1]) & 0x7fff7fffu) != 0u);
                     if (lane == 0) {
                         *(volatile int *)&s_bad[stage] = any;
                         mbar_arrive(kv_full + 8u * stage);
