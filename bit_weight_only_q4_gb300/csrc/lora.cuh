@@ -4,7 +4,8 @@
 //     t = x_m A_a^T  (rank values),   out_m = base_m + scale_a (t B_a^T).
 // A cluster of up to eight CTAs takes a tile of a request's tokens through both products in one launch:
 // each CTA sums t over its share of K, they add their sums up through each other's shared memory, and
-// each then has its share of the output columns.  Sums are fp32; t meets B as bf16, as wide as x and B are.
+// each then has its share of the output columns.  Sums are fp32; t meets B as bf16, as wide as x and B are, and
+// in tiles of a few tokens, where another MMA costs nothing, as two bf16 values, t's and what that leaves.
 #pragma once
 
 #include "layer_ops.h"
@@ -56,6 +57,14 @@ __device__ __forceinline__ void lr_mma(float (&c)[4], uint32_t a0, uint32_t a1, 
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// t as two bf16 values.
+__device__ __forceinline__ void lr_split(float v, uint16_t &most, uint16_t &rest)
+{
+    most = f32_to_bf16_bits(v);
+    const float m = __uint_as_float((uint32_t)most << 16);
+    rest = m - m == 0.f ? f32_to_bf16_bits(v - m) : 0;
 }
 
 // How many of n things dealt round `size` CTAs fall to CTA `rank`.

@@ -8,7 +8,8 @@
 // Output columns lie two to a lane, so that eight lanes store 32 bytes.
 //
 // What bounds it: the chain of offsets, x and A, the exchange, B (48 single tokens, rank 16: 5.4 us), and where tiles
-// share adapters, L2, from which each tile reads its own.
+// share adapters, L2, from which each tile reads its own.  t as two values costs 1 to 4% (64 requests of 5 with an adapter each, rank
+// 64: 18.9 -> 19.6 us) and leaves bf16's rounding of the result as the only one that counts.
 #include "lora.cuh"
 
 namespace q4 {
@@ -23,7 +24,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
     constexpr int RANKS = 16 * STEPS;
     constexpr int PITCH = RANKS + 8;
     __shared__ __align__(16) float s_part[LF_WARPS][RANKS][LF_TOKENS], s_sum[RANKS][LF_TOKENS];
-    __shared__ __align__(16) uint16_t s_t[LF_TOKENS][PITCH];
+    __shared__ __align__(16) uint16_t s_t[2][LF_TOKENS][PITCH];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;                  // MMA: row (or token) and place within it
     const uint32_t rank = lr_rank_in_cluster();
@@ -120,10 +121,10 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
         }
         const int j = i / (LF_TOKENS / 4), m = (i % (LF_TOKENS / 4)) * 4;
         const bool in = j < r;                              // (what lies behind meets zeros, and is to be one)
-        s_t[m][j] = f32_to_bf16_bits(in ? v.x : 0.f);
-        s_t[m + 1][j] = f32_to_bf16_bits(in ? v.y : 0.f);
-        s_t[m + 2][j] = f32_to_bf16_bits(in ? v.z : 0.f);
-        s_t[m + 3][j] = f32_to_bf16_bits(in ? v.w : 0.f);
+        lr_split(in ? v.x : 0.f, s_t[0][m][j], s_t[1][m][j]);
+        lr_split(in ? v.y : 0.f, s_t[0][m + 1][j], s_t[1][m + 1][j]);
+        lr_split(in ? v.z : 0.f, s_t[0][m + 2][j], s_t[1][m + 2][j]);
+        lr_split(in ? v.w : 0.f, s_t[0][m + 3][j], s_t[1][m + 3][j]);
     }
     __syncthreads();
     lr_cluster_arrive();                                    // no CTA leaves while its sums are read
@@ -131,15 +132,18 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
     uint2 tt[STEPS];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
-        tt[s] = *reinterpret_cast<const uint2 *>(&s_t[g][16 * s + 4 * t]);
+        tt[s] = *reinterpret_cast<const uint2 *>(&s_t[0][g][16 * s + 4 * t]);
 #pragma unroll 1
     for (int group = n0 + warp; group < n1; group += LF_WARPS) {
         Group next;
         ask(group + LF_WARPS, next);
         float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
+        for (int s = 0; s < STEPS; ++s) {
+            const uint2 rest = *reinterpret_cast<const uint2 *>(&s_t[1][g][16 * s + 4 * t]);
+            lr_mma(c, now.b[0][s].x, now.b[1][s].x, now.b[0][s].y, now.b[1][s].y, rest.x, rest.y);
             lr_mma(c, now.b[0][s].x, now.b[1][s].x, now.b[0][s].y, now.b[1][s].y, tt[s].x, tt[s].y);
+        }
         const int n = 16 * group + 2 * g;
 #pragma unroll
         for (int i = 0; i < 2; ++i)

@@ -8,7 +8,7 @@
 //
 // What bounds it: latency, of that and of the loads of A; so tiles are small and CTAs many.  Measured, against a tile for
 // each request: 64 requests of 5 tokens on 8 adapters, rank 64, K = 8192, N = 2048, 12.9 against 14.8 us (tiles of 32 tokens:
-// 17.4, of 8: 13.4); 48 single tokens on 4 adapters, rank 16, 4.2 against 5.6, on 24 adapters 5.1 against 5.6; 200 of 2
+// 17.4, of 8: 13.4; all with t as one bf16 value, as two 13.4); 48 single tokens on 4 adapters, rank 16, 4.2 against 5.6, on 24 adapters 5.1 against 5.6; 200 of 2
 // on 20, rank 64, N = 8192, 28 against 51.
 #include "lora.cuh"
 
@@ -48,7 +48,7 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LS_THREADS,
     constexpr int KPARTS = LS_WARPS / STEPS;                // warps that share 16 rank values' columns of K
     constexpr int PITCH = RANKS + 8;
     __shared__ __align__(16) float s_part[KPARTS][RANKS][TOKENS], s_sum[RANKS][TOKENS];
-    __shared__ __align__(16) uint16_t s_t[TOKENS][PITCH];
+    __shared__ __align__(16) uint16_t s_t[2][TOKENS][PITCH];
     __shared__ int s_total[LS_THREADS], s_warp[LS_WARPS], s_top[LS_WARPS], s_row[TOKENS], s_found[2];
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;                  // MMA: row (or token) and place within it
@@ -202,10 +202,10 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LS_THREADS,
         }
         const int j = i / (TOKENS / 4), m = (i % (TOKENS / 4)) * 4;
         const bool in = j < r;                              // (what lies behind meets zeros, and is to be one)
-        s_t[m][j] = f32_to_bf16_bits(in ? v.x : 0.f);
-        s_t[m + 1][j] = f32_to_bf16_bits(in ? v.y : 0.f);
-        s_t[m + 2][j] = f32_to_bf16_bits(in ? v.z : 0.f);
-        s_t[m + 3][j] = f32_to_bf16_bits(in ? v.w : 0.f);
+        lr_split(in ? v.x : 0.f, s_t[0][m][j], s_t[1][m][j]);
+        lr_split(in ? v.y : 0.f, s_t[0][m + 1][j], s_t[1][m + 1][j]);
+        lr_split(in ? v.z : 0.f, s_t[0][m + 2][j], s_t[1][m + 2][j]);
+        lr_split(in ? v.w : 0.f, s_t[0][m + 3][j], s_t[1][m + 3][j]);
     }
     __syncthreads();
     lr_cluster_arrive();                                    // no CTA leaves while its sums are read
@@ -220,7 +220,9 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LS_THREADS,
             float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const uint2 tt = *reinterpret_cast<const uint2 *>(&s_t[8 * i + g][16 * s + 4 * t]);
+                const uint2 tt = *reinterpret_cast<const uint2 *>(&s_t[0][8 * i + g][16 * s + 4 * t]);
+                const uint2 rest = *reinterpret_cast<const uint2 *>(&s_t[1][8 * i + g][16 * s + 4 * t]);
+                lr_mma(c, now.b[0][s].x, now.b[1][s].x, now.b[0][s].y, now.b[1][s].y, rest.x, rest.y);
                 lr_mma(c, now.b[0][s].x, now.b[1][s].x, now.b[0][s].y, now.b[1][s].y, tt.x, tt.y);
             }
 #pragma unroll

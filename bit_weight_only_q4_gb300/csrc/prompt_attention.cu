@@ -92,7 +92,8 @@ struct PaWalk {
 };
 
 // 32 scores of a row to probabilities: ta, tb += 2^(s sl + neg), p <- the same as bf16.  CUT: columns from `at` on
-// past `seen` count as none.
+// past `seen` count as none, and the sum is of the rounded values: where a row sees few tokens, what rounding does to all of
+// its probabilities alike goes away with that.
 template <bool CUT>
 __device__ __forceinline__ void pa_exp(const uint32_t (&s)[32], uint32_t *p, f32x2 sl2, f32x2 neg2, f32x2 &ta, f32x2 &tb,
                                        int at, int seen)
@@ -110,10 +111,15 @@ __device__ __forceinline__ void pa_exp(const uint32_t (&s)[32], uint32_t *p, f32
                 e[y] = at + i + y <= seen ? e[y] : -INFINITY;
             e[y] = ex2(e[y]);
         }
-        ta = add2(ta, pack2(e[0], e[1]));
-        tb = add2(tb, pack2(e[2], e[3]));
         p[i / 2] = bf16_pair(e[0], e[1]);
         p[i / 2 + 1] = bf16_pair(e[2], e[3]);
+        if (CUT) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                e[y] = __uint_as_float(y & 1 ? p[(i + y) / 2] & 0xffff0000u : p[(i + y) / 2] << 16);
+        }
+        ta = add2(ta, pack2(e[0], e[1]));
+        tb = add2(tb, pack2(e[2], e[3]));
     }
 }
 

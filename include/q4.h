@@ -432,7 +432,8 @@ q4_status q4_prompt_attention(const void *q_bf16, int64_t q_stride, const void *
  *             same (in place) or apart from all inputs
  * N and K multiples of 8, rank a multiple of 8 from 8 to 128, strides multiples of 8; x, a, b, base and out
  * 16-byte, scales, offsets and ids 4-byte aligned; at most 2^27 - 1 tokens and requests.  Products are bf16 with
- * fp32 sums; x A^T is rounded to bf16 between them, the result once more.  Uses no workspace.
+ * fp32 sums; x A^T is rounded to bf16 between them (in calls of a few tokens a request to twice its digits), the result once
+ * more.  Uses no workspace.
  */
 q4_status q4_lora(const void *x_bf16, int64_t x_stride, const void *a_bf16, const void *b_bf16, const float *scales,
                   int adapters, int rank, const int32_t *offsets, const int32_t *ids, int batch,
