@@ -30,7 +30,7 @@
 // What bounds it.  Heads of 128, 32 on 8: the tensor cores, whose pipe is busy for 76% of the SMs' time: 7 prompts of 333
 // to 8,191 tokens 1,050 us, 1,730 TFLOP/s of what the mask leaves (89% of a large library product's rate); one of 32,768
 // 5,200 us, 1,700 TFLOP/s under the power limit.  The rest is tiles that the mask cuts, and a unit's beginning and end, some
-// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 180 us, 880 TFLOP/s.
+// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 179 us, 885 TFLOP/s.
 // Heads of 64: half the products for as many exponentials, so 2^x (4 cycles a warp and scheduler) and what is about it: 3
 // prompts of 5,000 to 16,383 tokens, 28 on 4 heads, 1,330 us, 1,140 TFLOP/s.  5 of at most 77 tokens: 6 us, latency.
 #include "layer_ops.h"
@@ -272,8 +272,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
         };
 #pragma unroll 1
         for (int round = 0;; ++round) {
-            const bool have = unit(round);
-            if (bar_or(1 + x, 128, !have || *dead.flag != 0))          // leave together
+            if (!unit(round) || gone_all())
                 break;
             const int n = u.nb > 0 ? u.nb : u.na, mine = x ? u.nb : u.na;
             const int first = u.first + x * p.tile_tokens;
