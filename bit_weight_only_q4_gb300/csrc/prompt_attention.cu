@@ -30,7 +30,7 @@
 // What bounds it.  Heads of 128, 32 on 8: the tensor cores, whose pipe is busy for 76% of the SMs' time: 7 prompts of 333
 // to 8,191 tokens 1,050 us, 1,730 TFLOP/s of what the mask leaves (89% of a large library product's rate); one of 32,768
 // 5,200 us, 1,700 TFLOP/s under the power limit.  The rest is tiles that the mask cuts, and a unit's beginning and end, some
-// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 179 us, 885 TFLOP/s.
+// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 177 us, 895 TFLOP/s.
 // Heads of 64: half the products for as many exponentials, so 2^x (4 cycles a warp and scheduler) and what is about it: 3
 // prompts of 5,000 to 16,383 tokens, 28 on 4 heads, 1,210 us, 1,250 TFLOP/s.  5 of at most 77 tokens: 6 us, latency.
 #include "layer_ops.h"
@@ -393,10 +393,10 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                             tmem_ld32_async(t_s + (uint32_t)at, v);
                             tmem_wait_ld();
                             if (c == 0 && __any_sync(0xffffffffu, token >= 0 && m == -INFINITY)) {
-                                // the first reference: the largest of the first 32 scores that are seen
+                                // the first reference: the largest of the first 16 scores that are seen
                                 float want = -INFINITY;
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
+                                for (int i = 0; i < 16; ++i)
                                     want = at + i <= seen ? fmaxf(want, __uint_as_float(v[i]) * sl) : want;
                                 if (m == -INFINITY)
                                     m = want;
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 // All of the warp's rows are results: by way of its 4 KB of shared memory, 64 columns at a time, and from
                 // there by TMA (whose rows of 128 bytes have piece c at c ^ (row & 7)).
                 const uint32_t st = sm + L::STAGE + (uint32_t)warp * 4096u, st_row = st + (uint32_t)lane * 128u;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D; c += 64) {
                     uint32_t o[2][32];
                     tmem_ld32_async(t_o + c, o[0]);
