@@ -10,8 +10,8 @@
 // another request's).  The two groups of four warps take the pieces of 64 columns in turn.
 //
 // What bounds it: HBM, 2 bytes of x, and 4 of base and out, a value.  Two CTAs share an SM (112 KB each), so that the
-// beginning of one runs beside the columns of another.  Measured: 31,500 tokens, 8192 -> 2048, rank 128, 198 us, 5.7 TB/s
-// (84% of a copy's rate; the exchange of t and the last wave are the rest); 8,000 tokens in 79 tiles, 2048 -> 8192,
+// beginning of one runs beside the columns of another.  Measured: 30,705 tokens, 2048 -> 8192, rank 128, 198 us, 5.7 TB/s
+// (84% of a copy's rate; the exchange of t and the last wave are the rest); 9,446 tokens in 79 tiles, 2048 -> 8192,
 // rank 32, 63 us, 5.6 TB/s, one wave, whose first 10 us store nothing.
 #include "lora.cuh"
 #include "tma.h"

@@ -20,7 +20,7 @@
 // and the bracket's factors are worked out once for a token's queries and once for its keys.
 //
 // What bounds it: HBM, 4 bytes a value (65,000 tokens, 32 and 8 heads of 128: 235 us, 5.7 TB/s), with
-// instruction issue close behind (some 130 for 512 bytes); for a few thousand tokens the issue (8,162 tokens, 36 heads
+// instruction issue close behind (some 130 for 512 bytes); for a few thousand tokens the issue (9,446 tokens, 36 heads
 // of 64: 23 us) and for a step its launch and the chain of loads, fp64 and sincospif (3.3 us).
 #include "layer_ops.h"
 #include "tc_device.cuh"
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 6) norm_rope_kernel(const NormR
 q4_status launch_norm_rope(const DeviceInfo &dev, NormRopeArgs a, int head_dim, cudaStream_t st, bool pdl)
 {
     // A warp takes all heads of a token, or, where that would leave SMs without work, as many as
-    // one batch of loads brings.  Measured: 8,162 tokens of 36 heads of 64, whole 25.1, in batches 29.8 us (the angles are
+    // one batch of loads brings.  Measured: 9,446 tokens of 36 heads of 64, whole 25.1, in batches 29.8 us (the angles are
     // worked out for each); 48 tokens of 32 heads of 128 in CTAs of 4 warps 3.3, of 8 warps 4.2 us.
     const int heads = a.q_heads + a.kv_heads, batch = NR_BATCH * (256 / head_dim);
     a.part_heads = (int64_t)a.tokens >= (int64_t)dev.sms * NR_WARPS * 4 ? heads : batch;
