@@ -35,6 +35,7 @@ __device__ __forceinline__ uint64_t nr_turn(float f)
 {
     double t = (double)f * 0.15915494309189533577;
     t -= floor(t);
+    t = t < 1.0 ? t : 0.0;                 // (a negative t that is next to nothing rounds to a whole turn)
     const double hi = floor(t * 4294967296.0);
     const double lo = (t * 4294967296.0 - hi) * 4294967296.0;
     return ((uint64_t)(uint32_t)hi << 32) + (uint64_t)lo;
