@@ -8,9 +8,9 @@
 // Everything is fp32 from the bf16 values to one rounding of the result.
 //
 // Angles.  u = f / 2 pi mod 1 is kept as a 64-bit fraction of a turn; position * u modulo 2^64 is
-// then the angle, without the whole turns, by one integer product.  The error is that of u (f, 1 /
-// 2 pi and their product in fp64: 2^-53 of u) times the position: below 2^-24 of a turn for every
-// 32-bit position and |f| <= 1.  The top 32 bits go to sincospif.
+// then the angle, without the whole turns, by one integer product.  u comes from integers too: f's 24 bits
+// times 64 of 1 / 2 pi, cut to 64 behind the point, so that it is off by less than 2^-64 + |f| 2^-67, and the angle by
+// 2^31 times that: 2^-24 of a radian at |f| = 256.  The top 32 bits, as fp32 2^-23 at most, go to sincospif.
 //
 // Layout.  A lane holds eight adjacent columns (one 16-byte access), so a warp takes 256 / D
 // heads at a time, and the partner of a pair is a whole lane away: its values come by four
@@ -21,7 +21,7 @@
 //
 // What bounds it: HBM, 4 bytes a value (65,000 tokens, 32 and 8 heads of 128: 235 us, 5.7 TB/s), with
 // instruction issue close behind (some 130 for 512 bytes); for a few thousand tokens the issue (9,446 tokens, 36 heads
-// of 64: 23 us) and for a step its launch and the chain of loads, fp64 and sincospif (3.3 us).
+// of 64: 23 us) and for a step its launch and the chain of loads and sincospif (3.3 us).
 #include "layer_ops.h"
 #include "tc_device.cuh"
 
@@ -30,15 +30,21 @@ namespace q4 {
 constexpr int NR_WARPS = 4;
 constexpr int NR_BATCH = 2;                // passes over the warp whose loads are in flight together
 
-// u of frequency f (see above).
+// u of frequency f (see above): f = m 2^(23 - s) and 2^66 / 2 pi, rounded to 64 bits, have an 88-bit product.
 __device__ __forceinline__ uint64_t nr_turn(float f)
 {
-    double t = (double)f * 0.15915494309189533577;
-    t -= floor(t);
-    t = t < 1.0 ? t : 0.0;                 // (a negative t that is next to nothing rounds to a whole turn)
-    const double hi = floor(t * 4294967296.0);
-    const double lo = (t * 4294967296.0 - hi) * 4294967296.0;
-    return ((uint64_t)(uint32_t)hi << 32) + (uint64_t)lo;
+    const uint32_t bits = __float_as_uint(f), e = bits >> 23 & 0xffu;
+    const uint64_t m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u), c = 0xa2f9836e4e44152aull;
+    const uint64_t lo = m * c, hi = __umul64hi(m, c);
+    const int right = 152 - (int)(e ? e : 1u);
+    uint64_t u;
+    if (right >= 64)
+        u = right < 128 ? hi >> (right - 64) : 0ull;
+    else if (right > 0)
+        u = lo >> right | hi << (64 - right);
+    else
+        u = right > -64 ? lo << -right : 0ull;
+    return bits >> 31 ? 0ull - u : u;
 }
 
 __device__ __forceinline__ f32x2 nr_widen(uint32_t bf16_pair)

@@ -376,8 +376,8 @@ q4_status q4_kv_attention_shared(const void *q_bf16, int64_t q_stride, const uin
  * and of y's first rotary_dim columns the pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
  * interleaved = 1, are turned by the angle positions[token] * inv_freq[i]:
  *     (a, b) -> (a cos - b sin, b cos + a sin).
- * All of it is fp32 from the bf16 inputs to one rounding to bf16; angles are right to 2^-22 for
- * every position and |inv_freq| <= 1 (the error grows with larger ones).
+ * All of it is fp32 from the bf16 inputs to one rounding to bf16; angles are right to 2^-22 of
+ * a radian for every position and |inv_freq| <= 256 (the error grows with larger ones; they are finite).
  *   q, k            bf16; token n, head h, column d at n * stride + h * head_dim + d (strides in
  *                   elements, multiples of 8; parts of a fused q|k|v row work as they are)
  *   q_out, k_out    the same; either in place (the input's pointer and stride) or apart from all inputs

@@ -24,3 +24,54 @@ def test_negative_frequencies_and_those_next_to_zero(interleaved):
     check(a, q, None, pos, f, interleaved)
     backward, _ = q4.q4_norm_rope(q[:-2], None, None, None, -pos[:-2], -f, interleaved=interleaved)
     check(backward, q[:-2], None, -pos[:-2], -f, interleaved)
+
+
+PI = 314159265358979323846264338327950288419716939937510582097494459230781640628620899
+ONE = 10**80                                                 # (PI is pi * ONE)
+
+# frequency, position whose angle is within 2^-20 of whole turns: there bf16 shows the angle's own error
+NEAR_WHOLE_TURNS = [(0.9395782351493835, 2115895823), (0.967883825302124, 2138359862), (0.9996047019958496, 2122168943),
+                    (0.9511218070983887, 2127590030), (0.909855306148529, 2136313893), (0.9218469262123108, 2134484148),
+                    (0.914912223815918, 2140090169), (0.9124369621276855, 2132787872), (0.9825876951217651, 2134200106),
+                    (0.9074194431304932, 2121397446), (0.9759150147438049, 2130958333), (0.9897416234016418, 2114039147)]
+
+
+def angle(f, p):
+    """f p minus the nearest whole turns, by whole numbers; f is a fp32 value."""
+    num, den = float(f).as_integer_ratio()
+    turn = 2 * PI * den
+    rest = num * p * ONE % turn
+    return (rest if 2 * rest < turn else rest - turn) / (den * ONE)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_angles_far_out_are_right_to_2_to_minus_22(sign):
+    """Pairs (0, 1) give (-sin, cos); the sine is rounded once, to 2^-8 of itself."""
+    n = len(NEAR_WHOLE_TURNS)
+    f = torch.tensor([sign * f for f, _ in NEAR_WHOLE_TURNS] + [0.0] * (16 - n), device="cuda")
+    pos = ints(*[p for _, p in NEAR_WHOLE_TURNS])
+    x = torch.zeros(n, 1, 64, device="cuda", dtype=torch.bfloat16)
+    x[:, :, 16:32] = 1
+    y, _ = q4.q4_norm_rope(x, None, None, None, pos, f)
+    for i, (freq, p) in enumerate(NEAR_WHOLE_TURNS):
+        want = angle(sign * freq, p)
+        assert abs(want) < 2.0**-19
+        assert abs(-float(y[i, 0, i]) - want) <= 2.0**-22 + 2.0**-8 * abs(want), (freq, p)
+        assert float(y[i, 0, 16 + i]) == 1
+
+
+def test_frequencies_above_one():
+    """Up to 256 radians a position: whole turns go away exactly."""
+    import math
+
+    f = torch.tensor([1.5, 3.1415927, 10.0, 100.3, 255.9, -7.7, 64.0, 128.5], device="cuda")
+    pos = ints(0, 1, 77, 65537, (1 << 31) - 1, -(1 << 31), 2123456789, -1999999999)
+    x = torch.zeros(len(pos), 1, 64, device="cuda", dtype=torch.bfloat16)
+    x[:, :, 8:16] = 1
+    y, _ = q4.q4_norm_rope(x, None, None, None, pos, f)
+    for i, p in enumerate(pos.tolist()):
+        for j, freq in enumerate(f.tolist()):
+            a = angle(freq, p)
+            # the angle's error, sincospif's (a step of fp32) and the result's rounding
+            for got, want in ((-y[i, 0, j], math.sin(a)), (y[i, 0, 8 + j], math.cos(a))):
+                assert abs(float(got) - want) <= 2.0**-22 + 2.0**-24 + 2.0**-8 * abs(want), (freq, p)
