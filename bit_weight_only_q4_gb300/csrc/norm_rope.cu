@@ -194,23 +194,26 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 6) norm_rope_kernel(const NormR
                         unpack2(s2, s, t);
                         const float ss = nr_head_sum<LANES>(s + t);
                         r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-                        if (__any_sync(0xffffffffu, ss > 3.4e38f)) {
-                            // squares past fp32's range: a row 2^100 times smaller, beside which eps is nothing
-                            uint32_t small[4];
+                        const bool large = ss > 3.4e38f, tiny = ss < 0x1p-90f && a.eps < 0x1p-72f;
+                        if (__any_sync(0xffffffffu, large || tiny)) {
+                            // Squares past fp32's range: a row 2^100 times smaller, beside which eps is nothing; squares that
+                            // fp32 has no digits for (beside a larger eps they are nothing): a row 2^100 times larger.
+                            const float by = large ? 0x1p-100f : 0x1p100f;
+                            uint32_t other[4];
                             s2 = 0ull;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const f32x2 v = mul2(nr_widen(e[j]), pack2(0x1p-100f, 0x1p-100f));
-                                small[j] = nr_narrow(v);
+                                const f32x2 v = mul2(nr_widen(e[j]), pack2(by, by));
+                                other[j] = nr_narrow(v);
                                 s2 = fma2(v, v, s2);
                             }
                             unpack2(s2, s, t);
-                            const float ss_small = nr_head_sum<LANES>(s + t);
-                            if (ss > 3.4e38f) {
-                                r = rsqrtf(ss_small * (1.f / D));
+                            const float ss_other = nr_head_sum<LANES>(s + t);
+                            if (large || tiny) {
+                                r = rsqrtf(fmaf(ss_other, 1.f / D, large ? 0.f : a.eps * 0x1p100f * 0x1p100f));
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    e[j] = small[j];
+                                    e[j] = other[j];
                             }
                         }
                     }

@@ -1,11 +1,12 @@
 """Norms and rotation (q4_norm_rope) where a frequency, a position, a row or eps is at the end of its range."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 from bit_weight_only_q4_gb300 import q4
-from tests.test_gpu_norm_rope import check, made
+from tests.test_gpu_norm_rope import check, made, want
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,51 @@ def test_frequencies_above_one():
             # the angle's error, sincospif's (a step of fp32) and the result's rounding
             for got, want in ((-y[i, 0, j], math.sin(a)), (y[i, 0, 8 + j], math.cos(a))):
                 assert abs(float(got) - want) <= 2.0**-22 + 2.0**-24 + 2.0**-8 * abs(want), (freq, p)
+
+
+def check_small(got, x, w, positions, inv_freq, interleaved, eps):
+    """As check, and what fp32 loses below 2^-126: a value times its factor, and its partner's added, are each off by
+    half of the smallest step, 2^-150, however small they are, before the norm r = 1 / sqrt(mean(x^2) + eps)
+    multiplies them: 2^-149 r (without a norm r is 1)."""
+    ref, mag = want(x, w, positions, inv_freq, interleaved, eps)
+    z = x.double().cpu().numpy()
+    r = 1.0 if w is None else 1 / np.sqrt(np.mean(z * z, -1, keepdims=True) + eps)
+    assert (np.abs(got.double().cpu().numpy() - ref) <= 2.0**-8 * np.abs(ref) + 2.0**-19 * mag + 2.0**-149 * r + 1e-40).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1e-30, 2e-22, 2.2e-22, 1e-20, 1e-6])
+def test_rows_of_small_values_beside_every_eps(D, eps):
+    """Squares that fp32 has few or no digits for: results go by the formula with and without an eps of their size."""
+    low = 2.0**-133                                          # bf16's smallest
+    sizes = [low, 3 * low, 2.0**-126, 1e-36, 1e-30, 1e-25, 1e-23, 1e-22, 3e-21, 1e-20, 2.0**-49, 2.0**-48, 1e-14, 1e-10, 1.0]
+    x = made(len(sizes), 2, D, 5).float()
+    x = (x / x.abs().amax(-1, keepdim=True)).double() * torch.tensor(sizes, device="cuda").double().view(-1, 1, 1)
+    x = x.bfloat16()
+    assert (x.abs().amax((1, 2)) > 0).all()
+    w = (1 + 0.25 * torch.arange(D, device="cuda") / D).bfloat16()
+    f, pos = 10000.0 ** (-torch.arange(0, 16, device="cuda").float() / 16), torch.arange(len(sizes), device="cuda").int()
+    for interleaved in (False, True):
+        for k, p, fr in ((w, pos, f), (w, None, None)):
+            y, z = q4.q4_norm_rope(x, x, k, None, p, fr, eps=eps, interleaved=interleaved)
+            check_small(y, x, k, p, fr, interleaved, float(torch.tensor(eps).float()))
+            check_small(z, x, None, p, fr, interleaved, 0.0)
+
+
+def test_rows_of_every_size_without_an_eps():
+    D, top = 64, float(torch.finfo(torch.bfloat16).max)
+    x = made(6, 1, D)
+    x[0] = x[0].sign() * top
+    x[1] = x[1] * 1e-36
+    x[2] = x[2] * 1e30
+    x[3, 0, 1:] = 0                                          # a single value
+    x[3, 0, 0] = 1e25
+    x[4, 0, 1:] = 0
+    x[4, 0, 0] = 1e-39
+    w = (1 + 0.25 * torch.arange(D, device="cuda") / D).bfloat16()
+    a, _ = q4.q4_norm_rope(x, None, w, None, None, None, eps=0.0)
+    check(a, x, w, None, None, False, eps=0.0)
+    x[5] = 0                                                 # 0 / 0
+    a, _ = q4.q4_norm_rope(x, None, w, None, None, None, eps=0.0)
+    assert a[5].isnan().all()
+    check(a[:5], x[:5], w, None, None, False, eps=0.0)
