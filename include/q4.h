@@ -383,6 +383,7 @@ q4_status q4_kv_attention_shared(const void *q_bf16, int64_t q_stride, const uin
  *   q_out, k_out    the same; either in place (the input's pointer and stride) or apart from all inputs
  *   weights         bf16 [head_dim] or NULL
  *   positions       int32 [tokens], inv_freq fp32 [rotary_dim / 2]; unused with rotary_dim = 0
+ *   eps             0 .. 1e30
  * head_dim 64 or 128; rotary_dim a multiple of 16, at most head_dim; q_heads or kv_heads may be 0
  * (its pointers are not looked at then), at most 65536 each.  q, k, outputs and weights 16-byte, positions and
  * inv_freq 4-byte aligned.  With Q4_FLAG_PDL weights and inv_freq may be read before the previous kernel has finished.

@@ -124,3 +124,17 @@ def test_rows_of_every_size_without_an_eps():
     a, _ = q4.q4_norm_rope(x, None, w, None, None, None, eps=0.0)
     assert a[5].isnan().all()
     check(a[:5], x[:5], w, None, None, False, eps=0.0)
+
+
+@pytest.mark.parametrize("eps", [1e10, 1e30])
+def test_rows_beside_large_eps(eps):
+    """To the largest eps that is taken: rows whose squares overflow fp32 and rows that are nothing beside it."""
+    top = float(torch.finfo(torch.bfloat16).max)
+    sizes = [top, 1e20, 2e19, 1.9e18, 1e16, 1e15, 1e5, 1.0, 1e-10]
+    x = made(len(sizes), 2, 128, 6)
+    x = (x / x.abs().amax(-1, keepdim=True)).double() * torch.tensor(sizes, device="cuda").double().view(-1, 1, 1)
+    x = x.bfloat16()
+    w = (1 + 0.25 * torch.arange(128, device="cuda") / 128).bfloat16()
+    f, pos = 10000.0 ** (-torch.arange(0, 64, device="cuda").float() / 64), torch.arange(len(sizes), device="cuda").int()
+    y, _ = q4.q4_norm_rope(x, None, w, None, pos, f, eps=eps)
+    check(y, x, w, pos, f, False, eps=float(torch.tensor(eps).float()))

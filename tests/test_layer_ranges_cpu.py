@@ -1,0 +1,26 @@
+"""What the operators around a layer's projections take and refuse at the ends of their ranges, before any launch: 5 is a
+refused argument; 6 or 7, no device, that the checks were passed."""
+import pytest
+import torch
+
+from bit_weight_only_q4_gb300 import build as q4build
+from bit_weight_only_q4_gb300 import q4
+from tests.test_layer_refusals_cpu import FAKE, INF, lora, prompt, rope
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="calls that pass the checks would be launched")
+PASSED = (6, 7)
+APART = dict(q=FAKE, qo=FAKE, k=2 * FAKE, ko=2 * FAKE)       # q and k in place, each elsewhere
+
+
+@pytest.fixture(scope="module")
+def lib():
+    q4build.build()
+    return q4.load()
+
+
+@no_gpu
+def test_eps(lib):
+    for eps in (0.0, 1e-45, 1e-6, 1.0, 1e30):
+        assert rope(lib, eps=eps, **APART) in PASSED
+    for eps in (1.1e30, 1e37, 3e38, INF, -1e-45):
+        assert rope(lib, eps=eps, **APART) == 5
