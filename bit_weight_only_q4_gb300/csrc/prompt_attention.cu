@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
             tc_fence_after();
             float l0, l1;
             unpack2(add2(la, lb), l0, l1);
-            const float inv = l0 + l1 == 0.f ? 0.f : 1.f / (l0 + l1);
+            const float inv = 1.f / (l0 + l1);             // (a row of no score above -inf: 0 / 0)
             const bool gone = gone_all(), full = p.box_tokens > 0 && __all_sync(0xffffffffu, token >= 0);
             if (full) {
                 // All of the warp's rows are results: by way of its 4 KB of shared memory, 64 columns at a time, and from

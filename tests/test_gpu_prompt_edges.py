@@ -1,0 +1,39 @@
+"""Causal attention over packed prompts (q4_prompt_attention): scores, values and units at the ends of their ranges."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from bit_weight_only_q4_gb300 import q4
+from tests.test_gpu_prompt_attention import check, made, spans_of
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,H", [(2, 2), (8, 2), (6, 2)])
+@pytest.mark.parametrize("first", [1, 5, 63, 64, 130, 300])
+def test_rows_of_no_score_above_minus_infinity(first, Hq, H, D):
+    """The first keys of a sequence give -inf to all: rows that see no others are NaN, as their softmax is, and
+    what comes behind them is the attention over the keys that are left."""
+    q, k, v, offsets = made([70, 400, 333], Hq, H, D)
+    q, k = q.contiguous(), k.contiguous()
+    q[:, :, 3] = q[:, :, 3].abs() + 0.25
+    lo, hi = 70, 470
+    k[lo:lo + first, :, 3] = -INF
+    got = q4.q4_prompt_attention(q, k, v, offsets)
+    assert got[lo:lo + first].isnan().all()
+    check(got, q, k, v, [(0, 70), (lo + first, hi), (470, 803)])
+    # of one head of keys alone, and of a whole sequence
+    q, k, v, offsets = made([70, 400, 333], Hq, H, D)
+    q, k = q.contiguous(), k.contiguous()
+    q[:, :, 3] = q[:, :, 3].abs() + 0.25
+    k[:70, H - 1, 3] = -INF
+    got = q4.q4_prompt_attention(q, k, v, offsets)
+    G = Hq // H
+    assert got[:70, (H - 1) * G:].isnan().all()
+    k[:70, H - 1, 3] = 0
+    clean = q4.q4_prompt_attention(q, k, v, offsets)
+    assert torch.equal(got[:, :(H - 1) * G], clean[:, :(H - 1) * G])
+    check(got, q, k, v, spans_of(offsets)[1:])
