@@ -159,10 +159,11 @@ __global__ void __cluster_dims__(LR_CLUSTER, 1, 1) __launch_bounds__(LF_WARPS * 
 
 q4_status launch_lora_few(const LoraArgs &a, cudaStream_t st, bool pdl)
 {
-    // at most one part-filled tile a request
-    const int64_t tiles = (int64_t)a.tokens / LF_TOKENS + a.batch;
+    // at most one part-filled tile a request; where a request has no tokens that leaves a cluster behind the last tile,
+    // which goes through all offsets and notes those that are none
+    const int64_t tiles = (int64_t)a.tokens / LF_TOKENS + a.batch, most = (int64_t)a.tokens + 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((tiles < a.tokens ? tiles : a.tokens) * LR_CLUSTER));
+    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * LR_CLUSTER));
     cfg.blockDim = dim3(LF_WARPS * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -430,8 +430,8 @@ static q4_status lm_launch(const DeviceInfo &dev, const LoraArgs &a, cudaStream_
     // that has to wait for a place costs a second wave.  Measured, 79 tiles, 2048 -> 8192, rank 32: sizes 2 .. 8 take 76.6,
     // 62.7, 77.8, 74.5, 68.0, 75.2, 75.6 us (3: 237 CTAs of 304); 13 tiles, rank 64: 48, 36, 29, 26, 24, 22.7, 21.4 us.
     // With more tiles than that two: 248 tiles, rank 128, 199, 213, 205, 227, 227, 243, 241 us, and 282 without clusters.
-    int64_t tiles = (int64_t)a.tokens / LM_ROWS + a.batch;
-    tiles = tiles < a.tokens ? tiles : a.tokens;
+    // (A cluster behind the last tile, where a request has no tokens, goes through all offsets, as in lora_few.cu.)
+    const int64_t tiles = (int64_t)a.tokens / LM_ROWS + a.batch;
     int size = 2;
     while (size < LR_CLUSTER && tiles * (size + 1) <= 2 * (int64_t)dev.sms)
         ++size;

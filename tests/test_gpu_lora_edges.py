@@ -1,0 +1,40 @@
+"""Adapters of many requests (q4_lora): what each of its kernels reports, and its sums' width.
+
+FEW, SHARED and MANY are calls that go to the kernel of a request's few tokens, of requests that share adapters, and
+of many tokens: (tokens of each request, adapters).
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from bit_weight_only_q4_gb300 import q4
+from tests.test_gpu_lora import Case
+
+pytestmark = pytest.mark.gpu
+
+FEW, SHARED, MANY = ([1] * 64, 128), ([1] * 64, 8), ([40] * 64, 8)
+KERNELS = pytest.mark.parametrize("lens,adapters", [FEW, SHARED, MANY], ids=["few", "shared", "many"])
+
+
+def with_empty_requests(lens, adapters, empty):
+    """The requests and `empty` more, of no tokens, behind them."""
+    ids = [b % adapters for b in range(len(lens))]
+    return Case(lens + [0] * empty, ids + [0] * empty, 128, 256, 16, adapters=adapters)
+
+
+@KERNELS
+@pytest.mark.parametrize("at", [64, 70, 100, 127])
+@pytest.mark.parametrize("value", [3, -1, 1 << 20])
+def test_offsets_behind_the_last_token_are_looked_at(lens, adapters, at, value):
+    """Requests 64 .. 127 have no tokens; an offset among theirs that falls or lies outside is reported all the same."""
+    case = with_empty_requests(lens, adapters, 64)
+    q4.device_error_flags()
+    ref = case()
+    assert q4.device_error_flags() == 0
+    case.check(ref)
+    o = case.offsets.clone()
+    o[at + 1] = value
+    got = case(offsets=o)
+    assert q4.device_error_flags() == 4
+    assert torch.equal(got, ref)
