@@ -81,8 +81,14 @@ __device__ __forceinline__ bool lr_tile(const LoraArgs &p, int number, int span,
     const int lane = (int)(threadIdx.x & 31), id = lane < p.batch ? __ldg(p.ids + lane) : -1;
     SegmentWalk walk(Segments{p.offsets, p.batch, p.tokens, span, 1, p.err});
     SegmentUnit u;
-    if (!walk.find(number, u))
+    if (!walk.find(number, u)) {
+        // behind the last tile, where a request has no tokens: its id is looked at here
+        if (lr_rank_in_cluster() == 0 && threadIdx.x < 32 && p.err)
+            for (int b = lane; b < p.batch; b += 32)
+                if (__ldg(p.ids + b) >= p.adapters)
+                    atomicOr(p.err, kErrIndex);
         return false;
+    }
     const int first = u.unit * span;
     t.row = u.start + first;
     t.rows = u.len - first < span ? u.len - first : span;

@@ -38,3 +38,23 @@ def test_offsets_behind_the_last_token_are_looked_at(lens, adapters, at, value):
     got = case(offsets=o)
     assert q4.device_error_flags() == 4
     assert torch.equal(got, ref)
+
+
+@KERNELS
+@pytest.mark.parametrize("at", [0, 5, 40, 64, 100, 127])
+def test_ids_of_requests_without_tokens_are_looked_at(lens, adapters, at):
+    """An id past the adapters is reported whether its request has tokens or not, and whichever kernel runs."""
+    if at < 64:
+        lens = lens[:at] + [0] + lens[at + 1:]
+    case = with_empty_requests(lens, adapters, 64)
+    q4.device_error_flags()
+    ref = case()
+    assert q4.device_error_flags() == 0
+    case.check(ref)
+    ids = case.ids.clone()
+    ids[at] = adapters
+    got = case(ids=ids)
+    assert q4.device_error_flags() == 4
+    assert torch.equal(got, ref)
+    ids[at] = -7
+    assert torch.equal(case(ids=ids), ref) and q4.device_error_flags() == 0
