@@ -109,11 +109,13 @@ __device__ __forceinline__ void lr_copy(const LoraArgs &p, const LoraTile &t, ui
     if (p.out == p.base)
         return;
     const int c0 = lr_share(p.N / 8, rank, size), n = lr_share(p.N / 8, rank + 1, size) - c0;
-    for (int i = (int)threadIdx.x; i < t.rows * n; i += (int)blockDim.x) {
-        const int r = i / n, c = 8 * (c0 + i - r * n);
-        *reinterpret_cast<uint4 *>(p.out + (int64_t)(t.row + r) * p.out_stride + c) =
-            *reinterpret_cast<const uint4 *>(p.base + (int64_t)(t.row + r) * p.base_stride + c);
-    }
+    const int rows = n <= 1 << 23 ? t.rows : 1;              // at a time: their columns are counted in 32 bits
+    for (int r0 = 0; r0 < t.rows; r0 += rows)
+        for (int i = (int)threadIdx.x; i < rows * n; i += (int)blockDim.x) {
+            const int r = i / n, c = 8 * (c0 + i - r * n), row = t.row + r0 + r;
+            *reinterpret_cast<uint4 *>(p.out + (int64_t)row * p.out_stride + c) =
+                *reinterpret_cast<const uint4 *>(p.base + (int64_t)row * p.base_stride + c);
+        }
 }
 
 }  // namespace q4

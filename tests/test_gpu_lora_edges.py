@@ -58,3 +58,14 @@ def test_ids_of_requests_without_tokens_are_looked_at(lens, adapters, at):
     assert torch.equal(got, ref)
     ids[at] = -7
     assert torch.equal(case(ids=ids), ref) and q4.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("N", [8, 56, 64, 72, 1000, 2048, 23000])
+@pytest.mark.parametrize("lens", [[1] * 9, [3, 8, 0, 2] * 20, [300, 1, 0, 33, 128], [128] * 40], ids=["one", "few", "many", "tiles"])
+def test_requests_without_an_adapter(lens, N):
+    """base as it is, from shares of no columns to shares of more than a CTA has threads, and no row beside theirs."""
+    for adapters in (1, 200):
+        case = Case(lens, [-1] * len(lens), 64, N, 8, adapters=adapters, gap=3)
+        out = torch.full_like(case.base, 5.0)
+        case(out=out)
+        assert torch.equal(out[3:-3], case.base[3:-3]) and (out[:3] == 5).all() and (out[-3:] == 5).all()
