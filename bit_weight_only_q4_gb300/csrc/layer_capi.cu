@@ -110,6 +110,8 @@ q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, in
     return launch_prompt_attention(a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
+void q4_test_prompt_both_ends(int on) { prompt_set_both_ends(on != 0); }
+
 q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b, const float *scales, int adapters,
                   int rank, const int32_t *offsets, const int32_t *ids, int batch, const void *base,
                   int64_t base_stride, void *out, int64_t out_stride, int tokens, int N, int K, void *stream)

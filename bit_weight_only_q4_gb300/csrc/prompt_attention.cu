@@ -38,6 +38,8 @@
 #include "tc_device.cuh"
 #include "tma.h"
 
+#include <atomic>
+
 namespace q4 {
 
 constexpr int PA_ROWS = 128, PA_KEYS = 128;
@@ -169,6 +171,12 @@ __device__ __forceinline__ int pa_answer(uint32_t at)
     return r;
 }
 
+// The unit of CTA x of the grid: x, or, in tests, units from both ends in turn.
+__device__ __forceinline__ int pa_number(int x, const PromptArgs &p)
+{
+    return !p.both_ends ? x : (x & 1) ? (int)gridDim.x - 1 - (x >> 1) : x >> 1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     pdl_wait();
     PaWalk walk(p);
     PaUnit u;
-    if (!walk.find((int)blockIdx.x, u))
+    if (!walk.find(pa_number((int)blockIdx.x, p), u))
         return;                                            // (the whole CTA)
     if (warp == PA_COPY) {
         if (lane == 0) {
@@ -770,19 +778,20 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     } else if (warp == PA_NEXT) {
         // ------------------------------------------------- units to come
         // The grid has a CTA for each unit that there may be, and an SM room for one: a CTA takes over the units of those
-        // that have not begun, so that units of different lengths are dealt out as SMs come free.  The next unit is
-        // fetched before this one's V is looked through.
-        bool more = true, wanted = true;
-        int asked = 0;
+        // that have not begun, so that units of different lengths are dealt out as SMs come free.  CTAs without a unit
+        // are taken over too, and that is all: in whatever order CTAs are given up, the last answer is the one that there is
+        // none.  The next unit is fetched before this one's V is looked through.
+        bool more = true;
+        int asked = 0, told = 0;
         uint32_t at = 0u, uses = 0u;                       // copies before this unit, parities of v_raw
         PaUnit now = u;
 #pragma unroll 1
-        for (int round = 1; (more || now.na > 0) && !gone_all(); ++round) {
+        while ((more || now.na > 0) && !gone_all()) {
             u.na = 0;
             if (more) {
-                const int slot = (round - 1) % PA_QUEUE;
-                if (wanted && round > PA_QUEUE)
-                    kv_wait(unit_free + 8u * slot, (uint32_t)((round - 1) / PA_QUEUE - 1) & 1u, dead);
+                const int slot = told % PA_QUEUE;
+                if (told >= PA_QUEUE)
+                    kv_wait(unit_free + 8u * slot, (uint32_t)(told / PA_QUEUE - 1) & 1u, dead);
                 if (gone_all())
                     break;
                 if (elect_one())
@@ -793,18 +802,16 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 const int number = pa_answer(smem_u32(&s_answer));
                 fence_proxy_async();                       // (the next answer comes to the same place)
                 more = number >= 0;
-                if (wanted) {
-                    if (!more || !walk.find(number, u)) {
-                        // CTAs behind the last unit have nothing to do: they are taken over too, and that is all
-                        wanted = false;
-                        u.na = 0;
-                    }
+                if (!more || !walk.find(pa_number(number, p), u))
+                    u.na = 0;
+                if (!more || u.na > 0) {
                     if (lane == 0) {
                         const uint32_t to = smem_u32(&s_unit[slot]);
                         sts128(to, (uint32_t)u.start, (uint32_t)u.len, (uint32_t)u.first, (uint32_t)u.head);
                         sts128(to + 16u, (uint32_t)u.na, (uint32_t)u.nb, 0u, 0u);
                         mbar_arrive(unit_full + 8u * slot);
                     }
+                    ++told;
                 }
                 __syncwarp();
             }
@@ -884,11 +891,16 @@ static q4_status pa_launch(const PromptArgs &a, int64_t most_units, cudaStream_t
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of prompt_attention_kernel");
 }
 
+static std::atomic<bool> g_both_ends{false};
+
+void prompt_set_both_ends(bool on) { g_both_ends.store(on); }
+
 q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, bool pdl)
 {
     a.group = a.q_heads / a.kv_heads;
     a.tile_tokens = PA_ROWS / a.group;
     a.err = device_error_flags();
+    a.both_ends = g_both_ends.load() ? 1 : 0;
     a.box_tokens = 32 % a.group == 0 ? 32 / a.group : 0;
     // at most one part-filled pair of tiles a sequence
     const int64_t units = ((int64_t)a.tokens / (2 * a.tile_tokens) + a.batch) * a.kv_heads;

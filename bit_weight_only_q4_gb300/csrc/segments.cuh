@@ -52,10 +52,10 @@ struct SegmentWalk {
             ask(0);
         }
         while (number >= base + total) {
+            if (chunk >= s.batch - 32)             // (no more: the walk stays where it is)
+                return false;
             base += total;
             chunk += 32;
-            if (chunk >= s.batch)
-                return false;
             int lo = next_lo, hi = next_hi;
             if (chunk < s.batch - 32)
                 ask(chunk + 32);

@@ -201,6 +201,12 @@ q4_status q4_dequant_nvfp4_f32(const uint8_t *codes, const uint8_t *scale_e4m3,
 void q4_test_kv_give_up(int cta, int tiles);
 
 /*
+ * Test helper: in every later call of q4_prompt_attention the GPU's blocks are numbered from both ends of the list of
+ * work in turn, so that those without any lie between the others.  0 (the default): in the list's order.
+ */
+void q4_test_prompt_both_ends(int on);
+
+/*
  * INT8 weight-only linear ("Rumik TTS Fast Inference", "What Made It Faster": INT8
  * weight-only decode projections; the layout is not given there).  Reading, after
  * the int8 scheme "rumik-oss-1-int4" gives for its embedding: qweight int8 [N, K]

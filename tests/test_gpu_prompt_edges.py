@@ -37,3 +37,25 @@ def test_rows_of_no_score_above_minus_infinity(first, Hq, H, D):
     clean = q4.q4_prompt_attention(q, k, v, offsets)
     assert torch.equal(got[:, :(H - 1) * G], clean[:, :(H - 1) * G])
     check(got, q, k, v, spans_of(offsets)[1:])
+
+
+@pytest.mark.parametrize("Hq,H,D", [(8, 2, 128), (12, 12, 64), (2, 2, 128)])
+@pytest.mark.parametrize("batch", [1, 40, 400])
+def test_units_between_blocks_without_one(batch, Hq, H, D):
+    """Blocks that have not begun are taken over in an order of the GPU's own: those without work are passed over."""
+    gen = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 700 if batch < 100 else 300, (batch,), generator=gen).tolist()
+    lens[batch // 2] = 1300
+    q, k, v, offsets = made(lens, Hq, H, D)
+    want = q4.q4_prompt_attention(q, k, v, offsets)
+    out = torch.full_like(want, 7.0)
+    q4.load().q4_test_prompt_both_ends(1)
+    try:
+        for _ in range(3):
+            out.fill_(7.0)
+            q4.q4_prompt_attention(q, k, v, offsets, out=out)
+            assert torch.equal(out, want)
+    finally:
+        q4.load().q4_test_prompt_both_ends(0)
+    check(want, q, k, v, spans_of(offsets))
+    assert q4.device_error_flags() == 0
