@@ -44,8 +44,9 @@ q4_status q4_norm_rope(const void *q, int64_t q_stride, const void *q_weight, vo
         return fail(Q4_ERR_SHAPE, "strides must be multiples of 8, at least heads * head_dim");
     if ((q_heads > 0 && q == q_out && q_stride != q_out_stride) || (kv_heads > 0 && k == k_out && k_stride != k_out_stride))
         return fail(Q4_ERR_ARG, "in place, input and output have one stride");
-    if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(q_out, 16) || !aligned_to(k_out, 16) ||
-        !aligned_to(q_weight, 16) || !aligned_to(k_weight, 16) || !aligned_to(positions, 4) || !aligned_to(inv_freq, 4))
+    if ((q_heads > 0 && (!aligned_to(q, 16) || !aligned_to(q_out, 16) || !aligned_to(q_weight, 16))) ||
+        (kv_heads > 0 && (!aligned_to(k, 16) || !aligned_to(k_out, 16) || !aligned_to(k_weight, 16))) ||
+        (rotary_dim > 0 && (!aligned_to(positions, 4) || !aligned_to(inv_freq, 4))))
         return fail(Q4_ERR_ALIGN, "q, k, their outputs and weights must be 16-byte, positions and inv_freq 4-byte aligned");
     if (q_heads > 0 && kv_heads > 0 && (q_out == k_out || q_out == k || k_out == q))
         return fail(Q4_ERR_ARG, "q_out and k_out must be apart from each other and from the other's input");

@@ -24,3 +24,19 @@ def test_eps(lib):
         assert rope(lib, eps=eps, **APART) in PASSED
     for eps in (1.1e30, 1e37, 3e38, INF, -1e-45):
         assert rope(lib, eps=eps, **APART) == 5
+
+
+@no_gpu
+def test_pointers_of_no_heads_and_of_no_rotation_are_not_looked_at(lib):
+    for name in ("q", "qo", "qw"):
+        assert rope(lib, Hq=0, **dict(APART, **{name: FAKE + 2})) in PASSED
+        assert rope(lib, Hq=0, **dict(APART, **{name: None})) in PASSED
+        assert rope(lib, H=0, **dict(APART, **{name: FAKE + 2})) == 3
+    for name in ("k", "ko", "kw"):
+        assert rope(lib, H=0, **dict(APART, **{name: FAKE + 2})) in PASSED
+        assert rope(lib, H=0, **dict(APART, **{name: None})) in PASSED
+        assert rope(lib, Hq=0, **dict(APART, **{name: FAKE + 2})) == 3
+    for name in ("pos", "freq"):
+        assert rope(lib, rotary=0, **dict(APART, **{name: FAKE + 1})) in PASSED
+        assert rope(lib, rotary=0, **dict(APART, **{name: None})) in PASSED
+        assert rope(lib, **dict(APART, **{name: FAKE + 1})) == 3
