@@ -89,8 +89,9 @@ q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, in
     if (!row_stride_ok(q_stride, qr) || !row_stride_ok(k_stride, kr) || !row_stride_ok(v_stride, kr) || q_stride > most ||
         k_stride > most || v_stride > most)
         return fail(Q4_ERR_SHAPE, "strides must be multiples of 8, at least heads * head_dim and at most 2^38");
-    if (!(scale - scale == 0.f))
-        return fail(Q4_ERR_ARG, "scale must be finite");
+    // (exponents are of 2, so scale log2(e) has to be a number too)
+    if (!(scale >= -2e38f) || !(scale <= 2e38f))
+        return fail(Q4_ERR_ARG, "scale must be -2e38 .. 2e38");
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 16) || !aligned_to(offsets, 4))
         return fail(Q4_ERR_ALIGN, "q, k, v and out must be 16-byte, offsets 4-byte aligned");
     if (out == q || out == k || out == v)

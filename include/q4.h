@@ -413,7 +413,7 @@ q4_status q4_norm_rope(const void *q_bf16, int64_t q_stride, const void *q_weigh
  *             a sequence is left out, and such an offset counts as the nearest there is.
  *   out       bf16 [tokens, q_heads, head_dim], apart from the inputs
  * q_heads is a multiple of kv_heads, at most 128 times as many: query heads h * q_heads / kv_heads and on share the
- * keys of head h.  head_dim 64 or 128; q, k, v, out 16-byte, offsets 4-byte aligned.
+ * keys of head h.  head_dim 64 or 128; scale -2e38 .. 2e38; q, k, v, out 16-byte, offsets 4-byte aligned.
  * Scores, softmax statistics and sums are fp32; the probabilities meet V as bf16, so that a result's error
  * is at most 2^-8 of the weighted mean of |v|, and bf16's rounding (for values of V up to 2^100).  What a row does not see
  * has no part in its result, whatever it holds.  A row that sees no score above -inf is NaN, as its softmax is.  Uses

@@ -40,3 +40,12 @@ def test_pointers_of_no_heads_and_of_no_rotation_are_not_looked_at(lib):
         assert rope(lib, rotary=0, **dict(APART, **{name: FAKE + 1})) in PASSED
         assert rope(lib, rotary=0, **dict(APART, **{name: None})) in PASSED
         assert rope(lib, **dict(APART, **{name: FAKE + 1})) == 3
+
+
+@no_gpu
+def test_scales_whose_exponents_of_two_are_numbers(lib):
+    apart = dict(q=2 * FAKE, k=2 * FAKE, v=2 * FAKE)
+    for scale in (0.0, 1e-45, 1.0, 2e38, -2e38):
+        assert prompt(lib, scale=scale, **apart) in PASSED
+    for scale in (2.4e38, -2.4e38, 3.4e38, INF, float("nan")):
+        assert prompt(lib, scale=scale, **apart) == 5
