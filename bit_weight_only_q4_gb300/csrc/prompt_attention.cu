@@ -12,6 +12,7 @@
 // the mask, and the reference m_i that they give serves for the others.  m_i need not be the largest
 // s_ij: p keeps its relative precision at any size, and only when a tile's sum passes 2^20 is the
 // reference raised and what was summed scaled down.  So a tile that is seen whole costs one pass over its scores and no maximum.
+// (Of 2^31 tokens, 64 at least to a sum, the sums together stay below 2^45, and with |v| up to 2^80 in fp32's range.)
 //
 // One CTA per SM, 12 warps: four with the softmax of A (one thread a row), four with that of
 // B, one that copies (TMA), one or two that issue the MMAs, one that fetches units.  A step is one tile of

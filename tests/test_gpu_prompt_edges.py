@@ -59,3 +59,25 @@ def test_units_between_blocks_without_one(batch, Hq, H, D):
         q4.load().q4_test_prompt_both_ends(0)
     check(want, q, k, v, spans_of(offsets))
     assert q4.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values_behind_a_low_reference(D):
+    """The first reference is 13.9 below (of 2) all scores but its own 16: sums as large as they come, and V of 2^80."""
+    m = 33000
+    q, k = torch.zeros(m, 1, D, device="cuda"), torch.zeros(m, 1, D, device="cuda")
+    q[:, 0, 0] = 1
+    k[:, 0, 0] = 13.875
+    last = (m - 1) // 128 * 128
+    k[last:last + 16, 0, 0] = 0
+    gen = torch.Generator("cuda").manual_seed(1)
+    v = 2.0**80 * (0.5 + 0.5 * torch.rand(m, 1, D, device="cuda", generator=gen))
+    q, k, v = q.bfloat16(), k.bfloat16(), v.bfloat16()
+    offsets = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    got = q4.q4_prompt_attention(q, k, v, offsets, scale=0.6931471805599453)
+    # rows of the last tile see all keys before it and those up to their own
+    p = torch.exp2(k[:, 0, 0].double())
+    for r in (last + 20, last + 63, m - 1):
+        want = (p[:r + 1, None] * v[:r + 1, 0].double()).sum(0) / p[:r + 1].sum()
+        assert ((got[r, 0].double() - want).abs() <= 2 * 2.0**-8 * 1.01 * want).all()
+    assert got[last:].isfinite().all()
