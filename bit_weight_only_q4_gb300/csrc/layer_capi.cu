@@ -112,7 +112,7 @@ q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, in
     return launch_prompt_attention(a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
-void q4_test_prompt_both_ends(int on) { prompt_set_both_ends(on != 0); }
+void q4_test_prompt_swap(int blocks) { prompt_set_swap(blocks > 0 && blocks <= 65536 && (blocks & (blocks - 1)) == 0 ? blocks : 0); }
 
 q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b, const float *scales, int adapters,
                   int rank, const int32_t *offsets, const int32_t *ids, int batch, const void *base,

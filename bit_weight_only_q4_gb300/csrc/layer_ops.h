@@ -30,10 +30,10 @@ struct PromptArgs {
     int batch, tokens, q_heads, kv_heads;
     float scale_log2;                                          // scale * log2(e)
     int group, tile_tokens, box_tokens;                        // (by the launch) query heads per key head, tokens of a tile, of 32 rows
-    int both_ends;                                             // (tests) CTAs are given units from both ends of the list in turn
+    int swap;                                                  // (tests) so many CTAs change places with the next as many; 0: none
     unsigned *err;
 };
-void prompt_set_both_ends(bool on);
+void prompt_set_swap(int ctas);
 q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, bool pdl);
 
 // ---- lora_few.cu, lora_shared.cu, lora_many.cu

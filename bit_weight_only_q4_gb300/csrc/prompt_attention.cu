@@ -172,12 +172,6 @@ __device__ __forceinline__ int pa_answer(uint32_t at)
     return r;
 }
 
-// The unit of CTA x of the grid: x, or, in tests, units from both ends in turn.
-__device__ __forceinline__ int pa_number(int x, const PromptArgs &p)
-{
-    return !p.both_ends ? x : (x & 1) ? (int)gridDim.x - 1 - (x >> 1) : x >> 1;
-}
-
 template <int D>
 __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -212,7 +206,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
     pdl_wait();
     PaWalk walk(p);
     PaUnit u;
-    if (!walk.find(pa_number((int)blockIdx.x, p), u))
+    if (!walk.find((int)blockIdx.x ^ p.swap, u))
         return;                                            // (the whole CTA)
     if (warp == PA_COPY) {
         if (lane == 0) {
@@ -803,7 +797,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 1)
                 const int number = pa_answer(smem_u32(&s_answer));
                 fence_proxy_async();                       // (the next answer comes to the same place)
                 more = number >= 0;
-                if (!more || !walk.find(pa_number(number, p), u))
+                if (!more || !walk.find(number ^ p.swap, u))
                     u.na = 0;
                 if (!more || u.na > 0) {
                     if (lane == 0) {
@@ -892,19 +886,21 @@ static q4_status pa_launch(const PromptArgs &a, int64_t most_units, cudaStream_t
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "launch of prompt_attention_kernel");
 }
 
-static std::atomic<bool> g_both_ends{false};
+static std::atomic<int> g_swap{0};
 
-void prompt_set_both_ends(bool on) { g_both_ends.store(on); }
+void prompt_set_swap(int ctas) { g_swap.store(ctas); }
 
 q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, bool pdl)
 {
     a.group = a.q_heads / a.kv_heads;
     a.tile_tokens = PA_ROWS / a.group;
     a.err = device_error_flags();
-    a.both_ends = g_both_ends.load() ? 1 : 0;
+    a.swap = g_swap.load();
     a.box_tokens = 32 % a.group == 0 ? 32 / a.group : 0;
     // at most one part-filled pair of tiles a sequence
-    const int64_t units = ((int64_t)a.tokens / (2 * a.tile_tokens) + a.batch) * a.kv_heads;
+    int64_t units = ((int64_t)a.tokens / (2 * a.tile_tokens) + a.batch) * a.kv_heads;
+    if (a.swap)
+        units = (units + 2 * a.swap - 1) / (2 * a.swap) * (2 * a.swap);
     return head_dim == 64 ? pa_launch<64>(a, units, st, pdl) : pa_launch<128>(a, units, st, pdl);
 }
 

@@ -201,10 +201,10 @@ q4_status q4_dequant_nvfp4_f32(const uint8_t *codes, const uint8_t *scale_e4m3,
 void q4_test_kv_give_up(int cta, int tiles);
 
 /*
- * Test helper: in every later call of q4_prompt_attention the GPU's blocks are numbered from both ends of the list of
- * work in turn, so that those without any lie between the others.  0 (the default): in the list's order.
+ * Test helper: in every later call of q4_prompt_attention so many of the GPU's blocks (a power of two up to 65536) change
+ * places with the next as many, so that some without work come before others that have some.  0 (the default): none do.
  */
-void q4_test_prompt_both_ends(int on);
+void q4_test_prompt_swap(int blocks);
 
 /*
  * INT8 weight-only linear ("Rumik TTS Fast Inference", "What Made It Faster": INT8

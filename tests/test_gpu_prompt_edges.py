@@ -40,23 +40,24 @@ def test_rows_of_no_score_above_minus_infinity(first, Hq, H, D):
 
 
 @pytest.mark.parametrize("Hq,H,D", [(8, 2, 128), (12, 12, 64), (2, 2, 128)])
-@pytest.mark.parametrize("batch", [1, 40, 400])
-def test_units_between_blocks_without_one(batch, Hq, H, D):
-    """Blocks that have not begun are taken over in an order of the GPU's own: those without work are passed over."""
-    gen = torch.Generator().manual_seed(batch)
-    lens = torch.randint(0, 700 if batch < 100 else 300, (batch,), generator=gen).tolist()
-    lens[batch // 2] = 1300
+@pytest.mark.parametrize("swap,units", [(256, 600), (256, 768), (512, 1100), (16, 2000), (1, 300), (4096, 700)])
+def test_units_behind_blocks_without_one(swap, units, Hq, H, D):
+    """Blocks that have not begun are taken over in an order of the GPU's own: those without work are passed over.  Here
+    they come in front of the last `units` % (2 swap) units, up to a swap's length, with every SM busy."""
+    gen = torch.Generator().manual_seed(units)
+    per = 256 * H // Hq                                      # tokens of a unit
+    lens = torch.randint(1, per + 1, (units // H,), generator=gen).tolist()
     q, k, v, offsets = made(lens, Hq, H, D)
     want = q4.q4_prompt_attention(q, k, v, offsets)
     out = torch.full_like(want, 7.0)
-    q4.load().q4_test_prompt_both_ends(1)
+    q4.load().q4_test_prompt_swap(swap)
     try:
         for _ in range(3):
             out.fill_(7.0)
             q4.q4_prompt_attention(q, k, v, offsets, out=out)
             assert torch.equal(out, want)
     finally:
-        q4.load().q4_test_prompt_both_ends(0)
+        q4.load().q4_test_prompt_swap(0)
     check(want, q, k, v, spans_of(offsets))
     assert q4.device_error_flags() == 0
 
