@@ -164,6 +164,8 @@ q4_status launch_kv_attention(const DeviceInfo &dev, const KvCacheDesc &c, const
     p.all_rows = (int)(plans[0].rows * a.batch);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.err = device_error_flags();
+    if (!p.err)                                            // (a wait that runs out writes there)
+        return fail(Q4_ERR_CUDA, "the device error word was not found");
     p.give_up = g_give_up.load();
     p.give_up_tiles = g_give_up_tiles.load();
     p.tickets = reinterpret_cast<unsigned *>(ws);

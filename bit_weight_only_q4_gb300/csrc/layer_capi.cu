@@ -154,6 +154,8 @@ q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b,
     p.offsets = offsets, p.ids = ids;
     p.batch = batch, p.tokens = tokens, p.adapters = adapters, p.rank = rank, p.N = N, p.K = K;
     p.err = device_error_flags();
+    if (!p.err)                                            // (a wait that runs out writes there)
+        return fail(Q4_ERR_CUDA, "the device error word was not found");
     // Which kernel, for the lengths are on the device: the one of eight-token tiles where requests have
     // eight tokens in the mean, or where its CTAs are all on the GPU at once and what their tiles read of the
     // adapters, each anew, stays below 32 MB.  Measured (eight-token tiles, 128-token tiles): 64 requests of 5, rank 64, 14.9

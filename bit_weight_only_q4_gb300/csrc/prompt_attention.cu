@@ -895,6 +895,8 @@ q4_status launch_prompt_attention(PromptArgs a, int head_dim, cudaStream_t st, b
     a.group = a.q_heads / a.kv_heads;
     a.tile_tokens = PA_ROWS / a.group;
     a.err = device_error_flags();
+    if (!a.err)                                            // (a wait that runs out writes there)
+        return fail(Q4_ERR_CUDA, "the device error word was not found");
     a.swap = g_swap.load();
     a.box_tokens = 32 % a.group == 0 ? 32 / a.group : 0;
     // at most one part-filled pair of tiles a sequence
