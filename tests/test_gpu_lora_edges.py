@@ -69,3 +69,27 @@ def test_requests_without_an_adapter(lens, N):
         out = torch.full_like(case.base, 5.0)
         case(out=out)
         assert torch.equal(out[3:-3], case.base[3:-3]) and (out[:3] == 5).all() and (out[-3:] == 5).all()
+
+
+@pytest.mark.parametrize("rank", [8, 16, 40, 64, 72, 128])
+@pytest.mark.parametrize("K", [64, 136])
+@pytest.mark.parametrize("lens,adapters", [FEW, SHARED, ([3, 8, 0, 1, 5] * 9, 45), ([3, 8, 0, 1, 5] * 9, 3)],
+                         ids=["few", "shared", "few drafts", "shared drafts"])
+def test_sums_between_the_products_of_few_tokens_have_twice_the_digits(lens, adapters, K, rank):
+    """t = x A^T meets B as two bf16 values, each off by 2^-8 of what it stands for: 2^-16 of t is left.  Beside it
+    there are fp32's steps, 2^-23 each (the tensor cores cut), for K + 2 rank products and 32 sums of parts, and the result's
+    rounding.  With base 0, t as one bf16 value would be outside that."""
+    case = Case(lens, [b % adapters for b in range(len(lens))], K, 1024, rank, adapters=adapters)
+    case.base.zero_()
+    got = case()
+    beyond = 0
+    for lo, hi, i in zip(case.at, case.at[1:], case.id_list):
+        x, a, b, s = case.x[lo:hi].double(), case.a[i].double(), case.b[i].double(), case.scales[i].double()
+        t = x @ a.T
+        want = s * (t @ b.T)
+        sums = s * ((x.abs() @ a.abs().T) @ b.abs().T)
+        tol = 1.01 * (2.0**-8 * want.abs() + 2.0**-16 * s * (t.abs() @ b.abs().T) + 2.0**-23 * (K + 2 * rank + 32) * sums)
+        assert ((got[lo:hi].double() - want).abs() <= tol).all()
+        once = (s * (t.bfloat16().double() @ b.T)).bfloat16().double()
+        beyond += int(((once - want).abs() > tol).sum())
+    assert beyond > 0
