@@ -29,7 +29,9 @@ class CachedAttention:
 
     turn: norms and rotation of q and k, as q4_norm_rope takes them: (q_weight, k_weight, inv_freq),
     weights None for no norm.  adapters: (of qkv, of out), each (a, b, scales) as q4_lora takes them, or
-    None; calls then name their requests as (offsets, ids), and one that names none has the projections alone."""
+    None; calls then name their requests as (offsets, ids), and one that names none has the projections alone.  An
+    adapter of qkv is one for all of its rows: those of q, k and v apart are stacked, A's rows one below the
+    other and B's columns side by side with zeros in the others' rows, up to a rank of 128 together."""
 
     def __init__(self, qkv, out, q_heads: int, cache: torch.Tensor, fmt: int, head_dim: int, turn=None, adapters=None,
                  eps=1e-6, interleaved=False):

@@ -112,7 +112,10 @@ q4_status q4_prompt_attention(const void *q, int64_t q_stride, const void *k, in
     return launch_prompt_attention(a, head_dim, static_cast<cudaStream_t>(stream), pdl_on());
 }
 
-void q4_test_prompt_swap(int blocks) { prompt_set_swap(blocks > 0 && blocks <= 65536 && (blocks & (blocks - 1)) == 0 ? blocks : 0); }
+void q4_test_prompt_swap(int blocks)
+{
+    prompt_set_swap(blocks > 0 && blocks <= 65536 && (blocks & (blocks - 1)) == 0 ? blocks : 0);
+}
 
 q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b, const float *scales, int adapters,
                   int rank, const int32_t *offsets, const int32_t *ids, int batch, const void *base,
@@ -160,7 +163,10 @@ q4_status q4_lora(const void *x, int64_t x_stride, const void *a, const void *b,
     // eight tokens in the mean, or where its CTAs are all on the GPU at once and what their tiles read of the
     // adapters, each anew, stays below 32 MB.  Measured (eight-token tiles, 128-token tiles): 64 requests of 5, rank 64, 14.9
     // against 28 us; 16 of 32, rank 16, 6.4 against 10.8; 16 of 64, rank 64, 18.6 against 12.2; 60 of 50, rank 16, 33
-    // against 18.
+    // against 18.  One kernel has the whole call, also one of single tokens and prompts, where the mean says little:
+    // 63 single tokens with an adapter each and a prompt of 400 or of 500 (which goes to the other kernel), K = N = 2048,
+    // rank 16, take 10.7 and 15.0 us, the tokens alone 6.4 and the prompts alone 5.6 and 6.4; rank 64 19.5 and 16.5, alone
+    // 11.0, 9.9 and 11.3.
     const int64_t tiles = tokens / 8 + batch / 2;
     const bool few = tokens <= 8 * (int64_t)batch ||
                      (tiles <= dev.sms / 2 && tiles * 2 * rank * ((int64_t)N + K) <= 32 << 20);

@@ -9,7 +9,9 @@
 //
 // What bounds it: the chain of offsets, x and A, the exchange, B (48 single tokens, rank 16: 5.4 us), and where tiles
 // share adapters, L2, from which each tile reads its own.  t as two values costs 1 to 4% (64 requests of 5 with an adapter each, rank
-// 64: 18.9 -> 19.6 us) and leaves bf16's rounding of the result as the only one that counts.
+// 64: 18.9 -> 19.6 us) and leaves bf16's rounding of the result as the only one that counts.  Each cluster adds up the lengths
+// in front of its tile, so that many requests cost more than their number: single tokens, rank 16, 2048 -> 2048, of 64, 256,
+// 512, 1,024 and 4,096 requests take 6.1, 25.5, 62, 180 and 2,132 us.
 #include "lora.cuh"
 
 namespace q4 {

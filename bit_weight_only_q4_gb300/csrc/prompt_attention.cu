@@ -29,11 +29,12 @@
 // is multiplied by the softmax threads themselves, over the tokens that a row sees.
 //
 // What bounds it.  Heads of 128, 32 on 8: the tensor cores, whose pipe is busy for 76% of the SMs' time: 7 prompts of 333
-// to 8,191 tokens 1,040 us, 1,750 TFLOP/s of what the mask leaves (89% of a large library product's rate); one of 32,768
-// 5,050 us, 1,740 TFLOP/s under the power limit.  The rest is tiles that the mask cuts, and a unit's beginning and end, some
-// 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 177 us, 895 TFLOP/s.
+// to 8,191 tokens 1,050 us, 1,735 TFLOP/s of what the mask leaves (89% of a large library product's rate); one of 32,768
+// 5,000 to 5,300 us, 1,660 to 1,760 TFLOP/s, as the power limit has it.  The rest is tiles that the mask cuts, and a unit's
+// beginning and end, some 7,000 cycles, which rule for short prompts: 48 of 37 to 1,501 tokens, 16 heads, 177 us, 895 TFLOP/s.
 // Heads of 64: half the products for as many exponentials, so 2^x (4 cycles a warp and scheduler) and what is about it: 3
-// prompts of 5,000 to 16,383 tokens, 28 on 4 heads, 1,210 us, 1,250 TFLOP/s.  5 of at most 77 tokens: 6 us, latency.
+// prompts of 5,000 to 16,383 tokens, 28 on 4 heads, 1,240 us, 1,220 TFLOP/s.  5 of at most 77 tokens: 6.5 us, latency.
+// All of these are calls in a captured graph.
 #include "layer_ops.h"
 #include "segments.cuh"
 #include "tc_device.cuh"

@@ -155,7 +155,8 @@ def get_launch_flags() -> int:
 
 def device_error_flags(clear: bool = True) -> int:
     """Device error word (bit 0: a bounded in-kernel wait timed out; bit 2: an
-    embedding id, a cache slot or a page id out of range). Synchronises."""
+    embedding id, a cache slot, a page id, an offset or an adapter's id out of range).
+    Synchronises."""
     v = ctypes.c_uint(0)
     _check(load().q4_device_error_flags(ctypes.byref(v), 1 if clear else 0))
     return int(v.value)

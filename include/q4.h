@@ -178,7 +178,8 @@ q4_status audio_head_logits_restricted(const void *h, const void *head, int R_to
  */
 #define Q4_DEVERR_TIMEOUT 0x1u
 /* Bit 2: q4_embedding_int8 met a token id outside 0 .. V-1 and wrote a row of
- * zeros for it, or a key/value cache call met a slot or a page id outside the cache. */
+ * zeros for it, a key/value cache call met a slot or a page id outside the cache, or a call over packed requests met
+ * offsets that fall or lie outside its rows or an id past its adapters. */
 #define Q4_DEVERR_INDEX 0x4u
 q4_status q4_device_error_flags(unsigned *flags, int clear);
 
@@ -442,7 +443,8 @@ q4_status q4_prompt_attention(const void *q_bf16, int64_t q_stride, const void *
  * N and K multiples of 8, rank a multiple of 8 from 8 to 128, strides multiples of 8; x, a, b, base and out
  * 16-byte, scales, offsets and ids 4-byte aligned; at most 2^27 - 1 tokens and requests.  Products are bf16 with
  * fp32 sums; x A^T is rounded to bf16 between them (in calls of a few tokens a request to twice its digits), the result once
- * more.  Uses no workspace.
+ * more.  Which of the two, and the order of the sums, goes by the whole call's sizes: the same request's last bits may
+ * differ beside other requests; the same call's do not.  Uses no workspace.
  */
 q4_status q4_lora(const void *x_bf16, int64_t x_stride, const void *a_bf16, const void *b_bf16, const float *scales,
                   int adapters, int rank, const int32_t *offsets, const int32_t *ids, int batch,
