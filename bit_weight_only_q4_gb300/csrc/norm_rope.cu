@@ -196,10 +196,11 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 6) norm_rope_kernel(const NormR
                         unpack2(s2, s, t);
                         const float ss = nr_head_sum<LANES>(s + t);
                         r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-                        const bool large = ss > 3.4e38f, tiny = ss < 0x1p-90f && a.eps < 0x1p-72f;
+                        const bool large = ss > 3.4e38f, tiny = ss < 0x1p-90f && a.eps < 0x1p-73f;
                         if (__any_sync(0xffffffffu, large || tiny)) {
                             // Squares past fp32's range: a row 2^100 times smaller, beside which eps is nothing; squares that
-                            // fp32 has no digits for (beside a larger eps they are nothing): a row 2^100 times larger.
+                            // fp32 has no digits for (beside an eps of 2^-73 they are nothing): a row 2^100 times larger, and
+                            // eps 2^200 times, which is below 2^127.
                             const float by = large ? 0x1p-100f : 0x1p100f;
                             uint32_t other[4];
                             s2 = 0ull;

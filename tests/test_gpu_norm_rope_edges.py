@@ -138,3 +138,16 @@ def test_rows_beside_large_eps(eps):
     f, pos = 10000.0 ** (-torch.arange(0, 64, device="cuda").float() / 64), torch.arange(len(sizes), device="cuda").int()
     y, _ = q4.q4_norm_rope(x, None, w, None, pos, f, eps=eps)
     check(y, x, w, pos, f, False, eps=float(torch.tensor(eps).float()))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_eps_where_rows_cease_to_be_made_larger(D):
+    """2^-72 and 2^-73 and the values next to them, beside sums of squares around 2^-90."""
+    sizes = [2.0**-48 * f for f in (0.25, 0.5, 0.68, 0.7, 0.71, 0.98, 0.99, 1.0, 1.01, 1.4)]
+    x = made(len(sizes), 2, D, 7).sign().float() * torch.tensor(sizes, device="cuda").view(-1, 1, 1)
+    x = x.bfloat16()
+    w = (1 + 0.25 * torch.arange(D, device="cuda") / D).bfloat16()
+    for top in (2.0**-72, 2.0**-73):
+        for eps in (top * (1 - 2.0**-24), top, top * (1 + 2.0**-23)):
+            y, _ = q4.q4_norm_rope(x, None, w, None, None, None, eps=eps)
+            check(y, x, w, None, None, False, eps=eps)
