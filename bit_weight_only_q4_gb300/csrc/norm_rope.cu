@@ -198,25 +198,26 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 6) norm_rope_kernel(const NormR
                         r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
                         const bool large = ss > 3.4e38f, tiny = ss < 0x1p-90f && a.eps < 0x1p-73f;
                         if (__any_sync(0xffffffffu, large || tiny)) {
-                            // Squares past fp32's range: a row 2^100 times smaller, beside which eps is nothing; squares that
+                            // Squares past fp32's range: their sum from a row 2^100 times smaller, beside which eps is nothing, and
+                            // the row 2^34 times smaller, for its products and for bf16's digits of its smaller values; squares that
                             // fp32 has no digits for (beside an eps of 2^-73 they are nothing): a row 2^100 times larger, and
                             // eps 2^200 times, which is below 2^127.
                             const float by = large ? 0x1p-100f : 0x1p100f;
-                            uint32_t other[4];
                             s2 = 0ull;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const f32x2 v = mul2(nr_widen(e[j]), pack2(by, by));
-                                other[j] = nr_narrow(v);
                                 s2 = fma2(v, v, s2);
                             }
                             unpack2(s2, s, t);
                             const float ss_other = nr_head_sum<LANES>(s + t);
                             if (large || tiny) {
-                                r = rsqrtf(fmaf(ss_other, 1.f / D, large ? 0.f : a.eps * 0x1p100f * 0x1p100f));
+                                const float keep = large ? 0x1p-34f : 0x1p100f;
+                                r = rsqrtf(fmaf(ss_other, 1.f / D, large ? 0.f : a.eps * 0x1p100f * 0x1p100f)) *
+                                    (large ? 0x1p-66f : 1.f);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    e[j] = other[j];
+                                    e[j] = nr_narrow(mul2(nr_widen(e[j]), pack2(keep, keep)));
                             }
                         }
                     }

@@ -151,3 +151,20 @@ def test_an_eps_where_rows_cease_to_be_made_larger(D):
         for eps in (top * (1 - 2.0**-24), top, top * (1 + 2.0**-23)):
             y, _ = q4.q4_norm_rope(x, None, w, None, None, None, eps=eps)
             check(y, x, w, None, None, False, eps=eps)
+
+
+@pytest.mark.parametrize("top", [2e19, 1e20, 1e30, 3.38e38])
+def test_small_values_beside_those_whose_squares_overflow(top):
+    """One pair of a row so large that its squares leave fp32's range: the others' results are bf16 numbers still, from
+    normal ones down to none."""
+    D, n = 128, 40
+    x = made(n, 2, D, 8).float()
+    x = x / x.abs().amax(-1, keepdim=True) * 2.0 ** -torch.arange(0, 2 * n, 2, device="cuda").view(-1, 1, 1)
+    x[:, :, 7] = top
+    x[:, :, 64 + 7] = -0.7 * top
+    x = x.bfloat16()
+    w = (1 + 0.25 * torch.arange(D, device="cuda") / D).bfloat16()
+    f, pos = 10000.0 ** (-torch.arange(0, 64, device="cuda").float() / 64), torch.arange(n, device="cuda").int()
+    for p, fr in ((pos, f), (None, None)):
+        y, _ = q4.q4_norm_rope(x, None, w, None, p, fr, eps=1e-6)
+        check_small(y, x, w, p, fr, False, 1e-6)
