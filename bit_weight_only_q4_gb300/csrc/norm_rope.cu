@@ -19,9 +19,9 @@
 //     y_j = r (x_j (w_j cos_j) + x_p (+-w_p sin_j)),    p the partner,
 // and the bracket's factors are worked out once for a token's queries and once for its keys.
 //
-// What bounds it: HBM, 4 bytes a value (65,000 tokens, 32 and 8 heads of 128: 235 us, 5.7 TB/s), with
+// What bounds it: HBM, 4 bytes a value (65,000 tokens, 32 and 8 heads of 128: 236 us, 5.6 TB/s), with
 // instruction issue close behind (some 130 for 512 bytes).  A few thousand tokens: no one thing (9,446 tokens, 36 heads of 64:
-// 20.6 us against 12.9 of HBM).  The SMs are at work for three quarters of the launch; while they are they issue in 68% of
+// 20.9 us against 12.9 of HBM).  The SMs are at work for three quarters of the launch; while they are they issue in 68% of
 // their cycles, and the rest is the chain that each token begins with, of position, sincospif, factors and
 // first loads, which nine passes are too few to hide.  A step: its launch and that chain (48 tokens, 3.0 us).
 #include "layer_ops.h"
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 6) norm_rope_kernel(const NormR
 q4_status launch_norm_rope(const DeviceInfo &dev, NormRopeArgs a, int head_dim, cudaStream_t st, bool pdl)
 {
     // A warp takes all heads of a token, or, where that would leave SMs without work, as many as
-    // one batch of loads brings.  Measured: 9,446 tokens of 36 heads of 64, whole 20.6, in batches 29.4 us (the angles are
+    // one batch of loads brings.  Measured: 9,446 tokens of 36 heads of 64, whole 20.9, in batches 29.4 us (the angles are
     // worked out for each); 48 tokens of 32 heads of 128 in CTAs of 4 warps 3.3, of 8 warps 4.2 us (with turns from fp64;
     // from integers 3.0).
     const int heads = a.q_heads + a.kv_heads, batch = NR_BATCH * (256 / head_dim);

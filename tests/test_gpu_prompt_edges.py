@@ -39,6 +39,33 @@ def test_rows_of_no_score_above_minus_infinity(first, Hq, H, D):
     check(got, q, k, v, spans_of(offsets)[1:])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,H", [(2, 2), (8, 2), (6, 2)])
+def test_keys_of_no_weight_anywhere(Hq, H, D):
+    """Keys of -inf by ones, in runs from 16 to whole tiles and at tiles' beginnings, where references are taken."""
+    m = 900
+    q, k, v, offsets = made([m], Hq, H, D)
+    q, k = q.contiguous(), k.contiguous()
+    q[:, :, 3] = q[:, :, 3].abs() + 0.25
+    gen = torch.Generator().manual_seed(9)
+    gone = torch.rand(m, generator=gen) < 0.1
+    for lo, hi in ((128, 144), (192, 208), (256, 320), (384, 512), (512, 530), (640, 900)):
+        gone[lo:hi] = True
+    gone[0] = False
+    k[gone.cuda(), :, 3] = 0
+    scale = D**-0.5
+    kk, vv = (t.double().repeat_interleave(Hq // H, 1).transpose(0, 1) for t in (k, v))
+    s = q.double().transpose(0, 1) @ kk.transpose(1, 2) * scale
+    unseen = torch.ones(m, m, dtype=torch.bool, device="cuda").triu(1) | gone.cuda()
+    p = s.masked_fill(unseen, -INF).softmax(-1)
+    # (the error allowed for goes by the mean of |v| with these probabilities)
+    o, mag = (p @ vv).transpose(0, 1), (p @ vv.abs()).transpose(0, 1)
+    d = 2 * D * 2.0**-24 * scale * q.double().norm(dim=-1, keepdim=True) * k.double().norm(dim=-1).max()
+    k[gone.cuda(), :, 3] = -INF
+    got = q4.q4_prompt_attention(q, k, v, offsets).double()
+    assert ((got - o).abs() <= 2.0**-8 * o.abs() + (2.0**-8 + 2 * d) * mag * 1.01 + 1e-30).all()
+
+
 @pytest.mark.parametrize("Hq,H,D", [(8, 2, 128), (12, 12, 64), (2, 2, 128)])
 @pytest.mark.parametrize("swap,units", [(256, 600), (256, 768), (512, 1100), (16, 2000), (1, 300), (4096, 700)])
 def test_units_behind_blocks_without_one(swap, units, Hq, H, D):
