@@ -32,7 +32,7 @@ namespace q4 {
 constexpr int NR_WARPS = 4;
 constexpr int NR_BATCH = 2;                // passes over the warp whose loads are in flight together
 
-// u of frequency f (see above): f = m 2^(23 - s) and 2^66 / 2 pi, rounded to 64 bits, have an 88-bit product.
+// u of frequency f (see above) = m 2^(e - 150): 2^64 u = m c 2^(e - 152) with c = 2^66 / 2 pi, rounded to 64 bits; m c has 88.
 __device__ __forceinline__ uint64_t nr_turn(float f)
 {
     const uint32_t bits = __float_as_uint(f), e = bits >> 23 & 0xffu;

@@ -416,10 +416,9 @@ q4_status q4_norm_rope(const void *q_bf16, int64_t q_stride, const void *q_weigh
  * q_heads is a multiple of kv_heads, at most 128 times as many: query heads h * q_heads / kv_heads and on share the
  * keys of head h.  head_dim 64 or 128; scale -2e38 .. 2e38; q, k, v, out 16-byte, offsets 4-byte aligned.
  * Scores, softmax statistics and sums are fp32; the probabilities meet V as bf16, so that a result's error
- * is at most 2^-8 of the weighted mean of |v|, and bf16's rounding (for values of V up to 2^80, whatever the length: before the
- * division sums of p v may be 2^45 times as large).  What a row does not see
- * has no part in its result, whatever it holds.  A row that sees no score above -inf is NaN, as its softmax is.  Uses
- * no workspace.
+ * is at most 2^-8 of the weighted mean of |v|, and bf16's rounding (for values of V up to 2^80, whatever the length: before
+ * the division sums of p v may be 2^45 times as large).  What a row does not see has no part in its result, whatever it
+ * holds.  A row that sees no score above -inf is NaN, as its softmax is.  Uses no workspace.
  */
 q4_status q4_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf16, int64_t k_stride,
                               const void *v_bf16, int64_t v_stride, const int32_t *offsets, int batch,
